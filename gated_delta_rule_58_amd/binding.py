@@ -107,7 +107,10 @@ def exported_symbols():
             "kda_chunk_prefill_workspace_bytes", "kda_recurrent_decode",
             "kda_recurrent_decode_gated", "kda_shortconv_l2norm", "kda_chunk_prefill_backward",
             "kda_chunk_prefill_backward_workspace_bytes", "kda_gate_backward",
-            "kda_gate_backward_workspace_bytes"]
+            "kda_gate_backward_workspace_bytes", "kda_linattn_chunk_prefill",
+            "kda_linattn_chunk_prefill_workspace_bytes", "kda_linattn_chunk_prefill_backward",
+            "kda_linattn_chunk_prefill_backward_workspace_bytes", "kda_linattn_recurrent_decode",
+            "kda_layernorm", "kda_layernorm_backward", "kda_layernorm_backward_workspace_bytes"]
 
 
 def _check(status: int):

@@ -10,7 +10,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkda.so")
 SOURCES = ["api.hip", "debug.hip", "gate.hip", "decode.hip", "decode_gated.hip", "prefill.hip", "prep.hip",
-           "state.hip", "shortconv.hip", "backward.hip"]
+           "state.hip", "shortconv.hip", "backward.hip", "linattn_api.hip", "linattn_walk.hip",
+           "linattn_decode.hip", "layernorm.hip"]
 ARCH = os.environ.get("KDA_OFFLOAD_ARCH", "gfx950")
 
 

@@ -8,11 +8,15 @@
 #include <stdio.h>
 #include <string.h>
 
+#include "api_common.hpp"
 #include "kda_internal.hpp"
 
 namespace {
-
 thread_local char g_err[512] = "";
+}  // namespace
+
+namespace kda {
+namespace api {
 
 kda_status fail(kda_status st, const char* fmt, ...) {
   va_list ap;
@@ -27,9 +31,16 @@ kda_status ok() {
   return KDA_OK;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace api
+}  // namespace kda
 
-bool known_dtype(kda_dtype d) { return d == KDA_F32 || d == KDA_BF16; }
+namespace {
+
+using kda::api::aligned;
+using kda::api::fail;
+using kda::api::known_dtype;
+using kda::api::ok;
+using kda::api::run_checked;
 
 // A_log is one value per head ([H]) or, given explicitly, one per (head,
 // channel) ([H, d]); any other length, the checkpoint's [128] among them, is
@@ -41,44 +52,6 @@ kda_status check_alog(const char* fn, int64_t len, int32_t H, int32_t d, bool* p
               "%s: A_log has %lld values but H = %d, d = %d; A_log must be [H] (per head) or "
               "[H, d] (per head and channel); other shapes are refused, not reshaped",
               fn, (long long)len, H, d);
-}
-
-kda_status launched(hipError_t e, const char* what) {
-  if (e != hipSuccess) return fail(KDA_ERR_LAUNCH, "%s: launch failed: %s", what, hipGetErrorString(e));
-  return ok();
-}
-
-// Runs a call's launches (`run`).  With KDA_DEBUG=1 `pre` first adds the scans
-// of its inputs (a failure returns KDA_ERR_DOMAIN before `run`), and `post`
-// the scans of its outputs after it (KDA_ERR_NONFINITE); the call then waits
-// for its stream.
-template <class Pre, class Run, class Post>
-kda_status run_checked(const char* fn, hipStream_t s, Pre pre, Run run, Post post) {
-  if (!kda::dbg::enabled()) return launched(run(), fn);
-  std::lock_guard<std::mutex> lock(kda::dbg::mutex());
-  kda::dbg::Session ses(s);
-  std::string rep;
-  hipError_t e = ses.begin();
-  if (e == hipSuccess) {
-    pre(ses);
-    e = ses.finish(&rep);
-  }
-  if (e != hipSuccess)
-    return fail(KDA_ERR_LAUNCH, "%s (KDA_DEBUG): input scan failed: %s", fn, hipGetErrorString(e));
-  if (!rep.empty())
-    return fail(KDA_ERR_DOMAIN, "%s (KDA_DEBUG): %s; nothing was launched", fn, rep.c_str());
-  e = run();
-  if (e != hipSuccess) return launched(e, fn);
-  e = ses.begin();
-  if (e == hipSuccess) {
-    post(ses);
-    e = ses.finish(&rep);
-  }
-  if (e != hipSuccess)
-    return fail(KDA_ERR_LAUNCH, "%s (KDA_DEBUG): output scan failed: %s", fn,
-                hipGetErrorString(e));
-  if (!rep.empty()) return fail(KDA_ERR_NONFINITE, "%s (KDA_DEBUG): %s", fn, rep.c_str());
-  return ok();
 }
 
 using kda::dbg::kFinite;

@@ -63,17 +63,32 @@ __global__ void scan_kernel(const void* __restrict__ p, int64_t n, int rule, uin
   if (bad) atomicAdd(word, bad);
 }
 
-// One workgroup per (sequence, head): the 128 x 128 state of slot idx[n]
+// Rows of `cols` values, `stride` values apart.
+template <bool BF16>
+__global__ void scan_rows_kernel(const void* __restrict__ p, int64_t rows, int64_t cols,
+                                 int64_t stride, int rule, uint32_t* word) {
+  uint32_t bad = 0;
+  const int64_t step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < rows * cols; i += step) {
+    const int64_t at = (i / cols) * stride + i % cols;
+    const float x = BF16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(p)[at])
+                         : static_cast<const float*>(p)[at];
+    bad += value_ok(x, rule) ? 0u : 1u;
+  }
+  if (bad) atomicAdd(word, bad);
+}
+
+// One workgroup per (sequence, head): the state (elems values) of slot idx[n]
 // (n without indices); slots outside [0, slots) are skipped.
 template <bool BF16>
 __global__ void scan_states_kernel(const void* __restrict__ p, const int32_t* __restrict__ idx,
-                                   int64_t slots, int H, uint32_t* word) {
+                                   int64_t slots, int H, int elems, uint32_t* word) {
   const int n = blockIdx.x / H, h = blockIdx.x % H;
   const int64_t s = idx ? static_cast<int64_t>(idx[n]) : n;
   if (s < 0 || s >= slots) return;
-  const int64_t base = (s * H + h) * 128 * 128;
+  const int64_t base = (s * H + h) * elems;
   uint32_t bad = 0;
-  for (int i = threadIdx.x; i < 128 * 128; i += blockDim.x) {
+  for (int i = threadIdx.x; i < elems; i += blockDim.x) {
     const float x = BF16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(p)[base + i])
                          : static_cast<const float*>(p)[base + i];
     bad += __builtin_isfinite(x) ? 0u : 1u;
@@ -133,15 +148,30 @@ void Session::add(const char* what, const void* p, int64_t n, bool bf16, int rul
   ++count_;
 }
 
+void Session::add_rows(const char* what, const void* p, int64_t rows, int64_t cols,
+                       int64_t stride, bool bf16, int rule) {
+  if (!p || rows <= 0 || cols <= 0 || count_ >= kMaxScans) return;
+  const int64_t blocks64 = (rows * cols + 255) / 256;
+  const unsigned blocks = (unsigned)(blocks64 < 2048 ? blocks64 : 2048);
+  if (bf16)
+    scan_rows_kernel<true><<<blocks, 256, 0, stream_>>>(p, rows, cols, stride, rule, words_ + count_);
+  else
+    scan_rows_kernel<false><<<blocks, 256, 0, stream_>>>(p, rows, cols, stride, rule, words_ + count_);
+  what_[count_] = what;
+  rule_[count_] = rule;
+  n_[count_] = rows * cols;
+  ++count_;
+}
+
 void Session::add_states(const char* what, const void* p, bool bf16, const int32_t* idx,
-                         int64_t slots, int N, int H) {
+                         int64_t slots, int N, int H, int elems) {
   if (!p || N <= 0 || H <= 0 || count_ >= kMaxScans) return;
   const unsigned blocks = (unsigned)((int64_t)N * H);
-  if (bf16) scan_states_kernel<true><<<blocks, 256, 0, stream_>>>(p, idx, slots, H, words_ + count_);
-  else scan_states_kernel<false><<<blocks, 256, 0, stream_>>>(p, idx, slots, H, words_ + count_);
+  if (bf16) scan_states_kernel<true><<<blocks, 256, 0, stream_>>>(p, idx, slots, H, elems, words_ + count_);
+  else scan_states_kernel<false><<<blocks, 256, 0, stream_>>>(p, idx, slots, H, elems, words_ + count_);
   what_[count_] = what;
   rule_[count_] = kFinite;
-  n_[count_] = (int64_t)N * H * 128 * 128;
+  n_[count_] = (int64_t)N * H * elems;
   ++count_;
 }
 

@@ -23,10 +23,13 @@ class Session {
   hipError_t begin();    // clears the counters (a kernel on the stream)
   // count the values of p[0 .. n) (fp32 or bf16) that break `rule`
   void add(const char* what, const void* p, int64_t n, bool bf16, int rule);
-  // count non-finite values of the 128 x 128 states of slot idx[n] (n when idx is
-  // null) for every (sequence n < N, head), skipping slots outside [0, slots)
+  // the same over rows of `cols` values, `stride` values apart
+  void add_rows(const char* what, const void* p, int64_t rows, int64_t cols, int64_t stride,
+                bool bf16, int rule);
+  // count non-finite values of the states (elems values each) of slot idx[n] (n when
+  // idx is null) for every (sequence n < N, head), skipping slots outside [0, slots)
   void add_states(const char* what, const void* p, bool bf16, const int32_t* idx, int64_t slots,
-                  int N, int H);
+                  int N, int H, int elems = 128 * 128);
   // waits for the stream; report lists every scan that found values ("" if none)
   hipError_t finish(std::string* report);
 

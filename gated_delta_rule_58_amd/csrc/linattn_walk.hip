@@ -1,0 +1,1078 @@
+// kda_linattn_chunk_prefill and its backward: the chunked form of
+//
+//   S_t = exp(g_t) S_{t-1} + b_t c_t^T          out_t = scale S_t^T a_t
+//
+// with (a, b, c) = (q, k, v).  Per chunk of 64 tokens with entry state S and
+// gamma_r = sum_{s <= r} g_s inside the chunk:
+//   P[r,s]  = (a_r . b_s) e^(gamma_r - gamma_s)       (s <= r)
+//   out     = scale (e^gamma (A S) + P C)
+//   S      <- e^gamma_end S + B^T (e^(gamma_end - gamma) C)
+// Every factor is at most 1, so nothing overflows however strong the decay is.
+//
+// The gradients are the same recurrence.  With D_t = dL/dS_t,
+//   D_t = scale q_t do_t^T + e^{g_{t+1}} D_{t+1},   dq_t = scale S_t do_t,
+//   dk_t = D_t v_t,  dv_t = D_t^T k_t,
+// so dq is the walk of (a, b, c) = (do, v, k) with the state S^T, and dv and dk
+// are walks from the last token to the first of (k, q, do) with state D and of
+// (v, do, q) with state D^T; there token t's decay is g_{t+1} and the state
+// carries scale.  One kernel runs the three walks at once (blockIdx.y).
+//
+// dg: with G[j,i] = P[j,i] dP[j,i] the part of the loss's derivative that token
+// i's key and token j's query share (i = before the first token: the initial
+// state; j = after the last: the final state), the decay of t lies between i
+// and j when i < t <= j, so
+//   dg_t = sum_{i < t <= j} G[j,i] = sum_{j >= t} q_j.dq_j - sum_{i >= t} k_i.dk_i
+// The pairs i = j cancel in that difference; they are left out of both dots, in
+// which they would be the largest terms when the decay is strong.  To keep the
+// sums short, <S, dL/dS> at the end of every segment of tokens takes the place
+// of the sums over all later tokens (dg_kernel).
+//
+// Workgroup: four waves, 64 columns of c (and so of S and out) of one
+// (sequence, head); wave w owns columns 16w .. 16w+15 of the tile and keeps its
+// slice of S in MFMA accumulators.  The scores are shared: the waves compute
+// their 16 x 16 tiles together and exchange them through LDS.
+//
+// Fragments (16x16x32: lane = (lr, lg), lr the row or column, k = 8 lg + e):
+//   scores     computed transposed, b a^T: the accumulators of two row tiles of
+//              tokens s are, unchanged, the right operand of c^T P^T, with the
+//              token order 16(e >> 2) + 4 lg + (e & 3); c^T is read from LDS in
+//              that order with the transposing LDS read (four tokens of one
+//              column a lane)
+//   state      tile t = 2kk + h holds channels 32kk + 8lg + 4h + i in its rows
+//              4lg + i, so that the tile pair is the left operand S^T of S^T a^T
+//              in natural channel order; b^T is read transposed to match
+// LDS rows are 64 or 128 channels; the 16-byte blocks of a row are swizzled so
+// that both kinds of read spread over the banks.
+//
+// Precision: a, b, c in bf16 enter as they are (fp32 ones as three bf16 values
+// that add up to them), P as NPP, S as NPS and the decayed c as NPC bf16 values;
+// accumulators, decays and the state are fp32, gamma is summed in 64 bits and
+// kept as two fp32 values, so that a strong decay early in a chunk costs the
+// weak ones behind it no digits.
+#include "chunk_common.hpp"
+#include "linattn.hpp"
+
+namespace kda {
+namespace linattn {
+
+using chunk::ex2;
+using chunk::mma_bf16;
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+namespace {
+
+constexpr int C = 64;        // tokens a chunk
+constexpr int CT = 64;       // columns a workgroup
+constexpr int NTHR = 256;
+constexpr int kMinSegChunks = 8;   // shortest segment of a cut sequence
+constexpr int kBorderChunks = 32;  // segments of dg's sums when sequences are walked whole
+constexpr int UNITS = 6;     // score units: pairs of token tiles (row tile i, step ks)
+
+// swizzle of the 16-byte block index of a row (rows of 128 / 64 channels)
+template <int W>
+__device__ __forceinline__ int swz(int row) {
+  if constexpr (W == 128) return ((row & 3) << 2) | ((row >> 2) & 3);
+  else return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+}
+
+__device__ __forceinline__ f32x8 widen8(bf16x8 x) { return __builtin_convertvector(x, f32x8); }
+
+// x as the sum of NP bf16 values (each the rounding of what is left)
+template <int NP>
+__device__ __forceinline__ void split8(f32x8 x, bf16x8 (&out)[NP]) {
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    out[p] = __builtin_convertvector(x, bf16x8);
+    if (p + 1 < NP) x -= widen8(out[p]);
+  }
+}
+
+// acc += A B over the planes of A and B that matter (i + j < the larger count)
+template <int NA, int NB>
+__device__ __forceinline__ void mma_planes(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB],
+                                           f32x4& acc) {
+  constexpr int NMAX = NA > NB ? NA : NB;
+#pragma unroll
+  for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = NB - 1; j >= 0; --j)
+      if (i + j < NMAX) acc = mma_bf16(a[i], b[j], acc);
+}
+
+__device__ __forceinline__ s16x4 read_tr(const char* p) {
+  typedef __attribute__((address_space(3))) s16x4* P;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)p);
+}
+// tokens 4lg .. +3 of two token tiles, one column a lane
+__device__ __forceinline__ bf16x8 read_tr2(const char* p0, const char* p1) {
+  const s16x4 a = read_tr(p0), b = read_tr(p1);
+  return __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
+}
+
+struct Walk {
+  Operand a, b, c, x;       // x: the tensor of the dots (with dots)
+  const void* s_in;         // entry states, or null (zeros)
+  void* s_out;              // exit states, or null
+  int64_t s_row, s_col;     // element strides of the states' channel and column
+  int64_t s_elems;          // elements of one state
+  const int32_t* in_idx;    // slot per sequence, or null
+  const int32_t* out_idx;
+  int64_t in_slots, out_slots;
+  void* out;                // [T, H, CD]
+  float* dots;              // [T, H, 8]: x_t . out_t without the pair (t, t), per wave
+  float* ends;              // states at the segments' ends (dg), slot-major, or null
+  float* seg_state;         // cut sequences: each segment's own state, then its entry state
+  float* seg_decay;         // cut sequences: each segment's summed log2-decay [slot, H]
+  bool in_bf16, out_state_bf16, out_bf16, reverse;
+};
+
+struct Args {
+  Walk walk[3];
+  Decay g;
+  const int32_t* cu;   // null: equal lengths
+  int N, T_tot, H, eq_len;
+  int seg_chunks;      // chunks a segment (cut sequences and the dg borders)
+  int nseg;            // segments a workgroup grid covers (1: sequences walked whole)
+  float scale;
+};
+
+// Token range of sequence n.
+__device__ __forceinline__ void seq_range(const Args& A, int n, int& bos, int& len) {
+  if (A.cu) {
+    const int T = A.T_tot;
+    int b = A.cu[n], e = A.cu[n + 1];
+    b = b < 0 ? 0 : (b > T ? T : b);
+    e = e < b ? b : (e > T ? T : e);
+    bos = b;
+    len = e - b;
+  } else {
+    bos = n * A.eq_len;
+    len = A.eq_len;
+  }
+}
+// First slot of sequence n's segments: unique, below T_tot / (64 seg_chunks) + N.
+__device__ __forceinline__ int64_t seg_slot(const Args& A, int n, int bos) {
+  return bos / (C * A.seg_chunks) + n;
+}
+
+template <bool WIDE, int KD>
+struct Lds {
+  static constexpr int NPL = WIDE ? 3 : 1;          // planes of an operand
+  static constexpr int NBUF = WIDE ? 1 : 2;
+  static constexpr int AB = C * KD * 2;             // one plane of a or b
+  static constexpr int CC = C * CT * 2;             // one plane of c
+  static constexpr int buf = NPL * (2 * AB + CC);
+  static constexpr int off_a = 0, off_b = NPL * AB, off_c = 2 * NPL * AB;
+};
+
+// One operand's chunk, global memory -> registers -> LDS planes.  Thread t
+// moves blocks of 8 channels u = t + 256 i: row u / (W / 8), block u % (W / 8).
+template <bool WIDE, int W>
+struct Stage {
+  static constexpr int NB = C * W / 8 / NTHR;   // blocks of 8 channels a thread
+  static constexpr int NP = WIDE ? 3 : 1;
+  u32x4 r[NB][WIDE ? 2 : 1];
+  // rsrc covers the chunk's rows of this head; a row past the chunk lies
+  // outside it and reads zeros
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rsrc, int stride_bytes, bool bf16,
+                                       int rows, bool reverse) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int u = threadIdx.x + NTHR * i;
+      const int row = u / (W / 8), blk = u % (W / 8);
+      const bool in = row < rows;
+      const int tok = reverse ? rows - 1 - row : row;
+      const int off = in ? tok * stride_bytes + blk * (bf16 ? 16 : 32) : 0x7fffff00;
+      r[i][0] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0));
+      if constexpr (WIDE) {
+        r[i][1] = u32x4{0, 0, 0, 0};
+        if (!bf16)
+          r[i][1] = __builtin_bit_cast(
+              u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off + 16, 0, 0));
+      }
+    }
+  }
+  __device__ __forceinline__ void write(char* lds, bool bf16) const {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int u = threadIdx.x + NTHR * i;
+      const int row = u / (W / 8), blk = u % (W / 8);
+      char* p = lds + row * (W * 2) + ((blk ^ swz<W>(row)) << 4);
+      if constexpr (WIDE) {
+        f32x8 x;
+        if (bf16) {
+          x = widen8(__builtin_bit_cast(bf16x8, r[i][0]));
+        } else {
+          const f32x4 lo = __builtin_bit_cast(f32x4, r[i][0]), hi = __builtin_bit_cast(f32x4, r[i][1]);
+          x = f32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        }
+        bf16x8 pl[3];
+        split8<3>(x, pl);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<bf16x8*>(p + k * (C * W * 2)) = pl[k];
+      } else {
+        *reinterpret_cast<u32x4*>(p) = r[i][0];
+      }
+    }
+  }
+};
+
+// Buffer over the chunk's rows [tok0, tok0 + rows) of head h (a null tensor is zeros).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const Operand& o, int64_t tok0, int rows,
+                                                          int h, int d, int col0, int cols) {
+  const int es = o.bf16 ? 2 : 4;
+  const char* p = static_cast<const char*>(o.p) +
+                  (tok0 * o.stride + (int64_t)(h / o.group) * d + col0) * es;
+  return buffer_over(p, rows > 0 && o.p ? (uint32_t)(((rows - 1) * o.stride + cols) * es) : 0);
+}
+
+// FULL: out, dots and the states; else only the segment's own state and decay.
+// DOTS: the backward's walks.
+template <bool WIDE, int KD, bool FULL, bool DOTS>
+__global__ void __launch_bounds__(NTHR, 1) walk_kernel(Args A) {
+  using L = Lds<WIDE, KD>;
+  constexpr int NPL = L::NPL;
+  constexpr int NPP = WIDE ? 3 : 2, NPS = WIDE ? 3 : 2, NPC = 3;
+  constexpr int KK = KD / 32;   // contraction steps over the channels
+  constexpr int NT = KD / 16;   // state tiles a wave
+  __shared__ __attribute__((aligned(16))) char lds[L::NBUF * L::buf];
+  __shared__ __attribute__((aligned(16))) char s_p[FULL ? UNITS * 1024 * NPP : 16];
+  __shared__ __attribute__((aligned(16))) float s_gh[2][C], s_gl[2][C], s_row[2][C], s_col[2][C];
+  __shared__ float s_diag[C];
+  __shared__ float s_end[2];
+  __shared__ int s_seq[1];
+
+  const Walk& W = A.walk[blockIdx.y];
+  const int tid = threadIdx.x;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = tid & 63, lr = lane & 15, lg = lane >> 4;
+  const bool rev = W.reverse;
+
+  // ---- blockIdx.x -> (sequence, segment, head, tile): the tiles of a head on one XCD
+  const int CD = static_cast<int>(W.s_elems / KD);
+  const int ntile = CD / CT;
+  int id = blockIdx.x >> 3;
+  const int tile = id % ntile;
+  const int64_t pair = (int64_t)(id / ntile) * 8 + (blockIdx.x & 7);
+  if (pair >= (int64_t)A.N * A.nseg * A.H) return;
+  const int h = static_cast<int>(pair % A.H);
+  const int seg = static_cast<int>((pair / A.H) % A.nseg);
+  int n = static_cast<int>(pair / A.H / A.nseg);
+  if (A.cu) n = chunk::lpt_sequence(A.cu, A.N, A.T_tot, n, s_seq);
+  int bos, len;
+  seq_range(A, n, bos, len);
+  const int nch_all = (len + C - 1) / C;
+  int c_lo = 0, c_hi = nch_all;
+  if (A.nseg > 1) {
+    c_lo = seg * A.seg_chunks;
+    c_hi = c_lo + A.seg_chunks < nch_all ? c_lo + A.seg_chunks : nch_all;
+    if (c_lo >= c_hi) {
+      // a sequence without tokens still hands its entry state on (scan kernel)
+      return;
+    }
+  }
+  const int nch = c_hi - c_lo;
+  const int64_t slot0 = seg_slot(A, n, bos);
+  const int col = tile * CT + 16 * w + lr;  // this lane's column of S
+
+  // ---- entry state
+  f32x4 S[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto channel = [&](int t) { return 32 * (t >> 1) + 8 * lg + 4 * (t & 1); };
+  // a segment's states in the workspace: fp32, tile by tile in this lane's order
+  auto seg_at = [&](float* base, int64_t slot) {
+    return base + ((slot * A.H + h) * ntile + tile) * (int64_t)(KD * CT) + (w * 64 + lane) * 4;
+  };
+  if constexpr (FULL) {
+    if (A.nseg > 1) {
+      const float* p = seg_at(W.seg_state, slot0 + seg);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) S[t] = *reinterpret_cast<const f32x4*>(p + t * (NTHR * 4));
+    } else if (W.s_in) {
+      const int64_t sl = W.in_idx ? (int64_t)W.in_idx[n] : n;
+      if (sl >= 0 && sl < W.in_slots) {
+        const int64_t base = (sl * A.H + h) * W.s_elems + col * W.s_col;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            S[t][i] = load1(W.s_in, base + (channel(t) + i) * W.s_row, W.in_bf16);
+      }
+    }
+  }
+
+  Stage<WIDE, KD> ra, rb;
+  Stage<WIDE, CT> rc;
+  const int sa = (int)(W.a.stride * (W.a.bf16 ? 2 : 4)), sb = (int)(W.b.stride * (W.b.bf16 ? 2 : 4)),
+            sc = (int)(W.c.stride * (W.c.bf16 ? 2 : 4));
+  auto chunk_of = [&](int it) { return rev ? c_hi - 1 - it : c_lo + it; };
+  auto rows_in = [&](int c) { return len - c * C < C ? len - c * C : C; };
+  auto load_chunk = [&](int c) {
+    const int rows = rows_in(c);
+    const int64_t tok0 = (int64_t)bos + c * C;
+    if constexpr (FULL) ra.load(rows_of(W.a, tok0, rows, h, KD, 0, KD), sa, W.a.bf16, rows, rev);
+    rb.load(rows_of(W.b, tok0, rows, h, KD, 0, KD), sb, W.b.bf16, rows, rev);
+    rc.load(rows_of(W.c, tok0, rows, h, CD, tile * CT, CT), sc, W.c.bf16, rows, rev);
+  };
+  auto write_chunk = [&](int buf) {
+    char* p = lds + buf * L::buf;
+    if constexpr (FULL) ra.write(p + L::off_a, W.a.bf16);
+    rb.write(p + L::off_b, W.b.bf16);
+    rc.write(p + L::off_c, W.c.bf16);
+  };
+  // log2-decay of row `lane` of chunk c (rows past the chunk: 0).  Walking
+  // backwards, token t's decay is that of t + 1 and the last token's is 0.
+  auto load_decay = [&](int c) -> float {
+    const int rows = rows_in(c);
+    if (lane >= rows) return 0.f;
+    const int t = c * C + (rev ? rows - 1 - lane : lane) + (rev ? 1 : 0);
+    if (t >= len) return 0.f;
+    const float g = A.g.g[A.g.per_token ? ((int64_t)bos + t) * A.H + h : h];
+    return clamp_log_decay(g);
+  };
+  // the chunk's decays (one wave): gamma as two floats, row and column factors
+  double seg_sum = 0.0;
+  auto decays = [&](float g, int buf) {
+    double x = (double)g * 1.4426950408889634;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const double y = __shfl_up(x, off);
+      if (lane >= off) x += y;
+    }
+    const double end = __shfl(x, 63);
+    const float hi = (float)x;
+    s_gh[buf][lane] = hi;
+    s_gl[buf][lane] = (float)(x - (double)hi);
+    s_row[buf][lane] = ex2(hi) * (rev ? 1.0f : A.scale);
+    s_col[buf][lane] = ex2((float)(end - x)) * (rev ? A.scale : 1.0f);
+    if (lane == 0) s_end[buf] = ex2((float)end);
+    seg_sum += end;
+  };
+
+  // lane constants of the LDS reads
+  const int swA = swz<KD>(lr);                       // row reads: rows 16 i + lr
+  const int tj = 4 * lg + (lr >> 2);                 // transposed reads: row of a token tile
+  const int swB = swz<KD>(tj), swC = swz<CT>(tj);
+  const int pc = lr & 3;
+
+  float gnext = 0.f;
+  if (nch > 0) {
+    load_chunk(chunk_of(0));
+    if (w == 3) {
+      decays(load_decay(chunk_of(0)), 0);
+      if (nch > 1) gnext = load_decay(chunk_of(1));
+    }
+  }
+  const int out_es = W.out_bf16 ? 2 : 4;
+
+  for (int it = 0; it < nch; ++it) {
+    const int c = chunk_of(it);
+    const int rows = rows_in(c);
+    const int buf = L::NBUF == 2 ? (it & 1) : 0;
+    const int gb = it & 1;
+    const char* ba = lds + buf * L::buf + L::off_a;
+    const char* bb = lds + buf * L::buf + L::off_b;
+    const char* bc = lds + buf * L::buf + L::off_c;
+    if constexpr (L::NBUF == 1) {
+      if (it) barrier_lds();  // everyone has read the chunk before
+    }
+    write_chunk(buf);
+    if (it + 1 < nch) load_chunk(chunk_of(it + 1));
+    if constexpr (FULL && DOTS) {
+      // states at the segments' ends, for dg: the forward walk after the last
+      // chunk of a segment (below), the backward ones before it
+      if (W.ends && rev && ((c + 1) % A.seg_chunks == 0 || c + 1 == nch_all)) {
+        float* p = seg_at(W.ends, slot0 + c / A.seg_chunks);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(p + t * (NTHR * 4)) = S[t];
+      }
+    }
+    barrier_lds();
+
+    f32x4 acc[4];
+    if constexpr (FULL) {
+      // ---- scores: wave 0 (3,0), wave 1 (3,1), wave 2 (2,0) (2,1), wave 3 (1,0) (0,0)
+      auto unit = [&](int i, int ks, bool two, int slot) {
+        f32x4 p0 = {0.f, 0.f, 0.f, 0.f}, p1 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+          const int blk = ((4 * kk + lg) ^ swA) << 4;
+          bf16x8 fa[NPL], f0[NPL], f1[NPL];
+#pragma unroll
+          for (int p = 0; p < NPL; ++p) {
+            fa[p] = *reinterpret_cast<const bf16x8*>(ba + p * L::AB + (16 * i + lr) * (KD * 2) + blk);
+            f0[p] = *reinterpret_cast<const bf16x8*>(bb + p * L::AB + (32 * ks + lr) * (KD * 2) + blk);
+            f1[p] = *reinterpret_cast<const bf16x8*>(bb + p * L::AB + (32 * ks + 16 + lr) * (KD * 2) + blk);
+          }
+          mma_planes<NPL, NPL>(f0, fa, p0);
+          if (two) mma_planes<NPL, NPL>(f1, fa, p1);
+        }
+        const int r = 16 * i + lr;
+        const float rh = s_gh[gb][r], rl = s_gl[gb][r];
+        f32x8 pv;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int s0 = 32 * ks + 16 * half + 4 * lg;
+          const f32x4 sh = *reinterpret_cast<const f32x4*>(&s_gh[gb][s0]);
+          const f32x4 sl = *reinterpret_cast<const f32x4*>(&s_gl[gb][s0]);
+          const f32x4 v = half ? p1 : p0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = v[e] * A.scale * ex2((rh - sh[e]) + (rl - sl[e]));
+            if constexpr (DOTS) {
+              if (s0 + e == r) s_diag[r] = x;
+              pv[4 * half + e] = (W.dots ? s0 + e < r : s0 + e <= r) ? x : 0.f;
+            } else {
+              pv[4 * half + e] = s0 + e <= r ? x : 0.f;
+            }
+          }
+        }
+        bf16x8 pl[NPP];
+        split8<NPP>(pv, pl);
+#pragma unroll
+        for (int p = 0; p < NPP; ++p)
+          *reinterpret_cast<bf16x8*>(s_p + (p * UNITS + slot) * 1024 + lane * 16) = pl[p];
+      };
+      if (w == 0) {
+        unit(3, 0, true, 4);
+      } else if (w == 1) {
+        unit(3, 1, true, 5);
+      } else if (w == 2) {
+        unit(2, 0, true, 2);
+        unit(2, 1, false, 3);
+      } else {
+        unit(1, 0, true, 1);
+        unit(0, 0, false, 0);
+      }
+      // ---- out^T = S^T a^T, then its rows' decay
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        const f32x4 t0 = S[2 * kk], t1 = S[2 * kk + 1];
+        bf16x8 fs[NPS];
+        split8<NPS>(f32x8{t0[0], t0[1], t0[2], t0[3], t1[0], t1[1], t1[2], t1[3]}, fs);
+        const int blk = ((4 * kk + lg) ^ swA) << 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          bf16x8 fa[NPL];
+#pragma unroll
+          for (int p = 0; p < NPL; ++p)
+            fa[p] = *reinterpret_cast<const bf16x8*>(ba + p * L::AB + (16 * i + lr) * (KD * 2) + blk);
+          mma_planes<NPS, NPL>(fs, fa, acc[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] *= s_row[gb][16 * i + lr];
+      barrier_lds();
+    }
+
+    // ---- out^T += c^T P^T;  S <- e^gamma_end S + b^T (decayed c)
+    {
+      const float dec = s_end[gb];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) S[t] *= dec;
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const int r0 = 32 * ks + tj, r1 = r0 + 16;
+      bf16x8 fc[NPL];
+      const int cb = (((2 * w + (pc >> 1)) ^ swC) << 4) + ((pc & 1) << 3);
+#pragma unroll
+      for (int p = 0; p < NPL; ++p)
+        fc[p] = read_tr2(bc + p * L::CC + r0 * (CT * 2) + cb, bc + p * L::CC + r1 * (CT * 2) + cb);
+      if constexpr (FULL) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (2 * ks > i) continue;  // tokens behind row tile i
+          const int slot = i < 2 ? i : 2 * i - 2 + ks;
+          bf16x8 fp[NPP];
+#pragma unroll
+          for (int p = 0; p < NPP; ++p)
+            fp[p] = *reinterpret_cast<const bf16x8*>(s_p + (p * UNITS + slot) * 1024 + lane * 16);
+          mma_planes<NPL, NPP>(fc, fp, acc[i]);
+        }
+      }
+      // the decayed c
+      f32x8 x = widen8(fc[0]);
+#pragma unroll
+      for (int p = 1; p < NPL; ++p) x += widen8(fc[p]);
+      const f32x4 e0 = *reinterpret_cast<const f32x4*>(&s_col[gb][32 * ks + 4 * lg]);
+      const f32x4 e1 = *reinterpret_cast<const f32x4*>(&s_col[gb][32 * ks + 16 + 4 * lg]);
+      x *= f32x8{e0[0], e0[1], e0[2], e0[3], e1[0], e1[1], e1[2], e1[3]};
+      bf16x8 fx[NPC];
+      split8<NPC>(x, fx);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int at = (((4 * (t >> 1) + pc) ^ swB) << 4) + ((t & 1) << 3);
+        bf16x8 fb[NPL];
+#pragma unroll
+        for (int p = 0; p < NPL; ++p)
+          fb[p] = read_tr2(bb + p * L::AB + r0 * (KD * 2) + at, bb + p * L::AB + r1 * (KD * 2) + at);
+        mma_planes<NPL, NPC>(fb, fx, S[t]);
+      }
+    }
+    // the next chunk's decays, by the wave with the fewest scores
+    if (w == 3 && it + 1 < nch) {
+      decays(gnext, gb ^ 1);
+      if (it + 2 < nch) gnext = load_decay(chunk_of(it + 2));
+    }
+
+    if constexpr (FULL) {
+      const int64_t tok0 = (int64_t)bos + c * C;
+      const int64_t ld = (int64_t)A.H * CD;
+      if constexpr (DOTS) {
+        if (W.dots) {
+          // x_t . out_t over this wave's columns, then the pair (t, t)
+          const __amdgpu_buffer_rsrc_t xr = rows_of(W.x, tok0, rows, h, CD, 0, CD);
+          const int xs = (int)(W.x.stride * (W.x.bf16 ? 2 : 4));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 16 * i + lr;
+            const int tok = rev ? rows - 1 - row : row;
+            const int xc = tile * CT + 16 * w + 4 * lg;
+            f32x4 xv = {0.f, 0.f, 0.f, 0.f};
+            if (W.x.bf16) {
+              const int off = row < rows ? tok * xs + xc * 2 : 0x7fffff00;
+              typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+              const u16x4 b = __builtin_bit_cast(
+                  u16x4, __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(xr, off, 0, 0)));
+              xv = f32x4{bf16_bits_to_f32(b[0]), bf16_bits_to_f32(b[1]), bf16_bits_to_f32(b[2]),
+                         bf16_bits_to_f32(b[3])};
+            } else {
+              const int off = row < rows ? tok * xs + xc * 4 : 0x7fffff00;
+              xv = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, off, 0, 0));
+            }
+            float dot = xv[0] * acc[i][0] + xv[1] * acc[i][1] + xv[2] * acc[i][2] + xv[3] * acc[i][3];
+            dot += __shfl_xor(dot, 16);
+            dot += __shfl_xor(dot, 32);
+            if (lg == 0 && row < rows)
+              W.dots[((tok0 + tok) * A.H + h) * 8 + tile * 4 + w] = dot;
+            // + P[t,t] c_t
+            const float pd = s_diag[row];
+            const int cc = 16 * w + 4 * lg;
+            const char* cp = bc + row * (CT * 2) + (((cc >> 3) ^ swz<CT>(row)) << 4) + ((cc & 7) << 1);
+#pragma unroll
+            for (int p = 0; p < NPL; ++p) {
+              const u16x4 b = *reinterpret_cast<const u16x4*>(cp + p * L::CC);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][e] += pd * bf16_bits_to_f32(b[e]);
+            }
+          }
+        }
+      }
+      const __amdgpu_buffer_rsrc_t orow =
+          buffer_over(static_cast<char*>(W.out) + (tok0 * ld + (int64_t)h * CD) * out_es,
+                      (uint32_t)(((rows - 1) * ld + CD) * out_es));
+      const int oc = tile * CT + 16 * w + 4 * lg;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 16 * i + lr;
+        const int tok = rev ? rows - 1 - row : row;
+        const int off = row < rows ? (int)((tok * ld + oc) * out_es) : 0x7fffff00;
+        if (W.out_bf16) {
+          const u16x4 b = {f32_to_bf16_bits(acc[i][0]), f32_to_bf16_bits(acc[i][1]),
+                           f32_to_bf16_bits(acc[i][2]), f32_to_bf16_bits(acc[i][3])};
+          typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, b), orow, off, 0, 0);
+        } else {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i]), orow, off, 0, 0);
+        }
+      }
+      if constexpr (DOTS) {
+        if (W.ends && !rev && ((c + 1) % A.seg_chunks == 0 || c + 1 == nch_all)) {
+          float* p = seg_at(W.ends, slot0 + c / A.seg_chunks);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(p + t * (NTHR * 4)) = S[t];
+        }
+      }
+    }
+  }
+
+  if constexpr (!FULL) {
+    float* p = seg_at(W.seg_state, slot0 + seg);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(p + t * (NTHR * 4)) = S[t];
+    if (w == 3 && lane == 0 && tile == 0) W.seg_decay[(slot0 + seg) * A.H + h] = (float)seg_sum;
+  } else if (A.nseg == 1 && W.s_out) {
+    const int64_t sl = W.out_idx ? (int64_t)W.out_idx[n] : n;
+    if (sl >= 0 && sl < W.out_slots) {
+      // walking backwards, the state before the first token has its decay too
+      float first = 1.0f;
+      if (rev && len > 0)
+        first = ex2(clamp_log_decay(A.g.g[A.g.per_token ? (int64_t)bos * A.H + h : h]) *
+                    1.4426950408889634f);
+      const int64_t base = (sl * A.H + h) * W.s_elems + col * W.s_col;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t at = base + (channel(t) + i) * W.s_row;
+          const float x = S[t][i] * first;
+          if (W.out_state_bf16) static_cast<uint16_t*>(W.s_out)[at] = f32_to_bf16_bits(x);
+          else static_cast<float*>(W.s_out)[at] = x;
+        }
+    }
+  }
+}
+
+// Cut sequences: the segments' own states become their entry states, and the
+// exit state is written.  One workgroup per (sequence, head, tile) and walk;
+// the threads own the elements in the walk kernel's order.
+template <int KD>
+__global__ void __launch_bounds__(NTHR) scan_kernel(Args A) {
+  constexpr int NT = KD / 16;
+  const Walk& W = A.walk[blockIdx.y];
+  const int CD = static_cast<int>(W.s_elems / KD);
+  const int ntile = CD / CT;
+  const int t = blockIdx.x % NT;          // state tile
+  int id = blockIdx.x / NT;
+  const int tile = id % ntile;
+  id /= ntile;
+  const int h = id % A.H, n = id / A.H;
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  int bos, len;
+  seq_range(A, n, bos, len);
+  const int nch = (len + C - 1) / C;
+  const int nseg = (nch + A.seg_chunks - 1) / A.seg_chunks;
+  const int64_t slot0 = seg_slot(A, n, bos);
+  const int ch = 32 * (t >> 1) + 8 * lg + 4 * (t & 1);
+  const int col = tile * CT + 16 * w + lr;
+  f32x4 S = {0.f, 0.f, 0.f, 0.f};
+  if (W.s_in) {
+    const int64_t sl = W.in_idx ? (int64_t)W.in_idx[n] : n;
+    if (sl >= 0 && sl < W.in_slots) {
+      const int64_t base = (sl * A.H + h) * W.s_elems + col * W.s_col;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[i] = load1(W.s_in, base + (ch + i) * W.s_row, W.in_bf16);
+    }
+  }
+  auto at = [&](int j) {
+    const int64_t slot = slot0 + (W.reverse ? nseg - 1 - j : j);
+    return W.seg_state + ((slot * A.H + h) * ntile + tile) * (int64_t)(KD * CT) +
+           (w * 64 + lane) * 4 + t * (NTHR * 4);
+  };
+  f32x4 next = S;
+  if (nseg > 0) next = *reinterpret_cast<const f32x4*>(at(0));
+  for (int j = 0; j < nseg; ++j) {
+    const f32x4 own = next;
+    if (j + 1 < nseg) next = *reinterpret_cast<const f32x4*>(at(j + 1));
+    const int64_t slot = slot0 + (W.reverse ? nseg - 1 - j : j);
+    *reinterpret_cast<f32x4*>(at(j)) = S;
+    S = S * ex2(W.seg_decay[slot * A.H + h]) + own;
+  }
+  if (W.s_out) {
+    const int64_t sl = W.out_idx ? (int64_t)W.out_idx[n] : n;
+    if (sl >= 0 && sl < W.out_slots) {
+      float first = 1.0f;
+      if (W.reverse && len > 0)
+        first = ex2(clamp_log_decay(A.g.g[A.g.per_token ? (int64_t)bos * A.H + h : h]) *
+                    1.4426950408889634f);
+      const int64_t base = (sl * A.H + h) * W.s_elems + col * W.s_col;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t e = base + (ch + i) * W.s_row;
+        if (W.out_state_bf16) static_cast<uint16_t*>(W.s_out)[e] = f32_to_bf16_bits(S[i] * first);
+        else static_cast<float*>(W.s_out)[e] = S[i] * first;
+      }
+    }
+  }
+}
+
+// dg of one segment of one (sequence, head): suffix sums of q.dq - k.dk, plus
+// <S, dL/dS> at the segment's end.  In 64 bits (a few thousand terms).
+__global__ void __launch_bounds__(NTHR) dg_kernel(Args A, const float* dotq, const float* dotk,
+                                                  const float* ends_s, const float* ends_d,
+                                                  int dk, int dv, bool has_final, float* dg,
+                                                  float* dg_part, int nseg_max) {
+  __shared__ double s_w[4];
+  const int h = blockIdx.x % A.H;
+  const int seg = (blockIdx.x / A.H) % nseg_max;
+  const int n = blockIdx.x / A.H / nseg_max;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  int bos, len;
+  seq_range(A, n, bos, len);
+  const int nch = (len + C - 1) / C;
+  const int nseg = (nch + A.seg_chunks - 1) / A.seg_chunks;
+  if (seg >= nseg) return;
+  const int64_t slot = seg_slot(A, n, bos) + seg;
+  const bool last = seg == nseg - 1;
+  // <S, D> over the state, both in the walks' order
+  double m = 0.0;
+  if (!last || has_final) {
+    const int64_t elems = (int64_t)dk * dv;
+    const f32x4* a = reinterpret_cast<const f32x4*>(ends_s + (slot * A.H + h) * elems);
+    const f32x4* b = reinterpret_cast<const f32x4*>(ends_d + (slot * A.H + h) * elems);
+    f32x4 p = {0.f, 0.f, 0.f, 0.f};
+    for (int i = tid; i < elems / 4; i += NTHR) p += a[i] * b[i];
+    m = ((double)p[0] + (double)p[1]) + ((double)p[2] + (double)p[3]);
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) m += __shfl_xor(m, off);
+  if (lane == 0) s_w[w] = m;
+  __syncthreads();
+  const double border = (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
+  __syncthreads();
+  const int t_lo = seg * A.seg_chunks * C;
+  const int t_hi = t_lo + A.seg_chunks * C < len ? t_lo + A.seg_chunks * C : len;
+  double run = border;
+  if (!last) {  // the gradient walks keep dL/dS_t of the token behind the border
+    const float g = A.g.g[A.g.per_token ? ((int64_t)bos + t_hi) * A.H + h : h];
+    run *= exp((double)clamp_log_decay(g));
+  }
+  const int nq = dk / 16, nk = dk / 16;  // partial dots a token: one a wave
+  double total = 0.0;
+  for (int hi = t_hi; hi > t_lo; hi -= NTHR) {
+    const int t = hi - 1 - tid;
+    double x = 0.0;
+    if (t >= t_lo) {
+      const int64_t at = (((int64_t)bos + t) * A.H + h) * 8;
+      const f32x4 q0 = *reinterpret_cast<const f32x4*>(dotq + at);
+      const f32x4 k0 = *reinterpret_cast<const f32x4*>(dotk + at);
+      f32x4 q1 = {0.f, 0.f, 0.f, 0.f}, k1 = {0.f, 0.f, 0.f, 0.f};
+      if (nq > 4) q1 = *reinterpret_cast<const f32x4*>(dotq + at + 4);
+      if (nk > 4) k1 = *reinterpret_cast<const f32x4*>(dotk + at + 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        x += ((double)q0[e] - (double)k0[e]) + ((double)q1[e] - (double)k1[e]);
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const double y = __shfl_up(x, off);
+      if (lane >= off) x += y;
+    }
+    if (lane == 63) s_w[w] = x;
+    __syncthreads();
+    double before = run;
+    for (int j = 0; j < w; ++j) before += s_w[j];
+    x += before;
+    run += (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
+    __syncthreads();
+    if (t >= t_lo) {
+      if (A.g.per_token) dg[((int64_t)bos + t) * A.H + h] = (float)x;
+      else total += x;
+    }
+  }
+  if (!A.g.per_token) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) total += __shfl_xor(total, off);
+    if (lane == 0) s_w[w] = total;
+    __syncthreads();
+    if (tid == 0) {
+      const double s = (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
+      dg_part[2 * (slot * A.H + h)] = (float)s;
+      dg_part[2 * (slot * A.H + h) + 1] = (float)(s - (double)(float)s);
+    }
+  }
+}
+
+// dg [H] from the segments' sums, in order.  One workgroup per head.
+__global__ void __launch_bounds__(64) dg_heads_kernel(Args A, const float* part, float* dg) {
+  const int h = blockIdx.x;
+  double sum = 0.0;
+  for (int n = 0; n < A.N; ++n) {
+    int bos, len;
+    seq_range(A, n, bos, len);
+    const int nch = (len + C - 1) / C;
+    const int nseg = (nch + A.seg_chunks - 1) / A.seg_chunks;
+    const int64_t slot0 = seg_slot(A, n, bos);
+    for (int j = threadIdx.x; j < nseg; j += 64) {
+      const int64_t at = 2 * ((slot0 + j) * A.H + h);
+      sum += (double)part[at] + (double)part[at + 1];
+    }
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+  if (threadIdx.x == 0) dg[h] = (float)sum;
+}
+
+// dq, dk of shared heads: the sum over the group's heads of the tokens that
+// belong to a sequence.  One thread per 4 channels.
+__global__ void __launch_bounds__(NTHR) group_sum_kernel(Args A, const float* hq, const float* hk,
+                                                         int d, int group, void* dq, void* dk,
+                                                         bool bf16) {
+  const int Hk = A.H / group;
+  const int64_t per = (int64_t)Hk * (d / 4);
+  const int64_t i = (int64_t)blockIdx.x * NTHR + threadIdx.x;
+  // rows behind the last sequence stay as they are
+  int64_t T = A.T_tot;
+  if (A.cu) {
+    const int e = A.cu[A.N];
+    T = e < 0 ? 0 : (e > A.T_tot ? A.T_tot : e);
+  }
+  if (i >= T * per) return;
+  const int64_t t = i / per;
+  const int rest = static_cast<int>(i - t * per);
+  const int hk_i = rest / (d / 4), c = (rest % (d / 4)) * 4;
+  const float* src = blockIdx.y ? hk : hq;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < group; ++j)
+    s += *reinterpret_cast<const f32x4*>(src + (t * A.H + hk_i * group + j) * (int64_t)d + c);
+  store4(blockIdx.y ? dk : dq, (t * Hk + hk_i) * (int64_t)d + c, s, bf16);
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <bool WIDE, int KD, bool FULL, bool DOTS>
+hipError_t launch_walk_kd(const Args& A, int walks, hipStream_t s) {
+  const int64_t blocks =
+      cdiv((int64_t)A.N * A.nseg * A.H, 8) * 8 * (A.walk[0].s_elems / KD / CT);
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  walk_kernel<WIDE, KD, FULL, DOTS><<<dim3((unsigned)blocks, walks), NTHR, 0, s>>>(A);
+  return hipGetLastError();
+}
+// `walks` walks of one contraction width kd
+template <bool DOTS>
+hipError_t launch_walk(const Args& A, int walks, bool wide, int kd, bool full, hipStream_t s) {
+#define KDA_LW(WD, KDV)                                             \
+  return full ? launch_walk_kd<WD, KDV, true, DOTS>(A, walks, s)    \
+              : launch_walk_kd<WD, KDV, false, false>(A, walks, s)
+  if (wide && kd == 128) KDA_LW(true, 128);
+  if (wide) KDA_LW(true, 64);
+  if (kd == 128) KDA_LW(false, 128);
+  KDA_LW(false, 64);
+#undef KDA_LW
+}
+
+hipError_t launch_scan(const Args& A, int walks, int kd, hipStream_t s) {
+  const int64_t blocks = (int64_t)A.N * A.H * (A.walk[0].s_elems / kd / CT) * (kd / 16);
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)blocks, walks);
+  if (kd == 128) scan_kernel<128><<<grid, NTHR, 0, s>>>(A);
+  else scan_kernel<64><<<grid, NTHR, 0, s>>>(A);
+  return hipGetLastError();
+}
+
+// Chunks a segment when sequences are cut, 0 when they are walked whole: with
+// `walkers` workgroups a segment, cut when whole sequences are too few for the
+// card and long enough; segments then give about two workgroups a CU.
+int cut_chunks(int64_t T_tot, int64_t N, int64_t walkers) {
+  if (N * walkers >= 192) return 0;
+  const int64_t chunks = cdiv(T_tot, C);
+  if (chunks < N * 2 * kMinSegChunks) return 0;
+  const int64_t sc = cdiv(chunks * walkers, 512);
+  return static_cast<int>(sc > kMinSegChunks ? sc : kMinSegChunks);
+}
+
+int64_t slots_of(int64_t T_tot, int64_t N, int seg_chunks) {
+  return T_tot / (C * (int64_t)seg_chunks) + N;
+}
+
+struct Carve {  // 256-byte aligned pieces of a workspace
+  char* p;
+  size_t used = 0;
+  float* take(int64_t floats) {
+    float* r = p ? reinterpret_cast<float*>(p + used) : nullptr;
+    used += ((size_t)floats * 4 + 255) / 256 * 256;
+    return r;
+  }
+};
+
+struct ForwardWs {
+  float *state, *decay;
+  size_t bytes;
+  ForwardWs(void* ws, int64_t T_tot, int N, int H, int dk, int dv, int seg) {
+    Carve c{static_cast<char*>(ws)};
+    const int64_t slots = seg ? slots_of(T_tot, N, seg) : 0;
+    state = c.take(slots * H * dk * dv);
+    decay = c.take(slots * H);
+    bytes = c.used;
+  }
+};
+
+struct BackwardWs {
+  float *dotq, *dotk, *ends_s, *ends_d, *dg_part, *hq, *hk, *state[3], *decay[3];
+  size_t bytes;
+  BackwardWs(void* ws, int64_t T_tot, int N, int H, int Hk, int dk, int dv, int seg, bool cut) {
+    Carve c{static_cast<char*>(ws)};
+    const int64_t slots = slots_of(T_tot, N, seg), st = slots * H * dk * dv;
+    dotq = c.take(T_tot * H * 8);
+    dotk = c.take(T_tot * H * 8);
+    ends_s = c.take(st);
+    ends_d = c.take(st);
+    dg_part = c.take(slots * H * 2);
+    const int64_t heads = Hk < H ? T_tot * H * dk : 0;
+    hq = c.take(heads);
+    hk = c.take(heads);
+    for (int i = 0; i < 3; ++i) {
+      state[i] = c.take(cut ? st : 0);
+      decay[i] = c.take(cut ? slots * H : 0);
+    }
+    bytes = c.used;
+  }
+};
+
+// longest sequence: from the host copy, or the most it can be
+int64_t longest(const Args& A, const int32_t* cu_host) {
+  if (!A.cu) return A.eq_len;
+  if (!cu_host) return A.T_tot;
+  int64_t m = 0;
+  for (int n = 0; n < A.N; ++n)
+    m = cu_host[n + 1] - cu_host[n] > m ? cu_host[n + 1] - cu_host[n] : m;
+  return m;
+}
+
+}  // namespace
+
+size_t prefill_workspace_bytes(int64_t T_tot, int N, int H, int dk, int dv) {
+  const int seg = cut_chunks(T_tot, N, (int64_t)H * (dv / CT));
+  return seg ? ForwardWs(nullptr, T_tot, N, H, dk, dv, seg).bytes : 0;
+}
+
+hipError_t launch_prefill(const Problem& p, const Operand& q, const Operand& k, const Operand& v,
+                          const StatePool& st, void* o, bool o_bf16, void* ws, size_t ws_bytes,
+                          hipStream_t s) {
+  Args A{};
+  A.g = p.g;
+  A.cu = p.cu;
+  A.N = p.N;
+  A.T_tot = static_cast<int>(p.T_tot);
+  A.H = p.H;
+  A.eq_len = p.cu ? 0 : static_cast<int>(p.T_tot / p.N);
+  A.scale = p.scale;
+  A.nseg = 1;
+  A.seg_chunks = kBorderChunks;
+  Walk& W = A.walk[0];
+  W.a = q;
+  W.b = k;
+  W.c = v;
+  W.s_in = st.in;
+  W.s_out = st.out;
+  W.in_idx = W.out_idx = st.idx;
+  W.in_slots = W.out_slots = st.slots;
+  W.in_bf16 = W.out_state_bf16 = st.bf16;
+  W.s_row = p.dv;
+  W.s_col = 1;
+  W.s_elems = (int64_t)p.dk * p.dv;
+  W.out = o;
+  W.out_bf16 = o_bf16;
+  const bool wide = !(q.bf16 && k.bf16 && v.bf16);
+  const int seg = cut_chunks(p.T_tot, p.N, (int64_t)p.H * (p.dv / CT));
+  const ForwardWs f(ws, p.T_tot, p.N, p.H, p.dk, p.dv, seg);
+  if (seg && ws && ws_bytes >= f.bytes) {
+    A.seg_chunks = seg;
+    A.nseg = static_cast<int>(cdiv(cdiv(longest(A, p.cu_host), C), seg));
+    if (A.nseg < 1) A.nseg = 1;
+    W.seg_state = f.state;
+    W.seg_decay = f.decay;
+  }
+  if (A.nseg > 1) {
+    hipError_t e = launch_walk<false>(A, 1, wide, p.dk, false, s);
+    if (e == hipSuccess) e = launch_scan(A, 1, p.dk, s);
+    if (e != hipSuccess) return e;
+  }
+  return launch_walk<false>(A, 1, wide, p.dk, true, s);
+}
+
+namespace {
+int border_chunks(int64_t T_tot, int N, int H, int dk, int dv, bool* cut) {
+  const int seg = cut_chunks(T_tot, N, (int64_t)H * (2 * (dk / CT) + dv / CT));
+  *cut = seg > 0;
+  return seg ? seg : kBorderChunks;
+}
+}  // namespace
+
+size_t backward_workspace_bytes(int64_t T_tot, int N, int H, int Hk, int dk, int dv) {
+  bool cut;
+  const int seg = border_chunks(T_tot, N, H, dk, dv, &cut);
+  return BackwardWs(nullptr, T_tot, N, H, Hk, dk, dv, seg, cut).bytes;
+}
+
+hipError_t launch_backward(const Problem& p, const Operand& q, const Operand& k, const Operand& v,
+                           const float* S0, const Operand& d_o, const float* dS, void* dq, void* dk,
+                           void* dv, bool grad_bf16, float* dg, float* dS0, void* ws,
+                           hipStream_t s) {
+  const int DK = p.dk, DV = p.dv, group = p.H / p.Hk;
+  bool cut;
+  const int seg = border_chunks(p.T_tot, p.N, p.H, DK, DV, &cut);
+  const BackwardWs b(ws, p.T_tot, p.N, p.H, p.Hk, DK, DV, seg, cut);
+  Args A{};
+  A.g = p.g;
+  A.cu = p.cu;
+  A.N = p.N;
+  A.T_tot = static_cast<int>(p.T_tot);
+  A.H = p.H;
+  A.eq_len = p.cu ? 0 : static_cast<int>(p.T_tot / p.N);
+  A.scale = p.scale;
+  A.seg_chunks = seg;
+  const int64_t max_chunks = cdiv(longest(A, p.cu_host), C);
+  const int nseg = static_cast<int>(max_chunks ? cdiv(max_chunks, seg) : 1);
+  A.nseg = cut ? nseg : 1;
+
+  Walk wq{}, wk{}, wv{};
+  wq.a = d_o; wq.b = v; wq.c = k; wq.x = q;
+  wk.a = v; wk.b = d_o; wk.c = q; wk.x = k;
+  wv.a = k; wv.b = q; wv.c = d_o;
+  wk.reverse = wv.reverse = true;
+  Walk* ws3[3] = {&wq, &wk, &wv};
+  for (int i = 0; i < 3; ++i) {
+    ws3[i]->s_elems = (int64_t)DK * DV;
+    ws3[i]->in_slots = ws3[i]->out_slots = p.N;
+    ws3[i]->seg_state = b.state[i];
+    ws3[i]->seg_decay = b.decay[i];
+    ws3[i]->out_bf16 = grad_bf16;
+  }
+  wq.s_in = S0;
+  wk.s_in = wv.s_in = dS;
+  wv.s_out = dS0;
+  wq.s_row = wk.s_row = 1;      // the transposed states of dq and dk
+  wq.s_col = wk.s_col = DV;
+  wv.s_row = DV;
+  wv.s_col = 1;
+  wq.dots = b.dotq;
+  wk.dots = b.dotk;
+  wq.ends = b.ends_s;
+  wk.ends = b.ends_d;
+  wq.out = dq;
+  wk.out = dk;
+  wv.out = dv;
+  if (group > 1) {
+    wq.out = b.hq;
+    wk.out = b.hk;
+    wq.out_bf16 = wk.out_bf16 = false;
+  }
+  const bool wide = !(q.bf16 && k.bf16 && v.bf16 && (d_o.bf16 || !d_o.p));
+  A.walk[0] = wq;
+  A.walk[1] = wk;
+  A.walk[2] = wv;
+  Args B = A;  // dk != dv: the walk of dv contracts over another width
+  B.walk[0] = wv;
+  const bool same = DK == DV;
+  for (int phase = A.nseg > 1 ? 0 : 2; phase < 3; ++phase) {
+    hipError_t e;
+    if (phase == 1) {
+      e = launch_scan(A, same ? 3 : 2, DV, s);
+      if (e == hipSuccess && !same) e = launch_scan(B, 1, DK, s);
+    } else {
+      const bool full = phase == 2;
+      e = launch_walk<true>(A, same ? 3 : 2, wide, DV, full, s);
+      if (e == hipSuccess && !same) e = launch_walk<true>(B, 1, wide, DK, full, s);
+    }
+    if (e != hipSuccess) return e;
+  }
+  const int64_t blocks = (int64_t)p.N * nseg * p.H;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  dg_kernel<<<dim3((unsigned)blocks), NTHR, 0, s>>>(A, b.dotq, b.dotk, b.ends_s, b.ends_d, DK, DV,
+                                                    dS != nullptr, dg, b.dg_part, nseg);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (!A.g.per_token) {
+    dg_heads_kernel<<<dim3(p.H), 64, 0, s>>>(A, b.dg_part, dg);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (group > 1 && p.T_tot > 0) {
+    const int64_t n = cdiv(p.T_tot * p.Hk * (DK / 4), NTHR);
+    if (n > 0x7fffffff) return hipErrorInvalidValue;
+    group_sum_kernel<<<dim3((unsigned)n, 2), NTHR, 0, s>>>(A, b.hq, b.hk, DK, group, dq, dk,
+                                                         grad_bf16);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+}  // namespace linattn
+}  // namespace kda
