@@ -27,10 +27,22 @@
 // sums short, <S, dL/dS> at the end of every segment of tokens takes the place
 // of the sums over all later tokens (dg_kernel).
 //
-// Workgroup: four waves, 64 columns of c (and so of S and out) of one
-// (sequence, head); wave w owns columns 16w .. 16w+15 of the tile and keeps its
-// slice of S in MFMA accumulators.  The scores are shared: the waves compute
-// their 16 x 16 tiles together and exchange them through LDS.
+// Workgroup: 64 columns of c (and so of S and out) of one (sequence, head),
+// eight waves of two kinds, one of each kind on every SIMD:
+//   state waves   wave w owns columns 16w .. 16w+15 of S in MFMA accumulators.
+//                 Per chunk it adds b^T (decayed c) and leaves the new state's
+//                 bf16 values in LDS as the operands of the next readout.
+//   output waves  wave i owns the chunk's rows 16i .. 16i+15: scores against the
+//                 tokens up to its rows, S^T a^T, c^T P^T and the stores.  a goes
+//                 from global memory straight to its registers, and the scores
+//                 never leave them.
+// S is the only thing handed over.  With it, b and c double-buffered in LDS the
+// two kinds need one barrier a chunk.
+// What bounds it: the sequential walk.  A layer of 96 heads gives 192
+// workgroups for 256 CUs, each with T / 64 chunks to go through, so the time is
+// chunks x the latency of one chunk until HBM is reached.  LDS carries the most
+// per chunk (240 to 350 KB a workgroup at 128 B a cycle), which is why the output
+// waves split rows and not columns: a and the scores then need no LDS.
 //
 // Fragments (16x16x32: lane = (lr, lg), lr the row or column, k = 8 lg + e):
 //   scores     computed transposed, b a^T: the accumulators of two row tiles of
@@ -60,15 +72,15 @@ using chunk::mma_bf16;
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 namespace {
 
 constexpr int C = 64;        // tokens a chunk
 constexpr int CT = 64;       // columns a workgroup
-constexpr int NTHR = 256;
+constexpr int NTHR = 256;    // threads of the small kernels, and of the state waves
 constexpr int kMinSegChunks = 8;   // shortest segment of a cut sequence
 constexpr int kBorderChunks = 32;  // segments of dg's sums when sequences are walked whole
-constexpr int UNITS = 6;     // score units: pairs of token tiles (row tile i, step ks)
 
 // swizzle of the 16-byte block index of a row (rows of 128 / 64 channels)
 template <int W>
@@ -121,7 +133,7 @@ struct Walk {
   const int32_t* out_idx;
   int64_t in_slots, out_slots;
   void* out;                // [T, H, CD]
-  float* dots;              // [T, H, 8]: x_t . out_t without the pair (t, t), per wave
+  float* dots;              // [T, H, 2]: x_t . out_t without the pair (t, t), per column tile
   float* ends;              // states at the segments' ends (dg), slot-major, or null
   float* seg_state;         // cut sequences: each segment's own state, then its entry state
   float* seg_decay;         // cut sequences: each segment's summed log2-decay [slot, H]
@@ -160,87 +172,102 @@ __device__ __forceinline__ int64_t seg_slot(const Args& A, int n, int bos) {
 template <bool WIDE, int KD>
 struct Lds {
   static constexpr int NPL = WIDE ? 3 : 1;          // planes of an operand
+  static constexpr int NPS = WIDE ? 3 : 2;          // planes of the state
   static constexpr int NBUF = WIDE ? 1 : 2;
-  static constexpr int AB = C * KD * 2;             // one plane of a or b
+  static constexpr int BB = C * KD * 2;             // one plane of b
   static constexpr int CC = C * CT * 2;             // one plane of c
-  static constexpr int buf = NPL * (2 * AB + CC);
-  static constexpr int off_a = 0, off_b = NPL * AB, off_c = 2 * NPL * AB;
+  static constexpr int SS = KD * CT * 2;            // one plane of the state
+  static constexpr int buf = NPL * (BB + CC);
+  static constexpr int off_c = NPL * BB;
+  static constexpr int off_s = NBUF * buf;
+  static constexpr int total = off_s + NBUF * NPS * SS;
 };
 
-// One operand's chunk, global memory -> registers -> LDS planes.  Thread t
-// moves blocks of 8 channels u = t + 256 i: row u / (W / 8), block u % (W / 8).
-template <bool WIDE, int W>
+// The eight values of a block as NP bf16 planes.
+template <bool WIDE>
+__device__ __forceinline__ void planes_of(const u32x4 (&r)[WIDE ? 2 : 1], bool bf16,
+                                          bf16x8 (&pl)[WIDE ? 3 : 1]) {
+  if constexpr (WIDE) {
+    f32x8 x;
+    if (bf16) {
+      x = widen8(__builtin_bit_cast(bf16x8, r[0]));
+    } else {
+      const f32x4 lo = __builtin_bit_cast(f32x4, r[0]), hi = __builtin_bit_cast(f32x4, r[1]);
+      x = f32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    }
+    split8<3>(x, pl);
+  } else {
+    pl[0] = __builtin_bit_cast(bf16x8, r[0]);
+  }
+}
+constexpr int kOutside = 0x7fffff00;  // an offset past every chunk: reads 0, stores nothing
+template <bool WIDE>
+__device__ __forceinline__ void load_block(__amdgpu_buffer_rsrc_t rsrc, int off, bool bf16,
+                                           u32x4 (&r)[WIDE ? 2 : 1]) {
+  r[0] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0));
+  if constexpr (WIDE) {
+    r[1] = u32x4{0, 0, 0, 0};
+    if (!bf16)
+      r[1] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off + 16, 0, 0));
+  }
+}
+
+// One operand's chunk, global memory -> registers -> LDS planes.  Thread t of
+// TH moves blocks of 8 channels u = t + TH i: row u / (W / 8), block u % (W / 8).
+template <bool WIDE, int W, int TH>
 struct Stage {
-  static constexpr int NB = C * W / 8 / NTHR;   // blocks of 8 channels a thread
-  static constexpr int NP = WIDE ? 3 : 1;
+  static constexpr int NB = C * W / 8 / TH;   // blocks of 8 channels a thread
   u32x4 r[NB][WIDE ? 2 : 1];
-  // rsrc covers the chunk's rows of this head; a row past the chunk lies
-  // outside it and reads zeros
+  // rsrc covers the chunk's rows of this head; a row past the chunk reads zeros
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rsrc, int stride_bytes, bool bf16,
                                        int rows, bool reverse) {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      const int u = threadIdx.x + NTHR * i;
+      const int u = threadIdx.x + TH * i;
       const int row = u / (W / 8), blk = u % (W / 8);
-      const bool in = row < rows;
       const int tok = reverse ? rows - 1 - row : row;
-      const int off = in ? tok * stride_bytes + blk * (bf16 ? 16 : 32) : 0x7fffff00;
-      r[i][0] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0));
-      if constexpr (WIDE) {
-        r[i][1] = u32x4{0, 0, 0, 0};
-        if (!bf16)
-          r[i][1] = __builtin_bit_cast(
-              u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off + 16, 0, 0));
-      }
+      load_block<WIDE>(rsrc, row < rows ? tok * stride_bytes + blk * (bf16 ? 16 : 32) : kOutside,
+                       bf16, r[i]);
     }
   }
   __device__ __forceinline__ void write(char* lds, bool bf16) const {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      const int u = threadIdx.x + NTHR * i;
+      const int u = threadIdx.x + TH * i;
       const int row = u / (W / 8), blk = u % (W / 8);
       char* p = lds + row * (W * 2) + ((blk ^ swz<W>(row)) << 4);
-      if constexpr (WIDE) {
-        f32x8 x;
-        if (bf16) {
-          x = widen8(__builtin_bit_cast(bf16x8, r[i][0]));
-        } else {
-          const f32x4 lo = __builtin_bit_cast(f32x4, r[i][0]), hi = __builtin_bit_cast(f32x4, r[i][1]);
-          x = f32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        }
-        bf16x8 pl[3];
-        split8<3>(x, pl);
+      bf16x8 pl[WIDE ? 3 : 1];
+      planes_of<WIDE>(r[i], bf16, pl);
 #pragma unroll
-        for (int k = 0; k < 3; ++k) *reinterpret_cast<bf16x8*>(p + k * (C * W * 2)) = pl[k];
-      } else {
-        *reinterpret_cast<u32x4*>(p) = r[i][0];
-      }
+      for (int k = 0; k < (WIDE ? 3 : 1); ++k)
+        *reinterpret_cast<bf16x8*>(p + k * (C * W * 2)) = pl[k];
     }
   }
 };
 
 // Buffer over the chunk's rows [tok0, tok0 + rows) of head h (a null tensor is zeros).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const Operand& o, int64_t tok0, int rows,
-                                                          int h, int d, int col0, int cols) {
-  const int es = o.bf16 ? 2 : 4;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const Operand& o, bool bf16,
+                                                          int64_t tok0, int rows, int h, int d,
+                                                          int col0, int cols) {
+  const int es = bf16 ? 2 : 4;
   const char* p = static_cast<const char*>(o.p) +
                   (tok0 * o.stride + (int64_t)(h / o.group) * d + col0) * es;
   return buffer_over(p, rows > 0 && o.p ? (uint32_t)(((rows - 1) * o.stride + cols) * es) : 0);
 }
 
-// FULL: out, dots and the states; else only the segment's own state and decay.
-// DOTS: the backward's walks.
+// FULL: out, dots and the states; else (state waves only) the segment's own
+// state and decay.  DOTS: the backward's walks.
 template <bool WIDE, int KD, bool FULL, bool DOTS>
-__global__ void __launch_bounds__(NTHR, 1) walk_kernel(Args A) {
+__global__ void __launch_bounds__(FULL ? 2 * NTHR : NTHR, 1) walk_kernel(Args A) {
   using L = Lds<WIDE, KD>;
-  constexpr int NPL = L::NPL;
-  constexpr int NPP = WIDE ? 3 : 2, NPS = WIDE ? 3 : 2, NPC = 3;
+  constexpr int TH = FULL ? 2 * NTHR : NTHR;
+  constexpr int NPL = L::NPL, NPS = L::NPS;
+  constexpr int NPP = WIDE ? 3 : 2, NPC = 3;
   constexpr int KK = KD / 32;   // contraction steps over the channels
   constexpr int NT = KD / 16;   // state tiles a wave
-  __shared__ __attribute__((aligned(16))) char lds[L::NBUF * L::buf];
-  __shared__ __attribute__((aligned(16))) char s_p[FULL ? UNITS * 1024 * NPP : 16];
+  constexpr int JT = CT / 16;   // column tiles
+  __shared__ __attribute__((aligned(16))) char lds[FULL ? L::total : L::off_s];
   __shared__ __attribute__((aligned(16))) float s_gh[2][C], s_gl[2][C], s_row[2][C], s_col[2][C];
-  __shared__ float s_diag[C];
   __shared__ float s_end[2];
   __shared__ int s_seq[1];
 
@@ -249,11 +276,12 @@ __global__ void __launch_bounds__(NTHR, 1) walk_kernel(Args A) {
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lane = tid & 63, lr = lane & 15, lg = lane >> 4;
   const bool rev = W.reverse;
+  const bool a_bf = !WIDE || W.a.bf16, b_bf = !WIDE || W.b.bf16, c_bf = !WIDE || W.c.bf16;
 
   // ---- blockIdx.x -> (sequence, segment, head, tile): the tiles of a head on one XCD
   const int CD = static_cast<int>(W.s_elems / KD);
   const int ntile = CD / CT;
-  int id = blockIdx.x >> 3;
+  const int id = blockIdx.x >> 3;
   const int tile = id % ntile;
   const int64_t pair = (int64_t)(id / ntile) * 8 + (blockIdx.x & 7);
   if (pair >= (int64_t)A.N * A.nseg * A.H) return;
@@ -268,25 +296,24 @@ __global__ void __launch_bounds__(NTHR, 1) walk_kernel(Args A) {
   if (A.nseg > 1) {
     c_lo = seg * A.seg_chunks;
     c_hi = c_lo + A.seg_chunks < nch_all ? c_lo + A.seg_chunks : nch_all;
-    if (c_lo >= c_hi) {
-      // a sequence without tokens still hands its entry state on (scan kernel)
-      return;
-    }
+    if (c_lo >= c_hi) return;  // nothing here (scan_kernel hands empty sequences' states on)
   }
   const int nch = c_hi - c_lo;
   const int64_t slot0 = seg_slot(A, n, bos);
-  const int col = tile * CT + 16 * w + lr;  // this lane's column of S
+  const bool state_wave = !FULL || w < 4;
+  const int col = tile * CT + 16 * (w & 3) + lr;  // a state wave's lane: its column of S
+
+  auto channel = [&](int t) { return 32 * (t >> 1) + 8 * lg + 4 * (t & 1); };
+  // a segment's states in the workspace: fp32, tile by tile in this lane's order
+  auto seg_at = [&](float* base, int64_t slot) {
+    return base + ((slot * A.H + h) * ntile + tile) * (int64_t)(KD * CT) + ((w & 3) * 64 + lane) * 4;
+  };
 
   // ---- entry state
   f32x4 S[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto channel = [&](int t) { return 32 * (t >> 1) + 8 * lg + 4 * (t & 1); };
-  // a segment's states in the workspace: fp32, tile by tile in this lane's order
-  auto seg_at = [&](float* base, int64_t slot) {
-    return base + ((slot * A.H + h) * ntile + tile) * (int64_t)(KD * CT) + (w * 64 + lane) * 4;
-  };
-  if constexpr (FULL) {
+  if (FULL && state_wave) {
     if (A.nseg > 1) {
       const float* p = seg_at(W.seg_state, slot0 + seg);
 #pragma unroll
@@ -303,35 +330,58 @@ __global__ void __launch_bounds__(NTHR, 1) walk_kernel(Args A) {
       }
     }
   }
+  // the state's planes, as the left operands of S^T a^T: unit (column tile, kk), 16 bytes a lane
+  auto write_state = [&](int sbuf) {
+    if constexpr (FULL) {
+      char* p = lds + L::off_s + sbuf * (NPS * L::SS) + (w & 3) * (KK * 1024) + lane * 16;
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        const f32x4 t0 = S[2 * kk], t1 = S[2 * kk + 1];
+        bf16x8 f[NPS];
+        split8<NPS>(f32x8{t0[0], t0[1], t0[2], t0[3], t1[0], t1[1], t1[2], t1[3]}, f);
+#pragma unroll
+        for (int k = 0; k < NPS; ++k) *reinterpret_cast<bf16x8*>(p + k * L::SS + kk * 1024) = f[k];
+      }
+    }
+  };
 
-  Stage<WIDE, KD> ra, rb;
-  Stage<WIDE, CT> rc;
-  const int sa = (int)(W.a.stride * (W.a.bf16 ? 2 : 4)), sb = (int)(W.b.stride * (W.b.bf16 ? 2 : 4)),
-            sc = (int)(W.c.stride * (W.c.bf16 ? 2 : 4));
+  Stage<WIDE, KD, TH> rb;
+  Stage<WIDE, CT, TH> rc;
+  const int sa = (int)(W.a.stride * (a_bf ? 2 : 4)), sb = (int)(W.b.stride * (b_bf ? 2 : 4)),
+            sc = (int)(W.c.stride * (c_bf ? 2 : 4));
   auto chunk_of = [&](int it) { return rev ? c_hi - 1 - it : c_lo + it; };
   auto rows_in = [&](int c) { return len - c * C < C ? len - c * C : C; };
   auto load_chunk = [&](int c) {
     const int rows = rows_in(c);
     const int64_t tok0 = (int64_t)bos + c * C;
-    if constexpr (FULL) ra.load(rows_of(W.a, tok0, rows, h, KD, 0, KD), sa, W.a.bf16, rows, rev);
-    rb.load(rows_of(W.b, tok0, rows, h, KD, 0, KD), sb, W.b.bf16, rows, rev);
-    rc.load(rows_of(W.c, tok0, rows, h, CD, tile * CT, CT), sc, W.c.bf16, rows, rev);
+    rb.load(rows_of(W.b, b_bf, tok0, rows, h, KD, 0, KD), sb, b_bf, rows, rev);
+    rc.load(rows_of(W.c, c_bf, tok0, rows, h, CD, tile * CT, CT), sc, c_bf, rows, rev);
   };
   auto write_chunk = [&](int buf) {
     char* p = lds + buf * L::buf;
-    if constexpr (FULL) ra.write(p + L::off_a, W.a.bf16);
-    rb.write(p + L::off_b, W.b.bf16);
-    rc.write(p + L::off_c, W.c.bf16);
+    rb.write(p, b_bf);
+    rc.write(p + L::off_c, c_bf);
+  };
+  // output wave i: its row of a, the token of that row
+  const int orow = 16 * (w & 3) + lr;
+  u32x4 ra[KK][WIDE ? 2 : 1], ra_next[KK][WIDE ? 2 : 1];
+  auto load_a = [&](int c, u32x4 (&r4)[KK][WIDE ? 2 : 1]) {
+    const int rows = rows_in(c);
+    const __amdgpu_buffer_rsrc_t r = rows_of(W.a, a_bf, (int64_t)bos + c * C, rows, h, KD, 0, KD);
+    const int tok = rev ? rows - 1 - orow : orow;
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk)
+      load_block<WIDE>(r, orow < rows ? tok * sa + (4 * kk + lg) * (a_bf ? 16 : 32) : kOutside,
+                       a_bf, r4[kk]);
   };
   // log2-decay of row `lane` of chunk c (rows past the chunk: 0).  Walking
   // backwards, token t's decay is that of t + 1 and the last token's is 0.
   auto load_decay = [&](int c) -> float {
     const int rows = rows_in(c);
     if (lane >= rows) return 0.f;
-    const int t = c * C + (rev ? rows - 1 - lane : lane) + (rev ? 1 : 0);
+    const int t = c * C + (rev ? rows - lane : lane);
     if (t >= len) return 0.f;
-    const float g = A.g.g[A.g.per_token ? ((int64_t)bos + t) * A.H + h : h];
-    return clamp_log_decay(g);
+    return clamp_log_decay(A.g.g[A.g.per_token ? ((int64_t)bos + t) * A.H + h : h]);
   };
   // the chunk's decays (one wave): gamma as two floats, row and column factors
   double seg_sum = 0.0;
@@ -351,67 +401,134 @@ __global__ void __launch_bounds__(NTHR, 1) walk_kernel(Args A) {
     if (lane == 0) s_end[buf] = ex2((float)end);
     seg_sum += end;
   };
+  constexpr int kDecayWave = FULL ? 4 : 3;  // output wave 0 has the fewest scores
 
   // lane constants of the LDS reads
-  const int swA = swz<KD>(lr);                       // row reads: rows 16 i + lr
+  const int swB = swz<KD>(lr);                       // row reads: rows 16 i + lr
   const int tj = 4 * lg + (lr >> 2);                 // transposed reads: row of a token tile
-  const int swB = swz<KD>(tj), swC = swz<CT>(tj);
+  const int twB = swz<KD>(tj), twC = swz<CT>(tj);
   const int pc = lr & 3;
+  // c^T of column tile j, tokens of step ks
+  auto read_c = [&](const char* bc, int j, int ks, bf16x8 (&f)[NPL]) {
+    const int r0 = 32 * ks + tj, r1 = r0 + 16;
+    const int cb = (((2 * j + (pc >> 1)) ^ twC) << 4) + ((pc & 1) << 3);
+#pragma unroll
+    for (int p = 0; p < NPL; ++p)
+      f[p] = read_tr2(bc + p * L::CC + r0 * (CT * 2) + cb, bc + p * L::CC + r1 * (CT * 2) + cb);
+  };
 
   float gnext = 0.f;
   if (nch > 0) {
     load_chunk(chunk_of(0));
-    if (w == 3) {
+    if (FULL && !state_wave) load_a(chunk_of(0), ra);
+    if (w == kDecayWave) {
       decays(load_decay(chunk_of(0)), 0);
       if (nch > 1) gnext = load_decay(chunk_of(1));
     }
+    write_chunk(0);
+    if (nch > 1) load_chunk(chunk_of(1));
+    if (state_wave) write_state(0);
   }
-  const int out_es = W.out_bf16 ? 2 : 4;
 
   for (int it = 0; it < nch; ++it) {
     const int c = chunk_of(it);
     const int rows = rows_in(c);
-    const int buf = L::NBUF == 2 ? (it & 1) : 0;
     const int gb = it & 1;
-    const char* ba = lds + buf * L::buf + L::off_a;
-    const char* bb = lds + buf * L::buf + L::off_b;
-    const char* bc = lds + buf * L::buf + L::off_c;
-    if constexpr (L::NBUF == 1) {
-      if (it) barrier_lds();  // everyone has read the chunk before
-    }
-    write_chunk(buf);
-    if (it + 1 < nch) load_chunk(chunk_of(it + 1));
-    if constexpr (FULL && DOTS) {
-      // states at the segments' ends, for dg: the forward walk after the last
-      // chunk of a segment (below), the backward ones before it
-      if (W.ends && rev && ((c + 1) % A.seg_chunks == 0 || c + 1 == nch_all)) {
-        float* p = seg_at(W.ends, slot0 + c / A.seg_chunks);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(p + t * (NTHR * 4)) = S[t];
-      }
-    }
-    barrier_lds();
+    const int buf = L::NBUF == 2 ? gb : 0;
+    const char* bb = lds + buf * L::buf;
+    const char* bc = bb + L::off_c;
+    barrier_lds();  // chunk `it` and its entry state are in LDS, chunk it - 1 has been read
 
-    f32x4 acc[4];
-    if constexpr (FULL) {
-      // ---- scores: wave 0 (3,0), wave 1 (3,1), wave 2 (2,0) (2,1), wave 3 (1,0) (0,0)
-      auto unit = [&](int i, int ks, bool two, int slot) {
+    if (state_wave) {
+      if constexpr (FULL && DOTS) {
+        // states at the segments' ends, for dg: the forward walk after the last
+        // chunk of a segment (below), the backward ones before it
+        if (W.ends && rev && ((c + 1) % A.seg_chunks == 0 || c + 1 == nch_all)) {
+          float* p = seg_at(W.ends, slot0 + c / A.seg_chunks);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(p + t * (NTHR * 4)) = S[t];
+        }
+      }
+      // ---- S <- e^gamma_end S + b^T (decayed c)
+      const float dec = s_end[gb];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) S[t] *= dec;
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        bf16x8 fc[NPL];
+        read_c(bc, w & 3, ks, fc);
+        f32x8 x = widen8(fc[0]);
+#pragma unroll
+        for (int p = 1; p < NPL; ++p) x += widen8(fc[p]);
+        const f32x4 e0 = *reinterpret_cast<const f32x4*>(&s_col[gb][32 * ks + 4 * lg]);
+        const f32x4 e1 = *reinterpret_cast<const f32x4*>(&s_col[gb][32 * ks + 16 + 4 * lg]);
+        x *= f32x8{e0[0], e0[1], e0[2], e0[3], e1[0], e1[1], e1[2], e1[3]};
+        bf16x8 fx[NPC];
+        split8<NPC>(x, fx);
+        const int r0 = 32 * ks + tj, r1 = r0 + 16;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const int at = (((4 * (t >> 1) + pc) ^ twB) << 4) + ((t & 1) << 3);
+          bf16x8 fb[NPL];
+#pragma unroll
+          for (int p = 0; p < NPL; ++p)
+            fb[p] = read_tr2(bb + p * L::BB + r0 * (KD * 2) + at, bb + p * L::BB + r1 * (KD * 2) + at);
+          mma_planes<NPL, NPC>(fb, fx, S[t]);
+        }
+      }
+      if constexpr (FULL && DOTS) {
+        if (W.ends && !rev && ((c + 1) % A.seg_chunks == 0 || c + 1 == nch_all)) {
+          float* p = seg_at(W.ends, slot0 + c / A.seg_chunks);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(p + t * (NTHR * 4)) = S[t];
+        }
+      }
+    } else if constexpr (FULL) {
+      const int i = w & 3;  // row tile
+      const int64_t tok0 = (int64_t)bos + c * C;
+      const int tok = rev ? rows - 1 - orow : orow;
+      bf16x8 fa[KK][NPL];
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) planes_of<WIDE>(ra[kk], a_bf, fa[kk]);
+      if (it + 1 < nch) load_a(chunk_of(it + 1), ra_next);
+      u32x4 xr[JT];  // x of this lane's row, for the dots
+      if constexpr (DOTS) {
+        if (W.dots) {
+          const __amdgpu_buffer_rsrc_t r = rows_of(W.x, W.x.bf16, tok0, rows, h, CD, tile * CT, CT);
+          const int xs = (int)(W.x.stride * (W.x.bf16 ? 2 : 4));
+#pragma unroll
+          for (int j = 0; j < JT; ++j) {
+            if (W.x.bf16) {
+              const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(
+                  r, orow < rows ? tok * xs + (16 * j + 4 * lg) * 2 : kOutside, 0, 0));
+              xr[j] = u32x4{v[0], v[1], 0, 0};
+            } else {
+              xr[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                  r, orow < rows ? tok * xs + (16 * j + 4 * lg) * 4 : kOutside, 0, 0));
+            }
+          }
+        }
+      }
+      // ---- scores of row tile i against the tokens 0 .. 16i + 15, transposed
+      bf16x8 fp[2][NPP];
+      float diag = 0.f;
+      const float rh = s_gh[gb][orow], rl = s_gl[gb][orow];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        if (2 * ks > i) continue;
         f32x4 p0 = {0.f, 0.f, 0.f, 0.f}, p1 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
-          const int blk = ((4 * kk + lg) ^ swA) << 4;
-          bf16x8 fa[NPL], f0[NPL], f1[NPL];
+          const int blk = ((4 * kk + lg) ^ swB) << 4;
+          bf16x8 f0[NPL], f1[NPL];
 #pragma unroll
           for (int p = 0; p < NPL; ++p) {
-            fa[p] = *reinterpret_cast<const bf16x8*>(ba + p * L::AB + (16 * i + lr) * (KD * 2) + blk);
-            f0[p] = *reinterpret_cast<const bf16x8*>(bb + p * L::AB + (32 * ks + lr) * (KD * 2) + blk);
-            f1[p] = *reinterpret_cast<const bf16x8*>(bb + p * L::AB + (32 * ks + 16 + lr) * (KD * 2) + blk);
+            f0[p] = *reinterpret_cast<const bf16x8*>(bb + p * L::BB + (32 * ks + lr) * (KD * 2) + blk);
+            f1[p] = *reinterpret_cast<const bf16x8*>(bb + p * L::BB + (32 * ks + 16 + lr) * (KD * 2) + blk);
           }
-          mma_planes<NPL, NPL>(f0, fa, p0);
-          if (two) mma_planes<NPL, NPL>(f1, fa, p1);
+          mma_planes<NPL, NPL>(f0, fa[kk], p0);
+          mma_planes<NPL, NPL>(f1, fa[kk], p1);  // masked where it lies behind the rows
         }
-        const int r = 16 * i + lr;
-        const float rh = s_gh[gb][r], rl = s_gl[gb][r];
         f32x8 pv;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -423,171 +540,107 @@ __global__ void __launch_bounds__(NTHR, 1) walk_kernel(Args A) {
           for (int e = 0; e < 4; ++e) {
             const float x = v[e] * A.scale * ex2((rh - sh[e]) + (rl - sl[e]));
             if constexpr (DOTS) {
-              if (s0 + e == r) s_diag[r] = x;
-              pv[4 * half + e] = (W.dots ? s0 + e < r : s0 + e <= r) ? x : 0.f;
+              if (s0 + e == orow) diag = x;
+              pv[4 * half + e] = (W.dots ? s0 + e < orow : s0 + e <= orow) ? x : 0.f;
             } else {
-              pv[4 * half + e] = s0 + e <= r ? x : 0.f;
+              pv[4 * half + e] = s0 + e <= orow ? x : 0.f;
             }
           }
         }
-        bf16x8 pl[NPP];
-        split8<NPP>(pv, pl);
-#pragma unroll
-        for (int p = 0; p < NPP; ++p)
-          *reinterpret_cast<bf16x8*>(s_p + (p * UNITS + slot) * 1024 + lane * 16) = pl[p];
-      };
-      if (w == 0) {
-        unit(3, 0, true, 4);
-      } else if (w == 1) {
-        unit(3, 1, true, 5);
-      } else if (w == 2) {
-        unit(2, 0, true, 2);
-        unit(2, 1, false, 3);
-      } else {
-        unit(1, 0, true, 1);
-        unit(0, 0, false, 0);
+        split8<NPP>(pv, fp[ks]);
       }
-      // ---- out^T = S^T a^T, then its rows' decay
+      // ---- out^T = S^T a^T, the rows' decay, + c^T P^T
+      f32x4 acc[JT];
+      const float rowf = s_row[gb][orow];
+      const char* sp = lds + L::off_s + buf * (NPS * L::SS) + lane * 16;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < JT; ++j) {
+        acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        const f32x4 t0 = S[2 * kk], t1 = S[2 * kk + 1];
-        bf16x8 fs[NPS];
-        split8<NPS>(f32x8{t0[0], t0[1], t0[2], t0[3], t1[0], t1[1], t1[2], t1[3]}, fs);
-        const int blk = ((4 * kk + lg) ^ swA) << 4;
+        for (int kk = 0; kk < KK; ++kk) {
+          bf16x8 fs[NPS];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          bf16x8 fa[NPL];
+          for (int k = 0; k < NPS; ++k)
+            fs[k] = *reinterpret_cast<const bf16x8*>(sp + k * L::SS + (j * KK + kk) * 1024);
+          mma_planes<NPS, NPL>(fs, fa[kk], acc[j]);
+        }
+        acc[j] *= rowf;
+      }
 #pragma unroll
-          for (int p = 0; p < NPL; ++p)
-            fa[p] = *reinterpret_cast<const bf16x8*>(ba + p * L::AB + (16 * i + lr) * (KD * 2) + blk);
-          mma_planes<NPS, NPL>(fs, fa, acc[i]);
+      for (int ks = 0; ks < 2; ++ks) {
+        if (2 * ks > i) continue;
+#pragma unroll
+        for (int j = 0; j < JT; ++j) {
+          bf16x8 fc[NPL];
+          read_c(bc, j, ks, fc);
+          mma_planes<NPL, NPP>(fc, fp[ks], acc[j]);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] *= s_row[gb][16 * i + lr];
-      barrier_lds();
-    }
-
-    // ---- out^T += c^T P^T;  S <- e^gamma_end S + b^T (decayed c)
-    {
-      const float dec = s_end[gb];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) S[t] *= dec;
-    }
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      const int r0 = 32 * ks + tj, r1 = r0 + 16;
-      bf16x8 fc[NPL];
-      const int cb = (((2 * w + (pc >> 1)) ^ swC) << 4) + ((pc & 1) << 3);
-#pragma unroll
-      for (int p = 0; p < NPL; ++p)
-        fc[p] = read_tr2(bc + p * L::CC + r0 * (CT * 2) + cb, bc + p * L::CC + r1 * (CT * 2) + cb);
-      if constexpr (FULL) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (2 * ks > i) continue;  // tokens behind row tile i
-          const int slot = i < 2 ? i : 2 * i - 2 + ks;
-          bf16x8 fp[NPP];
-#pragma unroll
-          for (int p = 0; p < NPP; ++p)
-            fp[p] = *reinterpret_cast<const bf16x8*>(s_p + (p * UNITS + slot) * 1024 + lane * 16);
-          mma_planes<NPL, NPP>(fc, fp, acc[i]);
-        }
-      }
-      // the decayed c
-      f32x8 x = widen8(fc[0]);
-#pragma unroll
-      for (int p = 1; p < NPL; ++p) x += widen8(fc[p]);
-      const f32x4 e0 = *reinterpret_cast<const f32x4*>(&s_col[gb][32 * ks + 4 * lg]);
-      const f32x4 e1 = *reinterpret_cast<const f32x4*>(&s_col[gb][32 * ks + 16 + 4 * lg]);
-      x *= f32x8{e0[0], e0[1], e0[2], e0[3], e1[0], e1[1], e1[2], e1[3]};
-      bf16x8 fx[NPC];
-      split8<NPC>(x, fx);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int at = (((4 * (t >> 1) + pc) ^ swB) << 4) + ((t & 1) << 3);
-        bf16x8 fb[NPL];
-#pragma unroll
-        for (int p = 0; p < NPL; ++p)
-          fb[p] = read_tr2(bb + p * L::AB + r0 * (KD * 2) + at, bb + p * L::AB + r1 * (KD * 2) + at);
-        mma_planes<NPL, NPC>(fb, fx, S[t]);
-      }
-    }
-    // the next chunk's decays, by the wave with the fewest scores
-    if (w == 3 && it + 1 < nch) {
-      decays(gnext, gb ^ 1);
-      if (it + 2 < nch) gnext = load_decay(chunk_of(it + 2));
-    }
-
-    if constexpr (FULL) {
-      const int64_t tok0 = (int64_t)bos + c * C;
-      const int64_t ld = (int64_t)A.H * CD;
       if constexpr (DOTS) {
         if (W.dots) {
-          // x_t . out_t over this wave's columns, then the pair (t, t)
-          const __amdgpu_buffer_rsrc_t xr = rows_of(W.x, tok0, rows, h, CD, 0, CD);
-          const int xs = (int)(W.x.stride * (W.x.bf16 ? 2 : 4));
+          // x_t . out_t over the tile's columns, then the pair (t, t)
+          float dot = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = 16 * i + lr;
-            const int tok = rev ? rows - 1 - row : row;
-            const int xc = tile * CT + 16 * w + 4 * lg;
-            f32x4 xv = {0.f, 0.f, 0.f, 0.f};
+          for (int j = 0; j < JT; ++j) {
+            f32x4 xv = __builtin_bit_cast(f32x4, xr[j]);
             if (W.x.bf16) {
-              const int off = row < rows ? tok * xs + xc * 2 : 0x7fffff00;
-              typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-              const u16x4 b = __builtin_bit_cast(
-                  u16x4, __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(xr, off, 0, 0)));
-              xv = f32x4{bf16_bits_to_f32(b[0]), bf16_bits_to_f32(b[1]), bf16_bits_to_f32(b[2]),
-                         bf16_bits_to_f32(b[3])};
-            } else {
-              const int off = row < rows ? tok * xs + xc * 4 : 0x7fffff00;
-              xv = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, off, 0, 0));
+              xv = f32x4{__uint_as_float(xr[j][0] << 16), __uint_as_float(xr[j][0] & 0xffff0000u),
+                         __uint_as_float(xr[j][1] << 16), __uint_as_float(xr[j][1] & 0xffff0000u)};
             }
-            float dot = xv[0] * acc[i][0] + xv[1] * acc[i][1] + xv[2] * acc[i][2] + xv[3] * acc[i][3];
-            dot += __shfl_xor(dot, 16);
-            dot += __shfl_xor(dot, 32);
-            if (lg == 0 && row < rows)
-              W.dots[((tok0 + tok) * A.H + h) * 8 + tile * 4 + w] = dot;
-            // + P[t,t] c_t
-            const float pd = s_diag[row];
-            const int cc = 16 * w + 4 * lg;
-            const char* cp = bc + row * (CT * 2) + (((cc >> 3) ^ swz<CT>(row)) << 4) + ((cc & 7) << 1);
+            dot += (xv[0] * acc[j][0] + xv[1] * acc[j][1]) + (xv[2] * acc[j][2] + xv[3] * acc[j][3]);
+          }
+          dot += __shfl_xor(dot, 16);
+          dot += __shfl_xor(dot, 32);
+          if (lg == 0 && orow < rows) W.dots[((tok0 + tok) * A.H + h) * 2 + tile] = dot;
+          // + P[t,t] c_t: the lane that holds the pair hands it to the others of its row
+          const float pd = __shfl(diag, lr + 16 * (lr >> 2));
+#pragma unroll
+          for (int j = 0; j < JT; ++j) {
+            const int cc = 16 * j + 4 * lg;
+            const char* cp = bc + orow * (CT * 2) + (((cc >> 3) ^ swz<CT>(orow)) << 4) + ((cc & 7) << 1);
 #pragma unroll
             for (int p = 0; p < NPL; ++p) {
               const u16x4 b = *reinterpret_cast<const u16x4*>(cp + p * L::CC);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[i][e] += pd * bf16_bits_to_f32(b[e]);
+              for (int e = 0; e < 4; ++e) acc[j][e] += pd * bf16_bits_to_f32(b[e]);
             }
           }
         }
       }
-      const __amdgpu_buffer_rsrc_t orow =
-          buffer_over(static_cast<char*>(W.out) + (tok0 * ld + (int64_t)h * CD) * out_es,
-                      (uint32_t)(((rows - 1) * ld + CD) * out_es));
-      const int oc = tile * CT + 16 * w + 4 * lg;
+      const int64_t ld = (int64_t)A.H * CD;
+      const int out_es = W.out_bf16 ? 2 : 4;
+      const __amdgpu_buffer_rsrc_t ow =
+          buffer_over(static_cast<char*>(W.out) + (tok0 * ld + (int64_t)h * CD + tile * CT) * out_es,
+                      (uint32_t)(((rows - 1) * ld + CT) * out_es));
+      const int off0 = (int)((tok * ld + 4 * lg) * out_es);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 16 * i + lr;
-        const int tok = rev ? rows - 1 - row : row;
-        const int off = row < rows ? (int)((tok * ld + oc) * out_es) : 0x7fffff00;
+      for (int j = 0; j < JT; ++j) {
+        const int off = orow < rows ? off0 + 16 * j * out_es : kOutside;
         if (W.out_bf16) {
-          const u16x4 b = {f32_to_bf16_bits(acc[i][0]), f32_to_bf16_bits(acc[i][1]),
-                           f32_to_bf16_bits(acc[i][2]), f32_to_bf16_bits(acc[i][3])};
-          typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, b), orow, off, 0, 0);
+          const u16x4 b = {f32_to_bf16_bits(acc[j][0]), f32_to_bf16_bits(acc[j][1]),
+                           f32_to_bf16_bits(acc[j][2]), f32_to_bf16_bits(acc[j][3])};
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, b), ow, off, 0, 0);
         } else {
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i]), orow, off, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[j]), ow, off, 0, 0);
         }
       }
-      if constexpr (DOTS) {
-        if (W.ends && !rev && ((c + 1) % A.seg_chunks == 0 || c + 1 == nch_all)) {
-          float* p = seg_at(W.ends, slot0 + c / A.seg_chunks);
+    }
+
+    // ---- the next chunk into LDS, the one after it on its way
+    if (it + 1 < nch) {
+      if constexpr (L::NBUF == 1) barrier_lds();  // chunk `it` has been read
+      if (state_wave) write_state(L::NBUF == 2 ? gb ^ 1 : 0);
+      write_chunk(L::NBUF == 2 ? gb ^ 1 : 0);
+      if (FULL && !state_wave) {
 #pragma unroll
-          for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(p + t * (NTHR * 4)) = S[t];
-        }
+        for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+          for (int e = 0; e < (WIDE ? 2 : 1); ++e) ra[kk][e] = ra_next[kk][e];
+      }
+      if (it + 2 < nch) load_chunk(chunk_of(it + 2));
+      if (w == kDecayWave) {
+        decays(gnext, gb ^ 1);
+        if (it + 2 < nch) gnext = load_decay(chunk_of(it + 2));
       }
     }
   }
@@ -596,8 +649,9 @@ __global__ void __launch_bounds__(NTHR, 1) walk_kernel(Args A) {
     float* p = seg_at(W.seg_state, slot0 + seg);
 #pragma unroll
     for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(p + t * (NTHR * 4)) = S[t];
-    if (w == 3 && lane == 0 && tile == 0) W.seg_decay[(slot0 + seg) * A.H + h] = (float)seg_sum;
-  } else if (A.nseg == 1 && W.s_out) {
+    if (w == kDecayWave && lane == 0 && tile == 0)
+      W.seg_decay[(slot0 + seg) * A.H + h] = (float)seg_sum;
+  } else if (state_wave && A.nseg == 1 && W.s_out) {
     const int64_t sl = W.out_idx ? (int64_t)W.out_idx[n] : n;
     if (sl >= 0 && sl < W.out_slots) {
       // walking backwards, the state before the first token has its decay too
@@ -723,21 +777,14 @@ __global__ void __launch_bounds__(NTHR) dg_kernel(Args A, const float* dotq, con
     const float g = A.g.g[A.g.per_token ? ((int64_t)bos + t_hi) * A.H + h : h];
     run *= exp((double)clamp_log_decay(g));
   }
-  const int nq = dk / 16, nk = dk / 16;  // partial dots a token: one a wave
   double total = 0.0;
   for (int hi = t_hi; hi > t_lo; hi -= NTHR) {
     const int t = hi - 1 - tid;
     double x = 0.0;
-    if (t >= t_lo) {
-      const int64_t at = (((int64_t)bos + t) * A.H + h) * 8;
-      const f32x4 q0 = *reinterpret_cast<const f32x4*>(dotq + at);
-      const f32x4 k0 = *reinterpret_cast<const f32x4*>(dotk + at);
-      f32x4 q1 = {0.f, 0.f, 0.f, 0.f}, k1 = {0.f, 0.f, 0.f, 0.f};
-      if (nq > 4) q1 = *reinterpret_cast<const f32x4*>(dotq + at + 4);
-      if (nk > 4) k1 = *reinterpret_cast<const f32x4*>(dotk + at + 4);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        x += ((double)q0[e] - (double)k0[e]) + ((double)q1[e] - (double)k1[e]);
+    if (t >= t_lo) {  // one partial dot a column tile of 64 channels
+      const int64_t at = (((int64_t)bos + t) * A.H + h) * 2;
+      x = (double)dotq[at] - (double)dotk[at];
+      if (dk > CT) x += (double)dotq[at + 1] - (double)dotk[at + 1];
     }
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -821,7 +868,8 @@ hipError_t launch_walk_kd(const Args& A, int walks, hipStream_t s) {
   const int64_t blocks =
       cdiv((int64_t)A.N * A.nseg * A.H, 8) * 8 * (A.walk[0].s_elems / KD / CT);
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  walk_kernel<WIDE, KD, FULL, DOTS><<<dim3((unsigned)blocks, walks), NTHR, 0, s>>>(A);
+  walk_kernel<WIDE, KD, FULL, DOTS><<<dim3((unsigned)blocks, walks),
+                                      FULL ? 2 * NTHR : NTHR, 0, s>>>(A);
   return hipGetLastError();
 }
 // `walks` walks of one contraction width kd
@@ -889,8 +937,8 @@ struct BackwardWs {
   BackwardWs(void* ws, int64_t T_tot, int N, int H, int Hk, int dk, int dv, int seg, bool cut) {
     Carve c{static_cast<char*>(ws)};
     const int64_t slots = slots_of(T_tot, N, seg), st = slots * H * dk * dv;
-    dotq = c.take(T_tot * H * 8);
-    dotk = c.take(T_tot * H * 8);
+    dotq = c.take(T_tot * H * 2);
+    dotk = c.take(T_tot * H * 2);
     ends_s = c.take(st);
     ends_d = c.take(st);
     dg_part = c.take(slots * H * 2);
