@@ -28,7 +28,7 @@
 // of the sums over all later tokens (dg_kernel).
 //
 // Workgroup: 64 columns of c (and so of S and out) of one (sequence, head),
-// eight waves of two kinds, one of each kind on every SIMD:
+// waves of four kinds, each with a loop of its own over the chunks:
 //   state waves   wave w owns columns 16w .. 16w+15 of S in MFMA accumulators.
 //                 Per chunk it adds b^T (decayed c) and leaves the new state's
 //                 bf16 values in LDS as the operands of the next readout.
@@ -36,8 +36,13 @@
 //                 tokens up to its rows, S^T a^T, c^T P^T and the stores.  a goes
 //                 from global memory straight to its registers, and the scores
 //                 never leave them.
-// S is the only thing handed over.  With it, b and c double-buffered in LDS the
-// two kinds need one barrier a chunk.
+//   copy wave     brings b and c of the chunk after the next into LDS
+//                 (three buffers) and touches nothing else, so that its loads
+//                 are waited for in the copy wave alone.
+//   decay wave    the next chunk's decays.
+// S is the only thing handed between the kinds, so one barrier a chunk is
+// enough.  (fp32 operands: the state waves copy, because each value is split
+// into three, with one buffer and a second barrier.)
 // What bounds it: the sequential walk.  A layer of 96 heads gives 192
 // workgroups for 256 CUs, each with T / 64 chunks to go through, so the time is
 // chunks x the latency of one chunk until HBM is reached.  LDS carries the most
@@ -173,14 +178,23 @@ template <bool WIDE, int KD>
 struct Lds {
   static constexpr int NPL = WIDE ? 3 : 1;          // planes of an operand
   static constexpr int NPS = WIDE ? 3 : 2;          // planes of the state
-  static constexpr int NBUF = WIDE ? 1 : 2;
+  static constexpr int NBUF = WIDE ? 1 : 3;         // chunks of b and c
+  static constexpr int NSB = WIDE ? 1 : 2;          // states
   static constexpr int BB = C * KD * 2;             // one plane of b
   static constexpr int CC = C * CT * 2;             // one plane of c
   static constexpr int SS = KD * CT * 2;            // one plane of the state
   static constexpr int buf = NPL * (BB + CC);
   static constexpr int off_c = NPL * BB;
   static constexpr int off_s = NBUF * buf;
-  static constexpr int total = off_s + NBUF * NPS * SS;
+  static constexpr int total = off_s + NSB * NPS * SS;
+};
+// Waves of a workgroup: state waves 0 .. 3, then (FULL) output waves, then helpers.
+template <bool WIDE, bool FULL>
+struct Waves {
+  static constexpr int out = 4;                        // first output wave
+  static constexpr int decay = FULL ? 8 : 4;
+  static constexpr int copy = WIDE ? -1 : decay + 1;
+  static constexpr int threads = 64 * (decay + (WIDE ? 1 : 2));
 };
 
 // The eight values of a block as NP bf16 planes.
@@ -255,12 +269,36 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const Operand& o, bool
   return buffer_over(p, rows > 0 && o.p ? (uint32_t)(((rows - 1) * o.stride + cols) * es) : 0);
 }
 
-// FULL: out, dots and the states; else (state waves only) the segment's own
+// Copies 64 rows of W channels of bf16 straight into LDS: 1 KiB an instruction,
+// lane l writes 16 bytes at 16 l, so the swizzle is in which block a lane asks for.
+template <int W>
+__device__ __forceinline__ void copy_rows(__amdgpu_buffer_rsrc_t r, char* dst, int stride_bytes,
+                                          int rows, bool reverse, int lane) {
+  constexpr int BPR = W / 8, RPI = 64 / BPR;  // blocks a row, rows an instruction
+#pragma unroll
+  for (int u = 0; u < C / RPI; ++u) {
+    const int row = u * RPI + lane / BPR;
+    const int blk = (lane % BPR) ^ swz<W>(row);
+    const int tok = reverse ? rows - 1 - row : row;
+    chunk::buf_to_lds16(r, (chunk::lds_ptr_t)(dst + u * 1024),
+                        row < rows ? tok * stride_bytes + blk * 16 : kOutside, 0);
+  }
+}
+// waits until at most N vector-memory operations of this wave are outstanding
+template <int N>
+__device__ __forceinline__ void wait_vm_le() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+  asm volatile("" ::: "memory");
+}
+
+// FULL: out, dots and the states; else (no output waves) the segment's own
 // state and decay.  DOTS: the backward's walks.
 template <bool WIDE, int KD, bool FULL, bool DOTS>
-__global__ void __launch_bounds__(FULL ? 2 * NTHR : NTHR, 1) walk_kernel(Args A) {
+__global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(Args A) {
   using L = Lds<WIDE, KD>;
-  constexpr int TH = FULL ? 2 * NTHR : NTHR;
+  using WV = Waves<WIDE, FULL>;
   constexpr int NPL = L::NPL, NPS = L::NPS;
   constexpr int NPP = WIDE ? 3 : 2, NPC = 3;
   constexpr int KK = KD / 32;   // contraction steps over the channels
@@ -289,6 +327,7 @@ __global__ void __launch_bounds__(FULL ? 2 * NTHR : NTHR, 1) walk_kernel(Args A)
   const int seg = static_cast<int>((pair / A.H) % A.nseg);
   int n = static_cast<int>(pair / A.H / A.nseg);
   if (A.cu) n = chunk::lpt_sequence(A.cu, A.N, A.T_tot, n, s_seq);
+  n = __builtin_amdgcn_readfirstlane(n);
   int bos, len;
   seq_range(A, n, bos, len);
   const int nch_all = (len + C - 1) / C;
@@ -299,113 +338,14 @@ __global__ void __launch_bounds__(FULL ? 2 * NTHR : NTHR, 1) walk_kernel(Args A)
     if (c_lo >= c_hi) return;  // nothing here (scan_kernel hands empty sequences' states on)
   }
   const int nch = c_hi - c_lo;
-  const int64_t slot0 = seg_slot(A, n, bos);
-  const bool state_wave = !FULL || w < 4;
-  const int col = tile * CT + 16 * (w & 3) + lr;  // a state wave's lane: its column of S
-
-  auto channel = [&](int t) { return 32 * (t >> 1) + 8 * lg + 4 * (t & 1); };
-  // a segment's states in the workspace: fp32, tile by tile in this lane's order
-  auto seg_at = [&](float* base, int64_t slot) {
-    return base + ((slot * A.H + h) * ntile + tile) * (int64_t)(KD * CT) + ((w & 3) * 64 + lane) * 4;
-  };
-
-  // ---- entry state
-  f32x4 S[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (FULL && state_wave) {
-    if (A.nseg > 1) {
-      const float* p = seg_at(W.seg_state, slot0 + seg);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) S[t] = *reinterpret_cast<const f32x4*>(p + t * (NTHR * 4));
-    } else if (W.s_in) {
-      const int64_t sl = W.in_idx ? (int64_t)W.in_idx[n] : n;
-      if (sl >= 0 && sl < W.in_slots) {
-        const int64_t base = (sl * A.H + h) * W.s_elems + col * W.s_col;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            S[t][i] = load1(W.s_in, base + (channel(t) + i) * W.s_row, W.in_bf16);
-      }
-    }
-  }
-  // the state's planes, as the left operands of S^T a^T: unit (column tile, kk), 16 bytes a lane
-  auto write_state = [&](int sbuf) {
-    if constexpr (FULL) {
-      char* p = lds + L::off_s + sbuf * (NPS * L::SS) + (w & 3) * (KK * 1024) + lane * 16;
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        const f32x4 t0 = S[2 * kk], t1 = S[2 * kk + 1];
-        bf16x8 f[NPS];
-        split8<NPS>(f32x8{t0[0], t0[1], t0[2], t0[3], t1[0], t1[1], t1[2], t1[3]}, f);
-#pragma unroll
-        for (int k = 0; k < NPS; ++k) *reinterpret_cast<bf16x8*>(p + k * L::SS + kk * 1024) = f[k];
-      }
-    }
-  };
-
-  Stage<WIDE, KD, TH> rb;
-  Stage<WIDE, CT, TH> rc;
-  const int sa = (int)(W.a.stride * (a_bf ? 2 : 4)), sb = (int)(W.b.stride * (b_bf ? 2 : 4)),
-            sc = (int)(W.c.stride * (c_bf ? 2 : 4));
   auto chunk_of = [&](int it) { return rev ? c_hi - 1 - it : c_lo + it; };
   auto rows_in = [&](int c) { return len - c * C < C ? len - c * C : C; };
-  auto load_chunk = [&](int c) {
-    const int rows = rows_in(c);
-    const int64_t tok0 = (int64_t)bos + c * C;
-    rb.load(rows_of(W.b, b_bf, tok0, rows, h, KD, 0, KD), sb, b_bf, rows, rev);
-    rc.load(rows_of(W.c, c_bf, tok0, rows, h, CD, tile * CT, CT), sc, c_bf, rows, rev);
+  // chunk `it` is in buffer it % NBUF
+  auto buf_of = [&](int it) -> char* {
+    return lds + (L::NBUF == 1 ? 0 : (it % L::NBUF) * L::buf);
   };
-  auto write_chunk = [&](int buf) {
-    char* p = lds + buf * L::buf;
-    rb.write(p, b_bf);
-    rc.write(p + L::off_c, c_bf);
-  };
-  // output wave i: its row of a, the token of that row
-  const int orow = 16 * (w & 3) + lr;
-  u32x4 ra[KK][WIDE ? 2 : 1], ra_next[KK][WIDE ? 2 : 1];
-  auto load_a = [&](int c, u32x4 (&r4)[KK][WIDE ? 2 : 1]) {
-    const int rows = rows_in(c);
-    const __amdgpu_buffer_rsrc_t r = rows_of(W.a, a_bf, (int64_t)bos + c * C, rows, h, KD, 0, KD);
-    const int tok = rev ? rows - 1 - orow : orow;
-#pragma unroll
-    for (int kk = 0; kk < KK; ++kk)
-      load_block<WIDE>(r, orow < rows ? tok * sa + (4 * kk + lg) * (a_bf ? 16 : 32) : kOutside,
-                       a_bf, r4[kk]);
-  };
-  // log2-decay of row `lane` of chunk c (rows past the chunk: 0).  Walking
-  // backwards, token t's decay is that of t + 1 and the last token's is 0.
-  auto load_decay = [&](int c) -> float {
-    const int rows = rows_in(c);
-    if (lane >= rows) return 0.f;
-    const int t = c * C + (rev ? rows - lane : lane);
-    if (t >= len) return 0.f;
-    return clamp_log_decay(A.g.g[A.g.per_token ? ((int64_t)bos + t) * A.H + h : h]);
-  };
-  // the chunk's decays (one wave): gamma as two floats, row and column factors
-  double seg_sum = 0.0;
-  auto decays = [&](float g, int buf) {
-    double x = (double)g * 1.4426950408889634;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const double y = __shfl_up(x, off);
-      if (lane >= off) x += y;
-    }
-    const double end = __shfl(x, 63);
-    const float hi = (float)x;
-    s_gh[buf][lane] = hi;
-    s_gl[buf][lane] = (float)(x - (double)hi);
-    s_row[buf][lane] = ex2(hi) * (rev ? 1.0f : A.scale);
-    s_col[buf][lane] = ex2((float)(end - x)) * (rev ? A.scale : 1.0f);
-    if (lane == 0) s_end[buf] = ex2((float)end);
-    seg_sum += end;
-  };
-  constexpr int kDecayWave = FULL ? 4 : 3;  // output wave 0 has the fewest scores
-
-  // lane constants of the LDS reads
-  const int swB = swz<KD>(lr);                       // row reads: rows 16 i + lr
-  const int tj = 4 * lg + (lr >> 2);                 // transposed reads: row of a token tile
+  // lane constants of the transposed reads: row of a token tile, its swizzles, piece
+  const int tj = 4 * lg + (lr >> 2);
   const int twB = swz<KD>(tj), twC = swz<CT>(tj);
   const int pc = lr & 3;
   // c^T of column tile j, tokens of step ks
@@ -416,39 +356,89 @@ __global__ void __launch_bounds__(FULL ? 2 * NTHR : NTHR, 1) walk_kernel(Args A)
     for (int p = 0; p < NPL; ++p)
       f[p] = read_tr2(bc + p * L::CC + r0 * (CT * 2) + cb, bc + p * L::CC + r1 * (CT * 2) + cb);
   };
+  // Every wave passes the same barriers: one a chunk, when the chunk and its
+  // entry state are in LDS; with one buffer a second one when it has been read.
 
-  float gnext = 0.f;
-  if (nch > 0) {
-    load_chunk(chunk_of(0));
-    if (FULL && !state_wave) load_a(chunk_of(0), ra);
-    if (w == kDecayWave) {
-      decays(load_decay(chunk_of(0)), 0);
-      if (nch > 1) gnext = load_decay(chunk_of(1));
-    }
-    write_chunk(0);
-    if (nch > 1) load_chunk(chunk_of(1));
-    if (state_wave) write_state(0);
-  }
-
-  for (int it = 0; it < nch; ++it) {
-    const int c = chunk_of(it);
-    const int rows = rows_in(c);
-    const int gb = it & 1;
-    const int buf = L::NBUF == 2 ? gb : 0;
-    const char* bb = lds + buf * L::buf;
-    const char* bc = bb + L::off_c;
-    barrier_lds();  // chunk `it` and its entry state are in LDS, chunk it - 1 has been read
-
-    if (state_wave) {
-      if constexpr (FULL && DOTS) {
-        // states at the segments' ends, for dg: the forward walk after the last
-        // chunk of a segment (below), the backward ones before it
-        if (W.ends && rev && ((c + 1) % A.seg_chunks == 0 || c + 1 == nch_all)) {
-          float* p = seg_at(W.ends, slot0 + c / A.seg_chunks);
+  if (w < 4) {
+    // =================================================== state waves
+    const int64_t slot0 = seg_slot(A, n, bos);
+    const int col = tile * CT + 16 * w + lr;  // this lane's column of S
+    auto channel = [&](int t) { return 32 * (t >> 1) + 8 * lg + 4 * (t & 1); };
+    // a segment's states in the workspace: fp32, tile by tile in this lane's order
+    auto seg_at = [&](float* base, int64_t slot) {
+      return base + ((slot * A.H + h) * ntile + tile) * (int64_t)(KD * CT) + (w * 64 + lane) * 4;
+    };
+    f32x4 S[NT];
 #pragma unroll
-          for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(p + t * (NTHR * 4)) = S[t];
+    for (int t = 0; t < NT; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (FULL) {
+      if (A.nseg > 1) {
+        const float* p = seg_at(W.seg_state, slot0 + seg);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) S[t] = *reinterpret_cast<const f32x4*>(p + t * (NTHR * 4));
+      } else if (W.s_in) {
+        const int64_t sl = W.in_idx ? (int64_t)W.in_idx[n] : n;
+        if (sl >= 0 && sl < W.in_slots) {
+          const int64_t base = (sl * A.H + h) * W.s_elems + col * W.s_col;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              S[t][i] = load1(W.s_in, base + (channel(t) + i) * W.s_row, W.in_bf16);
         }
       }
+    }
+    // the state's planes, as the left operands of S^T a^T: unit (column tile, kk), 16 bytes a lane
+    auto write_state = [&](int sbuf) {
+      if constexpr (FULL) {
+        char* p = lds + L::off_s + sbuf * (NPS * L::SS) + w * (KK * 1024) + lane * 16;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+          const f32x4 t0 = S[2 * kk], t1 = S[2 * kk + 1];
+          bf16x8 f[NPS];
+          split8<NPS>(f32x8{t0[0], t0[1], t0[2], t0[3], t1[0], t1[1], t1[2], t1[3]}, f);
+#pragma unroll
+          for (int k = 0; k < NPS; ++k) *reinterpret_cast<bf16x8*>(p + k * L::SS + kk * 1024) = f[k];
+        }
+      }
+    };
+    auto dump = [&](int c) {  // S at a segment's end, for dg
+      float* p = seg_at(W.ends, slot0 + c / A.seg_chunks);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(p + t * (NTHR * 4)) = S[t];
+    };
+    // fp32 operands: these waves also copy
+    Stage<WIDE, KD, NTHR> rb;
+    Stage<WIDE, CT, NTHR> rc;
+    auto load_chunk = [&](int c) {
+      const int rows = rows_in(c);
+      const int64_t tok0 = (int64_t)bos + c * C;
+      rb.load(rows_of(W.b, b_bf, tok0, rows, h, KD, 0, KD), (int)(W.b.stride * (b_bf ? 2 : 4)), b_bf,
+              rows, rev);
+      rc.load(rows_of(W.c, c_bf, tok0, rows, h, CD, tile * CT, CT),
+              (int)(W.c.stride * (c_bf ? 2 : 4)), c_bf, rows, rev);
+    };
+    auto write_chunk = [&](char* p) {
+      rb.write(p, b_bf);
+      rc.write(p + L::off_c, c_bf);
+    };
+    if (nch > 0) {
+      if constexpr (WIDE) {
+        load_chunk(chunk_of(0));
+        write_chunk(lds);
+        if (nch > 1) load_chunk(chunk_of(1));
+      }
+      write_state(0);
+    }
+    for (int it = 0; it < nch; ++it) {
+      const int c = chunk_of(it);
+      const int gb = it & 1;
+      const char* bb = buf_of(it);
+      const char* bc = bb + L::off_c;
+      const bool ends = DOTS && W.ends && ((c + 1) % A.seg_chunks == 0 || c + 1 == nch_all);
+      barrier_lds();
+      // the backward walks have the state at the segment's end before its last chunk
+      if (ends && rev) dump(c);
       // ---- S <- e^gamma_end S + b^T (decayed c)
       const float dec = s_end[gb];
 #pragma unroll
@@ -456,7 +446,7 @@ __global__ void __launch_bounds__(FULL ? 2 * NTHR : NTHR, 1) walk_kernel(Args A)
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         bf16x8 fc[NPL];
-        read_c(bc, w & 3, ks, fc);
+        read_c(bc, w, ks, fc);
         f32x8 x = widen8(fc[0]);
 #pragma unroll
         for (int p = 1; p < NPL; ++p) x += widen8(fc[p]);
@@ -476,15 +466,145 @@ __global__ void __launch_bounds__(FULL ? 2 * NTHR : NTHR, 1) walk_kernel(Args A)
           mma_planes<NPL, NPC>(fb, fx, S[t]);
         }
       }
-      if constexpr (FULL && DOTS) {
-        if (W.ends && !rev && ((c + 1) % A.seg_chunks == 0 || c + 1 == nch_all)) {
-          float* p = seg_at(W.ends, slot0 + c / A.seg_chunks);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(p + t * (NTHR * 4)) = S[t];
+      if (ends && !rev) dump(c);
+      if constexpr (L::NBUF == 1) barrier_lds();
+      if (it + 1 < nch) {
+        write_state(L::NSB == 1 ? 0 : gb ^ 1);
+        if constexpr (WIDE) {
+          write_chunk(lds);
+          if (it + 2 < nch) load_chunk(chunk_of(it + 2));
         }
       }
-    } else if constexpr (FULL) {
-      const int i = w & 3;  // row tile
+    }
+    if constexpr (!FULL) {
+      float* p = seg_at(W.seg_state, slot0 + seg);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(p + t * (NTHR * 4)) = S[t];
+    } else if (A.nseg == 1 && W.s_out) {
+      const int64_t sl = W.out_idx ? (int64_t)W.out_idx[n] : n;
+      if (sl >= 0 && sl < W.out_slots) {
+        // walking backwards, the state before the first token has its decay too
+        float first = 1.0f;
+        if (rev && len > 0)
+          first = ex2(clamp_log_decay(A.g.g[A.g.per_token ? (int64_t)bos * A.H + h : h]) *
+                      1.4426950408889634f);
+        const int64_t base = (sl * A.H + h) * W.s_elems + col * W.s_col;
+        const bool sbf = W.out_state_bf16;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int64_t at = base + (channel(t) + i) * W.s_row;
+            const float x = S[t][i] * first;
+            if (sbf) static_cast<uint16_t*>(W.s_out)[at] = f32_to_bf16_bits(x);
+            else static_cast<float*>(W.s_out)[at] = x;
+          }
+      }
+    }
+    return;
+  }
+
+  if (w == WV::decay) {
+    // =================================================== decay wave
+    // log2-decay of row `lane` of chunk c (rows past the chunk: 0).  Walking
+    // backwards, token t's decay is that of t + 1 and the last token's is 0.
+    auto load_decay = [&](int c) -> float {
+      const int rows = rows_in(c);
+      if (lane >= rows) return 0.f;
+      const int t = c * C + (rev ? rows - lane : lane);
+      if (t >= len) return 0.f;
+      return clamp_log_decay(A.g.g[A.g.per_token ? ((int64_t)bos + t) * A.H + h : h]);
+    };
+    double sum = 0.0;
+    // gamma as two floats, row and column factors
+    auto decays = [&](float g, int buf) {
+      double x = (double)g * 1.4426950408889634;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const double y = __shfl_up(x, off);
+        if (lane >= off) x += y;
+      }
+      const double end = __shfl(x, 63);
+      const float hi = (float)x;
+      s_gh[buf][lane] = hi;
+      s_gl[buf][lane] = (float)(x - (double)hi);
+      s_row[buf][lane] = ex2(hi) * (rev ? 1.0f : A.scale);
+      s_col[buf][lane] = ex2((float)(end - x)) * (rev ? A.scale : 1.0f);
+      if (lane == 0) s_end[buf] = ex2((float)end);
+      sum += end;
+    };
+    float g1 = 0.f, g2 = 0.f;  // the next two chunks'
+    if (nch > 0) decays(load_decay(chunk_of(0)), 0);
+    if (nch > 1) g1 = load_decay(chunk_of(1));
+    if (nch > 2) g2 = load_decay(chunk_of(2));
+    for (int it = 0; it < nch; ++it) {
+      barrier_lds();
+      if (it + 1 < nch) {
+        const float g = g1;
+        g1 = g2;
+        if (it + 3 < nch) g2 = load_decay(chunk_of(it + 3));
+        decays(g, (it & 1) ^ 1);
+      }
+      if constexpr (L::NBUF == 1) barrier_lds();
+    }
+    if (!FULL && lane == 0 && tile == 0)
+      W.seg_decay[(seg_slot(A, n, bos) + seg) * A.H + h] = (float)sum;
+    return;
+  }
+
+  if constexpr (!WIDE) {
+    if (w == WV::copy) {
+      // ================================================= copy wave
+      constexpr int OPS = L::buf / 1024;  // instructions a chunk
+      static_assert(L::NBUF == 3 && 2 * OPS < 64, "two chunks in flight");
+      const int sb = (int)(W.b.stride * 2), sc = (int)(W.c.stride * 2);
+      auto issue = [&](int it) {
+        const int c = chunk_of(it);
+        const int rows = rows_in(c);
+        const int64_t tok0 = (int64_t)bos + c * C;
+        char* p = buf_of(it);
+        copy_rows<KD>(rows_of(W.b, true, tok0, rows, h, KD, 0, KD), p, sb, rows, rev, lane);
+        copy_rows<CT>(rows_of(W.c, true, tok0, rows, h, CD, tile * CT, CT), p + L::off_c, sc, rows,
+                      rev, lane);
+      };
+      if (nch > 0) issue(0);
+      if (nch > 1) issue(1);
+      for (int it = 0; it < nch; ++it) {
+        // chunk `it` has arrived; the one behind it may be on its way
+        if (it + 1 < nch) wait_vm_le<OPS>();
+        else wait_vm_le<0>();
+        chunk::barrier_nofence();
+        if (it + 2 < nch) issue(it + 2);  // into the buffer of chunk it - 1, which has been read
+      }
+      return;
+    }
+  }
+
+  if constexpr (FULL) {
+    // =================================================== output waves
+    const int i = w - WV::out;          // row tile
+    const int orow = 16 * i + lr;       // this lane's row
+    const int swB = swz<KD>(lr);        // row reads: rows 16 x + lr
+    const int sa = (int)(W.a.stride * (a_bf ? 2 : 4));
+    const bool x_bf = !WIDE || W.x.bf16, o_bf = W.out_bf16;
+    float* const dots = DOTS ? W.dots : nullptr;
+    u32x4 ra[KK][WIDE ? 2 : 1], ra_next[KK][WIDE ? 2 : 1];
+    auto load_a = [&](int c, u32x4 (&r4)[KK][WIDE ? 2 : 1]) {
+      const int rows = rows_in(c);
+      const __amdgpu_buffer_rsrc_t r = rows_of(W.a, a_bf, (int64_t)bos + c * C, rows, h, KD, 0, KD);
+      const int tok = rev ? rows - 1 - orow : orow;
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk)
+        load_block<WIDE>(r, orow < rows ? tok * sa + (4 * kk + lg) * (a_bf ? 16 : 32) : kOutside,
+                         a_bf, r4[kk]);
+    };
+    if (nch > 0) load_a(chunk_of(0), ra);
+    for (int it = 0; it < nch; ++it) {
+      const int c = chunk_of(it);
+      const int rows = rows_in(c);
+      const int gb = it & 1;
+      const char* bb = buf_of(it);
+      const char* bc = bb + L::off_c;
       const int64_t tok0 = (int64_t)bos + c * C;
       const int tok = rev ? rows - 1 - orow : orow;
       bf16x8 fa[KK][NPL];
@@ -493,12 +613,12 @@ __global__ void __launch_bounds__(FULL ? 2 * NTHR : NTHR, 1) walk_kernel(Args A)
       if (it + 1 < nch) load_a(chunk_of(it + 1), ra_next);
       u32x4 xr[JT];  // x of this lane's row, for the dots
       if constexpr (DOTS) {
-        if (W.dots) {
-          const __amdgpu_buffer_rsrc_t r = rows_of(W.x, W.x.bf16, tok0, rows, h, CD, tile * CT, CT);
-          const int xs = (int)(W.x.stride * (W.x.bf16 ? 2 : 4));
+        if (dots) {
+          const __amdgpu_buffer_rsrc_t r = rows_of(W.x, x_bf, tok0, rows, h, CD, tile * CT, CT);
+          const int xs = (int)(W.x.stride * (x_bf ? 2 : 4));
 #pragma unroll
           for (int j = 0; j < JT; ++j) {
-            if (W.x.bf16) {
+            if (x_bf) {
               const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(
                   r, orow < rows ? tok * xs + (16 * j + 4 * lg) * 2 : kOutside, 0, 0));
               xr[j] = u32x4{v[0], v[1], 0, 0};
@@ -509,6 +629,7 @@ __global__ void __launch_bounds__(FULL ? 2 * NTHR : NTHR, 1) walk_kernel(Args A)
           }
         }
       }
+      barrier_lds();
       // ---- scores of row tile i against the tokens 0 .. 16i + 15, transposed
       bf16x8 fp[2][NPP];
       float diag = 0.f;
@@ -541,7 +662,7 @@ __global__ void __launch_bounds__(FULL ? 2 * NTHR : NTHR, 1) walk_kernel(Args A)
             const float x = v[e] * A.scale * ex2((rh - sh[e]) + (rl - sl[e]));
             if constexpr (DOTS) {
               if (s0 + e == orow) diag = x;
-              pv[4 * half + e] = (W.dots ? s0 + e < orow : s0 + e <= orow) ? x : 0.f;
+              pv[4 * half + e] = (dots ? s0 + e < orow : s0 + e <= orow) ? x : 0.f;
             } else {
               pv[4 * half + e] = s0 + e <= orow ? x : 0.f;
             }
@@ -552,7 +673,7 @@ __global__ void __launch_bounds__(FULL ? 2 * NTHR : NTHR, 1) walk_kernel(Args A)
       // ---- out^T = S^T a^T, the rows' decay, + c^T P^T
       f32x4 acc[JT];
       const float rowf = s_row[gb][orow];
-      const char* sp = lds + L::off_s + buf * (NPS * L::SS) + lane * 16;
+      const char* sp = lds + L::off_s + (L::NSB == 1 ? 0 : gb) * (NPS * L::SS) + lane * 16;
 #pragma unroll
       for (int j = 0; j < JT; ++j) {
         acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -577,13 +698,13 @@ __global__ void __launch_bounds__(FULL ? 2 * NTHR : NTHR, 1) walk_kernel(Args A)
         }
       }
       if constexpr (DOTS) {
-        if (W.dots) {
+        if (dots) {
           // x_t . out_t over the tile's columns, then the pair (t, t)
           float dot = 0.f;
 #pragma unroll
           for (int j = 0; j < JT; ++j) {
             f32x4 xv = __builtin_bit_cast(f32x4, xr[j]);
-            if (W.x.bf16) {
+            if (x_bf) {
               xv = f32x4{__uint_as_float(xr[j][0] << 16), __uint_as_float(xr[j][0] & 0xffff0000u),
                          __uint_as_float(xr[j][1] << 16), __uint_as_float(xr[j][1] & 0xffff0000u)};
             }
@@ -591,7 +712,7 @@ __global__ void __launch_bounds__(FULL ? 2 * NTHR : NTHR, 1) walk_kernel(Args A)
           }
           dot += __shfl_xor(dot, 16);
           dot += __shfl_xor(dot, 32);
-          if (lg == 0 && orow < rows) W.dots[((tok0 + tok) * A.H + h) * 2 + tile] = dot;
+          if (lg == 0 && orow < rows) dots[((tok0 + tok) * A.H + h) * 2 + tile] = dot;
           // + P[t,t] c_t: the lane that holds the pair hands it to the others of its row
           const float pd = __shfl(diag, lr + 16 * (lr >> 2));
 #pragma unroll
@@ -607,68 +728,30 @@ __global__ void __launch_bounds__(FULL ? 2 * NTHR : NTHR, 1) walk_kernel(Args A)
           }
         }
       }
+      if constexpr (L::NBUF == 1) barrier_lds();
       const int64_t ld = (int64_t)A.H * CD;
-      const int out_es = W.out_bf16 ? 2 : 4;
+      const int out_es = o_bf ? 2 : 4;
       const __amdgpu_buffer_rsrc_t ow =
           buffer_over(static_cast<char*>(W.out) + (tok0 * ld + (int64_t)h * CD + tile * CT) * out_es,
                       (uint32_t)(((rows - 1) * ld + CT) * out_es));
-      const int off0 = (int)((tok * ld + 4 * lg) * out_es);
+      const int off = orow < rows ? (int)((tok * ld + 4 * lg) * out_es) : kOutside;
+      if (o_bf) {
 #pragma unroll
-      for (int j = 0; j < JT; ++j) {
-        const int off = orow < rows ? off0 + 16 * j * out_es : kOutside;
-        if (W.out_bf16) {
+        for (int j = 0; j < JT; ++j) {
           const u16x4 b = {f32_to_bf16_bits(acc[j][0]), f32_to_bf16_bits(acc[j][1]),
                            f32_to_bf16_bits(acc[j][2]), f32_to_bf16_bits(acc[j][3])};
-          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, b), ow, off, 0, 0);
-        } else {
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[j]), ow, off, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, b), ow, off + 32 * j, 0, 0);
         }
+      } else {
+#pragma unroll
+        for (int j = 0; j < JT; ++j)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[j]), ow, off + 64 * j,
+                                                 0, 0);
       }
-    }
-
-    // ---- the next chunk into LDS, the one after it on its way
-    if (it + 1 < nch) {
-      if constexpr (L::NBUF == 1) barrier_lds();  // chunk `it` has been read
-      if (state_wave) write_state(L::NBUF == 2 ? gb ^ 1 : 0);
-      write_chunk(L::NBUF == 2 ? gb ^ 1 : 0);
-      if (FULL && !state_wave) {
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
+      for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-          for (int e = 0; e < (WIDE ? 2 : 1); ++e) ra[kk][e] = ra_next[kk][e];
-      }
-      if (it + 2 < nch) load_chunk(chunk_of(it + 2));
-      if (w == kDecayWave) {
-        decays(gnext, gb ^ 1);
-        if (it + 2 < nch) gnext = load_decay(chunk_of(it + 2));
-      }
-    }
-  }
-
-  if constexpr (!FULL) {
-    float* p = seg_at(W.seg_state, slot0 + seg);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(p + t * (NTHR * 4)) = S[t];
-    if (w == kDecayWave && lane == 0 && tile == 0)
-      W.seg_decay[(slot0 + seg) * A.H + h] = (float)seg_sum;
-  } else if (state_wave && A.nseg == 1 && W.s_out) {
-    const int64_t sl = W.out_idx ? (int64_t)W.out_idx[n] : n;
-    if (sl >= 0 && sl < W.out_slots) {
-      // walking backwards, the state before the first token has its decay too
-      float first = 1.0f;
-      if (rev && len > 0)
-        first = ex2(clamp_log_decay(A.g.g[A.g.per_token ? (int64_t)bos * A.H + h : h]) *
-                    1.4426950408889634f);
-      const int64_t base = (sl * A.H + h) * W.s_elems + col * W.s_col;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t at = base + (channel(t) + i) * W.s_row;
-          const float x = S[t][i] * first;
-          if (W.out_state_bf16) static_cast<uint16_t*>(W.s_out)[at] = f32_to_bf16_bits(x);
-          else static_cast<float*>(W.s_out)[at] = x;
-        }
+        for (int e = 0; e < (WIDE ? 2 : 1); ++e) ra[kk][e] = ra_next[kk][e];
     }
   }
 }
@@ -869,7 +952,7 @@ hipError_t launch_walk_kd(const Args& A, int walks, hipStream_t s) {
       cdiv((int64_t)A.N * A.nseg * A.H, 8) * 8 * (A.walk[0].s_elems / KD / CT);
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   walk_kernel<WIDE, KD, FULL, DOTS><<<dim3((unsigned)blocks, walks),
-                                      FULL ? 2 * NTHR : NTHR, 0, s>>>(A);
+                                      Waves<WIDE, FULL>::threads, 0, s>>>(A);
   return hipGetLastError();
 }
 // `walks` walks of one contraction width kd
