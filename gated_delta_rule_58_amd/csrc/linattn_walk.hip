@@ -15,7 +15,7 @@
 // so dq is the walk of (a, b, c) = (do, v, k) with the state S^T, and dv and dk
 // are walks from the last token to the first of (k, q, do) with state D and of
 // (v, do, q) with state D^T; there token t's decay is g_{t+1} and the state
-// carries scale.  One kernel runs the three walks at once (blockIdx.y).
+// carries scale.  (blockIdx.y: the walks of dq and dk share a launch.)
 //
 // dg: with G[j,i] = P[j,i] dP[j,i] the part of the loss's derivative that token
 // i's key and token j's query share (i = before the first token: the initial
@@ -28,26 +28,25 @@
 // of the sums over all later tokens (dg_kernel).
 //
 // Workgroup: 64 columns of c (and so of S and out) of one (sequence, head),
-// waves of four kinds, each with a loop of its own over the chunks:
-//   state waves   wave w owns columns 16w .. 16w+15 of S in MFMA accumulators.
-//                 Per chunk it adds b^T (decayed c) and leaves the new state's
-//                 bf16 values in LDS as the operands of the next readout.
-//   output waves  wave i owns the chunk's rows 16i .. 16i+15: scores against the
-//                 tokens up to its rows, S^T a^T, c^T P^T and the stores.  a goes
-//                 from global memory straight to its registers, and the scores
-//                 never leave them.
-//   copy wave     brings b and c of the chunk after the next into LDS
-//                 (three buffers) and touches nothing else, so that its loads
-//                 are waited for in the copy wave alone.
+// waves of four kinds, each kind with a loop of its own over the chunks:
+//   state waves   wave w owns 16 columns of S in MFMA accumulators.  Per chunk it
+//                 adds b^T (decayed c) and leaves the new state's bf16 values in
+//                 LDS as the operands of the next readout.
+//   output waves  two row tiles (0 and 3, or 1 and 2: the same work) and two
+//                 column tiles each: scores against the tokens up to the rows,
+//                 S^T a^T, c^T P^T and the stores.  The scores never leave the
+//                 registers.
+//   copy waves    bring a, b and c of coming chunks straight into LDS and do
+//                 nothing else: under load a wave spends thousands of cycles in
+//                 the issue of its loads, which no other wave then waits for.
 //   decay wave    the next chunk's decays.
 // S is the only thing handed between the kinds, so one barrier a chunk is
-// enough.  (fp32 operands: the state waves copy, because each value is split
-// into three, with one buffer and a second barrier.)
-// What bounds it: the sequential walk.  A layer of 96 heads gives 192
-// workgroups for 256 CUs, each with T / 64 chunks to go through, so the time is
-// chunks x the latency of one chunk until HBM is reached.  LDS carries the most
-// per chunk (240 to 350 KB a workgroup at 128 B a cycle), which is why the output
-// waves split rows and not columns: a and the scores then need no LDS.
+// enough.  (fp32 operands, three values each: the state waves copy, with one
+// buffer and a second barrier.)
+// What bounds it: a layer of 96 heads gives 192 workgroups for 256 CUs, each with
+// T / 64 chunks to go through one after the other; in a chunk LDS moves about
+// 250 KB at 128 B a cycle (stores into it at 79), and the matrix and the vector
+// units of a SIMD take about 2,000 cycles each.
 //
 // Fragments (16x16x32: lane = (lr, lg), lr the row or column, k = 8 lg + e):
 //   scores     computed transposed, b a^T: the accumulators of two row tiles of
@@ -62,10 +61,15 @@
 // that both kinds of read spread over the banks.
 //
 // Precision: a, b, c in bf16 enter as they are (fp32 ones as three bf16 values
-// that add up to them), P as NPP, S as NPS and the decayed c as NPC bf16 values;
+// that add up to them).  The decayed c, of which the fp32 state is made, enters as
+// three bf16 values; S and P, of which out is made, as one where out is bf16 (each
+// element is then off by at most 2^-8 of itself, as the rounding of out is), as
+// two where out is fp32 or makes dg;
 // accumulators, decays and the state are fp32, gamma is summed in 64 bits and
 // kept as two fp32 values, so that a strong decay early in a chunk costs the
 // weak ones behind it no digits.
+#include <type_traits>
+
 #include "chunk_common.hpp"
 #include "linattn.hpp"
 
@@ -78,6 +82,8 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 namespace {
 
@@ -96,26 +102,42 @@ __device__ __forceinline__ int swz(int row) {
 
 __device__ __forceinline__ f32x8 widen8(bf16x8 x) { return __builtin_convertvector(x, f32x8); }
 
-// x as the sum of NP bf16 values (each the rounding of what is left)
+// x as the sum of NP bf16 values (each the rounding of what is left).  Two
+// values a conversion: the empty asm keeps the pair in one register, or the
+// compiler converts each value by itself to widen it again.
 template <int NP>
 __device__ __forceinline__ void split8(f32x8 x, bf16x8 (&out)[NP]) {
+  u32x4 w[NP];
 #pragma unroll
-  for (int p = 0; p < NP; ++p) {
-    out[p] = __builtin_convertvector(x, bf16x8);
-    if (p + 1 < NP) x -= widen8(out[p]);
+  for (int k = 0; k < 4; ++k) {
+    float a = x[2 * k], b = x[2 * k + 1];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      uint32_t u = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+      if (p + 1 < NP) {
+        asm("" : "+v"(u));
+        a -= __uint_as_float(u << 16);
+        b -= __uint_as_float(u & 0xffff0000u);
+      }
+      w[p][k] = u;
+    }
   }
+#pragma unroll
+  for (int p = 0; p < NP; ++p) out[p] = __builtin_bit_cast(bf16x8, w[p]);
 }
 
-// acc += A B over the planes of A and B that matter (i + j < the larger count)
-template <int NA, int NB>
-__device__ __forceinline__ void mma_planes(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB],
-                                           f32x4& acc) {
+// Calls f(i, j) for the products of plane i of A and plane j of B that matter
+// (i + j < the larger count), the smallest first.  The products of several
+// accumulators go inside f: an MFMA that waits for the one before it takes more
+// than twice as long as one that does not (44 against 20 clocks here).
+template <int NA, int NB, class F>
+__device__ __forceinline__ void for_planes(F f) {
   constexpr int NMAX = NA > NB ? NA : NB;
 #pragma unroll
   for (int i = NA - 1; i >= 0; --i)
 #pragma unroll
     for (int j = NB - 1; j >= 0; --j)
-      if (i + j < NMAX) acc = mma_bf16(a[i], b[j], acc);
+      if (i + j < NMAX) f(i, j);
 }
 
 __device__ __forceinline__ s16x4 read_tr(const char* p) {
@@ -128,6 +150,33 @@ __device__ __forceinline__ bf16x8 read_tr2(const char* p0, const char* p1) {
   return __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
 }
 
+// x of another lane of the wave, by data-parallel move (0 where there is none)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Inclusive sums over the 64 lanes.  Moves between registers and no LDS
+// permutes: under the other waves' LDS traffic a chain of permutes took longer
+// than the rest of the chunk's work.
+__device__ __forceinline__ double wave_scan(double x) {
+  x += moved<0x111, 0xf>(x);  // row_shr 1, 2, 4, 8: within 16 lanes
+  x += moved<0x112, 0xf>(x);
+  x += moved<0x114, 0xf>(x);
+  x += moved<0x118, 0xf>(x);
+  x += moved<0x142, 0xa>(x);  // lane 15 of a row to the next row (rows 1, 3)
+  x += moved<0x143, 0xc>(x);  // lane 31 to rows 2, 3
+  return x;
+}
+__device__ __forceinline__ double of_lane(double x, int l) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, l);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), l);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 struct Walk {
   Operand a, b, c, x;       // x: the tensor of the dots (with dots)
   const void* s_in;         // entry states, or null (zeros)
@@ -138,7 +187,7 @@ struct Walk {
   const int32_t* out_idx;
   int64_t in_slots, out_slots;
   void* out;                // [T, H, CD]
-  float* dots;              // [T, H, 2]: x_t . out_t without the pair (t, t), per column tile
+  float* dots;              // [T, H, 4]: x_t . out_t without the pair (t, t), per 32 columns
   float* ends;              // states at the segments' ends (dg), slot-major, or null
   float* seg_state;         // cut sequences: each segment's own state, then its entry state
   float* seg_decay;         // cut sequences: each segment's summed log2-decay [slot, H]
@@ -146,7 +195,7 @@ struct Walk {
 };
 
 struct Args {
-  Walk walk[3];
+  Walk walk[2];
   Decay g;
   const int32_t* cu;   // null: equal lengths
   int N, T_tot, H, eq_len;
@@ -174,27 +223,26 @@ __device__ __forceinline__ int64_t seg_slot(const Args& A, int n, int bos) {
   return bos / (C * A.seg_chunks) + n;
 }
 
-template <bool WIDE, int KD>
+template <bool WIDE, int KD, int PL>
 struct Lds {
   static constexpr int NPL = WIDE ? 3 : 1;          // planes of an operand
-  static constexpr int NPS = WIDE ? 3 : 2;          // planes of the state
-  static constexpr int NBUF = WIDE ? 1 : 3;         // chunks of b and c
+  static constexpr int NBUF = WIDE ? 1 : PL == 1 ? 3 : 2;  // chunks of a, b and c
   static constexpr int NSB = WIDE ? 1 : 2;          // states
-  static constexpr int BB = C * KD * 2;             // one plane of b
+  static constexpr int AB = C * KD * 2;             // one plane of a or b
   static constexpr int CC = C * CT * 2;             // one plane of c
   static constexpr int SS = KD * CT * 2;            // one plane of the state
-  static constexpr int buf = NPL * (BB + CC);
-  static constexpr int off_c = NPL * BB;
+  static constexpr int off_b = WIDE ? 0 : AB;       // (fp32: a goes straight to registers)
+  static constexpr int off_c = off_b + NPL * AB;
+  static constexpr int buf = off_c + NPL * CC;
   static constexpr int off_s = NBUF * buf;
-  static constexpr int total = off_s + NSB * NPS * SS;
+  static constexpr int total = off_s + NSB * PL * SS;
 };
-// Waves of a workgroup: state waves 0 .. 3, then (FULL) output waves, then helpers.
+// Waves of a workgroup: state waves 0 .. 3, output waves 4 .. 7, then the helpers.
 template <bool WIDE, bool FULL>
 struct Waves {
-  static constexpr int out = 4;                        // first output wave
   static constexpr int decay = FULL ? 8 : 4;
-  static constexpr int copy = WIDE ? -1 : decay + 1;
-  static constexpr int threads = 64 * (decay + (WIDE ? 1 : 2));
+  static constexpr int copy = decay + 1;  // and copy + 1
+  static constexpr int threads = 64 * (WIDE ? decay : copy + 2);
 };
 
 // The eight values of a block as NP bf16 planes.
@@ -214,7 +262,10 @@ __device__ __forceinline__ void planes_of(const u32x4 (&r)[WIDE ? 2 : 1], bool b
     pl[0] = __builtin_bit_cast(bf16x8, r[0]);
   }
 }
-constexpr int kOutside = 0x7fffff00;  // an offset past every chunk: reads 0, stores nothing
+// Rows past a chunk's end need no test: their offsets lie behind the buffer's
+// range (or, walking backwards, below 0, which is behind it as an unsigned
+// offset), where loads read 0 and stores are dropped.  A test here becomes a
+// branch around each load, and the loads then wait for each other.
 template <bool WIDE>
 __device__ __forceinline__ void load_block(__amdgpu_buffer_rsrc_t rsrc, int off, bool bf16,
                                            u32x4 (&r)[WIDE ? 2 : 1]) {
@@ -237,17 +288,16 @@ struct Stage {
                                        int rows, bool reverse) {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      const int u = threadIdx.x + TH * i;
+      const int u = threadIdx.x % TH + TH * i;
       const int row = u / (W / 8), blk = u % (W / 8);
       const int tok = reverse ? rows - 1 - row : row;
-      load_block<WIDE>(rsrc, row < rows ? tok * stride_bytes + blk * (bf16 ? 16 : 32) : kOutside,
-                       bf16, r[i]);
+      load_block<WIDE>(rsrc, tok * stride_bytes + blk * (bf16 ? 16 : 32), bf16, r[i]);
     }
   }
   __device__ __forceinline__ void write(char* lds, bool bf16) const {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      const int u = threadIdx.x + TH * i;
+      const int u = threadIdx.x % TH + TH * i;
       const int row = u / (W / 8), blk = u % (W / 8);
       char* p = lds + row * (W * 2) + ((blk ^ swz<W>(row)) << 4);
       bf16x8 pl[WIDE ? 3 : 1];
@@ -259,29 +309,43 @@ struct Stage {
   }
 };
 
-// Buffer over the chunk's rows [tok0, tok0 + rows) of head h (a null tensor is zeros).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const Operand& o, bool bf16,
-                                                          int64_t tok0, int rows, int h, int d,
-                                                          int col0, int cols) {
-  const int es = bf16 ? 2 : 4;
-  const char* p = static_cast<const char*>(o.p) +
-                  (tok0 * o.stride + (int64_t)(h / o.group) * d + col0) * es;
-  return buffer_over(p, rows > 0 && o.p ? (uint32_t)(((rows - 1) * o.stride + cols) * es) : 0);
-}
+// The rows of one operand (or of out) that a workgroup walks over: one head's
+// `cols` channels from col0 of every token of its sequence.  Everything here is
+// the same for all lanes; the division by the group is done once.
+struct Rows {
+  const char* base;   // first token of the sequence
+  int64_t chunk;      // bytes a chunk
+  int stride, width;  // bytes between tokens, bytes of a row
+  __device__ __forceinline__ Rows(const Operand& o, bool bf16, int bos, int h, int d, int col0,
+                                  int cols) {
+    const int es = bf16 ? 2 : 4;
+    stride = (int)o.stride * es;
+    chunk = (int64_t)C * stride;
+    width = o.p ? cols * es : 0;  // a null tensor: nothing in range, which is zeros
+    base = static_cast<const char*>(o.p) +
+           (bos * o.stride + (int64_t)(h / o.group) * d + col0) * es;
+  }
+  // Buffer over `rows` rows of chunk c (none: everything reads zeros).
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t of(int c, int rows) const {
+    const int n = rows > 0 && width > 0 ? (rows - 1) * stride + width : 0;
+    return buffer_over(base + c * chunk, (uint32_t)n);
+  }
+};
 
-// Copies 64 rows of W channels of bf16 straight into LDS: 1 KiB an instruction,
-// lane l writes 16 bytes at 16 l, so the swizzle is in which block a lane asks for.
-template <int W>
+// Copies rows [row0, row0 + 64 / PARTS) of 64 rows of W channels of bf16 straight
+// into LDS: 1 KiB an instruction, lane l writes 16 bytes at 16 l, so the swizzle
+// is in which block a lane asks for.
+template <int W, int PARTS>
 __device__ __forceinline__ void copy_rows(__amdgpu_buffer_rsrc_t r, char* dst, int stride_bytes,
-                                          int rows, bool reverse, int lane) {
+                                          int rows, bool reverse, int lane, int row0) {
   constexpr int BPR = W / 8, RPI = 64 / BPR;  // blocks a row, rows an instruction
 #pragma unroll
-  for (int u = 0; u < C / RPI; ++u) {
-    const int row = u * RPI + lane / BPR;
+  for (int u = 0; u < C / RPI / PARTS; ++u) {
+    const int row = row0 + u * RPI + lane / BPR;
     const int blk = (lane % BPR) ^ swz<W>(row);
     const int tok = reverse ? rows - 1 - row : row;
-    chunk::buf_to_lds16(r, (chunk::lds_ptr_t)(dst + u * 1024),
-                        row < rows ? tok * stride_bytes + blk * 16 : kOutside, 0);
+    chunk::buf_to_lds16(r, (chunk::lds_ptr_t)(dst + row0 * (W * 2) + u * 1024),
+                        tok * stride_bytes + blk * 16, 0);
   }
 }
 // waits until at most N vector-memory operations of this wave are outstanding
@@ -293,20 +357,25 @@ __device__ __forceinline__ void wait_vm_le() {
   asm volatile("" ::: "memory");
 }
 
-// FULL: out, dots and the states; else (no output waves) the segment's own
-// state and decay.  DOTS: the backward's walks.
-template <bool WIDE, int KD, bool FULL, bool DOTS>
+// FULL: out, dots and the states; else (no output waves) the segment's own state
+// and decay.  DOTS: the backward's walks.  PL: bf16 values that stand for an
+// element of S and P in the products for out.
+template <bool WIDE, int KD, bool FULL, bool DOTS, int PL>
 __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(Args A) {
-  using L = Lds<WIDE, KD>;
+  using L = Lds<WIDE, KD, PL>;
   using WV = Waves<WIDE, FULL>;
-  constexpr int NPL = L::NPL, NPS = L::NPS;
-  constexpr int NPP = WIDE ? 3 : 2, NPC = 3;
+  constexpr int NPL = L::NPL, NBUF = L::NBUF;
+  constexpr int NPS = PL, NPP = PL, NPC = 3;
   constexpr int KK = KD / 32;   // contraction steps over the channels
   constexpr int NT = KD / 16;   // state tiles a wave
-  constexpr int JT = CT / 16;   // column tiles
   __shared__ __attribute__((aligned(16))) char lds[FULL ? L::total : L::off_s];
-  __shared__ __attribute__((aligned(16))) float s_gh[2][C], s_gl[2][C], s_row[2][C], s_col[2][C];
-  __shared__ float s_end[2];
+  // the chunk's decays, with gamma_i the sum up to row tile i's first row:
+  __shared__ __attribute__((aligned(16))) float s_gh[2][C], s_gl[2][C];  // gamma as two floats
+  __shared__ __attribute__((aligned(16))) float s_row[2][C];     // e^(gamma_r - gamma_i), r in tile i
+  __shared__ __attribute__((aligned(16))) float s_tok[2][3][C];  // scale e^(gamma_i - gamma_s), tile i = 1 ..
+  __shared__ __attribute__((aligned(16))) float s_col[2][C];     // e^(gamma_end - gamma_s)
+  __shared__ float s_tile[2][4];                                 // e^gamma_i
+  __shared__ float s_end[2];                                     // e^gamma_end
   __shared__ int s_seq[1];
 
   const Walk& W = A.walk[blockIdx.y];
@@ -316,16 +385,22 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
   const bool rev = W.reverse;
   const bool a_bf = !WIDE || W.a.bf16, b_bf = !WIDE || W.b.bf16, c_bf = !WIDE || W.c.bf16;
 
-  // ---- blockIdx.x -> (sequence, segment, head, tile): the tiles of a head on one XCD
+  // ---- blockIdx.x -> (sequence, segment, head, tile).  Workgroups go to the XCDs
+  // in turn; an XCD gets hb = ceil(H / 8) consecutive heads of every segment, with
+  // their tiles.  (Every eighth head instead: the tokens of a head are H rows
+  // apart, so for H a multiple of 16 its rows and those of the heads 16 further
+  // share one channel of the XCD's L2, and the XCD used two channels of sixteen.)
   const int CD = static_cast<int>(W.s_elems / KD);
   const int ntile = CD / CT;
-  const int id = blockIdx.x >> 3;
+  const int hb = (A.H + 7) >> 3;
+  int id = blockIdx.x >> 3;
   const int tile = id % ntile;
-  const int64_t pair = (int64_t)(id / ntile) * 8 + (blockIdx.x & 7);
-  if (pair >= (int64_t)A.N * A.nseg * A.H) return;
-  const int h = static_cast<int>(pair % A.H);
-  const int seg = static_cast<int>((pair / A.H) % A.nseg);
-  int n = static_cast<int>(pair / A.H / A.nseg);
+  id /= ntile;
+  const int h = (blockIdx.x & 7) * hb + id % hb;
+  id /= hb;
+  const int seg = id % A.nseg;
+  int n = id / A.nseg;
+  if (h >= A.H) return;
   if (A.cu) n = chunk::lpt_sequence(A.cu, A.N, A.T_tot, n, s_seq);
   n = __builtin_amdgcn_readfirstlane(n);
   int bos, len;
@@ -339,35 +414,104 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
   }
   const int nch = c_hi - c_lo;
   auto chunk_of = [&](int it) { return rev ? c_hi - 1 - it : c_lo + it; };
-  auto rows_in = [&](int c) { return len - c * C < C ? len - c * C : C; };
-  // chunk `it` is in buffer it % NBUF
-  auto buf_of = [&](int it) -> char* {
-    return lds + (L::NBUF == 1 ? 0 : (it % L::NBUF) * L::buf);
+  // rows of the walk's `it`-th chunk; none behind the last one, where the loads
+  // run all the same and read nothing (a branch around them would make every
+  // wait one for all of them)
+  auto rows_in = [&](int it) {
+    const int left = len - chunk_of(it) * C;
+    return it >= nch ? 0 : left < C ? left : C;
   };
-  // lane constants of the transposed reads: row of a token tile, its swizzles, piece
-  const int tj = 4 * lg + (lr >> 2);
-  const int twB = swz<KD>(tj), twC = swz<CT>(tj);
+  const int tj = 4 * lg + (lr >> 2);  // transposed reads: row of a token tile, piece
   const int pc = lr & 3;
-  // c^T of column tile j, tokens of step ks
-  auto read_c = [&](const char* bc, int j, int ks, bf16x8 (&f)[NPL]) {
-    const int r0 = 32 * ks + tj, r1 = r0 + 16;
-    const int cb = (((2 * j + (pc >> 1)) ^ twC) << 4) + ((pc & 1) << 3);
+  // Column tile 2 jh + j of the workgroup's columns: its column m is column
+  // 32 jh + 8 (m >> 2) + 4 j + (m & 3), so that a lane's rows 4 lg + i of a tile
+  // pair are eight consecutive columns of out.
+  auto column_of = [](int tl, int m) { return 32 * (tl >> 1) + 8 * (m >> 2) + 4 * (tl & 1) + (m & 3); };
+  // the lane's part of the reads of c^T, column tile tl
+  auto lane_c = [&](int tl) {
+    return L::off_c + tj * (CT * 2) + (((4 * (tl >> 1) + pc) ^ swz<CT>(tj)) << 4) + ((tl & 1) << 3);
+  };
+  auto read_c = [&](const char* bc, int ks, bf16x8 (&f)[NPL]) {
 #pragma unroll
     for (int p = 0; p < NPL; ++p)
-      f[p] = read_tr2(bc + p * L::CC + r0 * (CT * 2) + cb, bc + p * L::CC + r1 * (CT * 2) + cb);
+      f[p] = read_tr2(bc + p * L::CC + 32 * ks * (CT * 2), bc + p * L::CC + (32 * ks + 16) * (CT * 2));
   };
-  // Every wave passes the same barriers: one a chunk, when the chunk and its
-  // entry state are in LDS; with one buffer a second one when it has been read.
+  // All kinds pass the same barriers: one a chunk, when the chunk and its entry
+  // state are in LDS; with one buffer a second one when it has been read.
+
+  // ---- decays: the decay wave's (fp32 operands: state wave 3's)
+  // Log-decay of row `lane` of a chunk as loaded, by every state wave (a load
+  // that only one of them makes would make the others' waits inexact).  Walking
+  // backwards, token t's decay is that of t + 1.
+  const float* const g0 = A.g.g + (A.g.per_token ? (int64_t)bos * A.H + h : h);
+  const int g_step = A.g.per_token ? A.H * 4 : 0;
+  auto load_decay = [&](int it) -> float {
+    const int c = chunk_of(it), rows = rows_in(it);
+    const int last = len - c * C < rows + 1 ? rows - 1 : rows;  // last token a lane may ask for
+    const __amdgpu_buffer_rsrc_t r =
+        buffer_over(reinterpret_cast<const char*>(g0) + (int64_t)c * C * g_step,
+                    rows > 0 ? (uint32_t)(last * g_step + 4) : 0);
+    return __uint_as_float(
+        __builtin_amdgcn_raw_buffer_load_b32(r, (rev ? rows - lane : lane) * g_step, 0, 0));
+  };
+  double sum = 0.0;
+  // of chunk `it` from its loaded g; rows past its end and, walking backwards, the
+  // last token have none
+  auto decays = [&](int it, float g, int buf) {
+    const int c = chunk_of(it), rows = rows_in(it);
+    const int t = c * C + (rev ? rows - lane : lane);
+    g = lane < rows && t < len ? clamp_log_decay(g) : 0.f;
+    const double x = wave_scan((double)g * 1.4426950408889634);
+    const double end = of_lane(x, 63);
+    const double e1 = of_lane(x, 15), e2 = of_lane(x, 31), e3 = of_lane(x, 47);
+    const float hi = (float)x;
+    // walking backwards the state carries scale, so the readout does not
+    s_col[buf][lane] = ex2((float)(end - x)) * (rev ? A.scale : 1.0f);
+    if constexpr (FULL) {
+      s_gh[buf][lane] = hi;
+      s_gl[buf][lane] = (float)(x - (double)hi);
+      const double mine = lane < 16 ? 0.0 : lane < 32 ? e1 : lane < 48 ? e2 : e3;
+      s_row[buf][lane] = ex2((float)(x - mine));
+      s_tok[buf][0][lane] = A.scale * ex2((float)(e1 - x));  // read for s before the tile only
+      s_tok[buf][1][lane] = A.scale * ex2((float)(e2 - x));
+      s_tok[buf][2][lane] = A.scale * ex2((float)(e3 - x));
+      if ((lane & 15) == 0) s_tile[buf][lane >> 4] = ex2((float)mine) * (rev ? 1.0f : A.scale);
+    }
+    if (lane == 0) s_end[buf] = ex2((float)end);
+    sum += end;
+  };
 
   if (w < 4) {
     // =================================================== state waves
     const int64_t slot0 = seg_slot(A, n, bos);
-    const int col = tile * CT + 16 * w + lr;  // this lane's column of S
+    const int col = tile * CT + column_of(w, lr);  // this lane's column of S
     auto channel = [&](int t) { return 32 * (t >> 1) + 8 * lg + 4 * (t & 1); };
     // a segment's states in the workspace: fp32, tile by tile in this lane's order
     auto seg_at = [&](float* base, int64_t slot) {
       return base + ((slot * A.H + h) * ntile + tile) * (int64_t)(KD * CT) + (w * 64 + lane) * 4;
     };
+    // fp32 operands: b and c of the next chunk on their way
+    Stage<WIDE, KD, NTHR> rb[1];
+    Stage<WIDE, CT, NTHR> rc[1];
+    const Rows b_rows(W.b, b_bf, bos, h, KD, 0, KD), c_rows(W.c, c_bf, bos, h, CD, tile * CT, CT);
+    auto load_chunk = [&](int it, auto& sb, auto& sc) {
+      const int c = chunk_of(it), rows = rows_in(it);
+      sb.load(b_rows.of(c, rows), b_rows.stride, b_bf, rows, rev);
+      sc.load(c_rows.of(c, rows), c_rows.stride, c_bf, rows, rev);
+    };
+    auto write_chunk = [&](char* p, const auto& sb, const auto& sc) {
+      sb.write(p + L::off_b, b_bf);
+      sc.write(p + L::off_c, c_bf);
+    };
+    float g_next = 0.f;  // of the next chunk
+    if constexpr (WIDE) {
+      if (nch > 0) {
+        const float g_first = load_decay(0);
+        load_chunk(0, rb[0], rc[0]);
+        g_next = load_decay(1);
+        if (w == 3) decays(0, g_first, 0);
+      }
+    }
     f32x4 S[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -407,79 +551,96 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
 #pragma unroll
       for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(p + t * (NTHR * 4)) = S[t];
     };
-    // fp32 operands: these waves also copy
-    Stage<WIDE, KD, NTHR> rb;
-    Stage<WIDE, CT, NTHR> rc;
-    auto load_chunk = [&](int c) {
-      const int rows = rows_in(c);
-      const int64_t tok0 = (int64_t)bos + c * C;
-      rb.load(rows_of(W.b, b_bf, tok0, rows, h, KD, 0, KD), (int)(W.b.stride * (b_bf ? 2 : 4)), b_bf,
-              rows, rev);
-      rc.load(rows_of(W.c, c_bf, tok0, rows, h, CD, tile * CT, CT),
-              (int)(W.c.stride * (c_bf ? 2 : 4)), c_bf, rows, rev);
-    };
-    auto write_chunk = [&](char* p) {
-      rb.write(p, b_bf);
-      rc.write(p + L::off_c, c_bf);
-    };
+    // the lane's part of the transposed reads
+    const int my_c = lane_c(w);
+    int my_b[KK];
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk)
+      my_b[kk] = L::off_b + tj * (KD * 2) + (((4 * kk + pc) ^ swz<KD>(tj)) << 4);
+
     if (nch > 0) {
       if constexpr (WIDE) {
-        load_chunk(chunk_of(0));
-        write_chunk(lds);
-        if (nch > 1) load_chunk(chunk_of(1));
+        write_chunk(lds, rb[0], rc[0]);
+        load_chunk(1, rb[0], rc[0]);
       }
       write_state(0);
     }
+    int slot = 0;  // it % NBUF
     for (int it = 0; it < nch; ++it) {
       const int c = chunk_of(it);
       const int gb = it & 1;
-      const char* bb = buf_of(it);
-      const char* bc = bb + L::off_c;
+      const char* const buf = lds + slot * L::buf;
       const bool ends = DOTS && W.ends && ((c + 1) % A.seg_chunks == 0 || c + 1 == nch_all);
       barrier_lds();
       // the backward walks have the state at the segment's end before its last chunk
       if (ends && rev) dump(c);
-      // ---- S <- e^gamma_end S + b^T (decayed c)
+      // ---- S <- e^gamma_end S + b^T (decayed c), G tiles at a time: the fragments
+      // of b^T of the next tiles are read while these are multiplied.
+      constexpr int G = WIDE ? 2 : 4;
+      bf16x8 fc[2][NPL], fb[2][G][NPL];
+      auto read_b = [&](int grp, bf16x8 (&f)[G][NPL]) {  // grp = (step ks, tiles)
+#pragma unroll
+        for (int x = 0; x < G; ++x) {
+          const int idx = grp * G + x, t = idx % NT, r0 = 32 * (idx / NT);
+#pragma unroll
+          for (int p = 0; p < NPL; ++p) {
+            const char* q = buf + my_b[t >> 1] + (p * L::AB + r0 * (KD * 2) + 8 * (t & 1));
+            f[x][p] = read_tr2(q, q + 16 * (KD * 2));
+          }
+        }
+      };
+      f32x4 ec[4];
       const float dec = s_end[gb];
 #pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        read_c(buf + my_c, ks, fc[ks]);
+        ec[2 * ks] = *reinterpret_cast<const f32x4*>(&s_col[gb][32 * ks + 4 * lg]);
+        ec[2 * ks + 1] = *reinterpret_cast<const f32x4*>(&s_col[gb][32 * ks + 16 + 4 * lg]);
+      }
+      read_b(0, fb[0]);
+      if constexpr (WIDE) {
+        if (w == 3 && it + 1 < nch) decays(it + 1, g_next, gb ^ 1);
+      }
+#pragma unroll
       for (int t = 0; t < NT; ++t) S[t] *= dec;
+      bf16x8 fx[2][NPC];
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        bf16x8 fc[NPL];
-        read_c(bc, w, ks, fc);
-        f32x8 x = widen8(fc[0]);
+        f32x8 x = widen8(fc[ks][0]);
 #pragma unroll
-        for (int p = 1; p < NPL; ++p) x += widen8(fc[p]);
-        const f32x4 e0 = *reinterpret_cast<const f32x4*>(&s_col[gb][32 * ks + 4 * lg]);
-        const f32x4 e1 = *reinterpret_cast<const f32x4*>(&s_col[gb][32 * ks + 16 + 4 * lg]);
+        for (int p = 1; p < NPL; ++p) x += widen8(fc[ks][p]);
+        const f32x4 e0 = ec[2 * ks], e1 = ec[2 * ks + 1];
         x *= f32x8{e0[0], e0[1], e0[2], e0[3], e1[0], e1[1], e1[2], e1[3]};
-        bf16x8 fx[NPC];
-        split8<NPC>(x, fx);
-        const int r0 = 32 * ks + tj, r1 = r0 + 16;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const int at = (((4 * (t >> 1) + pc) ^ twB) << 4) + ((t & 1) << 3);
-          bf16x8 fb[NPL];
-#pragma unroll
-          for (int p = 0; p < NPL; ++p)
-            fb[p] = read_tr2(bb + p * L::BB + r0 * (KD * 2) + at, bb + p * L::BB + r1 * (KD * 2) + at);
-          mma_planes<NPL, NPC>(fb, fx, S[t]);
-        }
+        split8<NPC>(x, fx[ks]);
       }
+#pragma unroll
+      for (int grp = 0; grp < 2 * NT / G; ++grp) {
+        if (grp + 1 < 2 * NT / G) read_b(grp + 1, fb[(grp + 1) & 1]);
+          for_planes<NPL, NPC>([&](int i, int j) {
+#pragma unroll
+          for (int x = 0; x < G; ++x) {
+            f32x4& acc = S[(grp * G + x) % NT];
+            acc = mma_bf16(fb[grp & 1][x][i], fx[grp * G / NT][j], acc);
+          }
+        });
+        }
       if (ends && !rev) dump(c);
-      if constexpr (L::NBUF == 1) barrier_lds();
-      if (it + 1 < nch) {
-        write_state(L::NSB == 1 ? 0 : gb ^ 1);
-        if constexpr (WIDE) {
-          write_chunk(lds);
-          if (it + 2 < nch) load_chunk(chunk_of(it + 2));
-        }
+      if constexpr (WIDE) barrier_lds();
+      write_state(L::NSB == 2 ? gb ^ 1 : 0);
+      if constexpr (WIDE) {
+        write_chunk(lds, rb[0], rc[0]);
+        g_next = load_decay(it + 2);
+        load_chunk(it + 2, rb[0], rc[0]);
       }
+      slot = slot + 1 == NBUF ? 0 : slot + 1;
     }
+
     if constexpr (!FULL) {
       float* p = seg_at(W.seg_state, slot0 + seg);
 #pragma unroll
       for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(p + t * (NTHR * 4)) = S[t];
+      if (WIDE && w == 3 && lane == 0 && tile == 0)
+        W.seg_decay[(slot0 + seg) * A.H + h] = (float)sum;
     } else if (A.nseg == 1 && W.s_out) {
       const int64_t sl = W.out_idx ? (int64_t)W.out_idx[n] : n;
       if (sl >= 0 && sl < W.out_slots) {
@@ -504,255 +665,365 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
     return;
   }
 
-  if (w == WV::decay) {
-    // =================================================== decay wave
-    // log2-decay of row `lane` of chunk c (rows past the chunk: 0).  Walking
-    // backwards, token t's decay is that of t + 1 and the last token's is 0.
-    auto load_decay = [&](int c) -> float {
-      const int rows = rows_in(c);
-      if (lane >= rows) return 0.f;
-      const int t = c * C + (rev ? rows - lane : lane);
-      if (t >= len) return 0.f;
-      return clamp_log_decay(A.g.g[A.g.per_token ? ((int64_t)bos + t) * A.H + h : h]);
-    };
-    double sum = 0.0;
-    // gamma as two floats, row and column factors
-    auto decays = [&](float g, int buf) {
-      double x = (double)g * 1.4426950408889634;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const double y = __shfl_up(x, off);
-        if (lane >= off) x += y;
-      }
-      const double end = __shfl(x, 63);
-      const float hi = (float)x;
-      s_gh[buf][lane] = hi;
-      s_gl[buf][lane] = (float)(x - (double)hi);
-      s_row[buf][lane] = ex2(hi) * (rev ? 1.0f : A.scale);
-      s_col[buf][lane] = ex2((float)(end - x)) * (rev ? A.scale : 1.0f);
-      if (lane == 0) s_end[buf] = ex2((float)end);
-      sum += end;
-    };
-    float g1 = 0.f, g2 = 0.f;  // the next two chunks'
-    if (nch > 0) decays(load_decay(chunk_of(0)), 0);
-    if (nch > 1) g1 = load_decay(chunk_of(1));
-    if (nch > 2) g2 = load_decay(chunk_of(2));
-    for (int it = 0; it < nch; ++it) {
-      barrier_lds();
-      if (it + 1 < nch) {
+  if constexpr (!WIDE) {
+    if (w == WV::decay) {
+      // ================================================= decay wave
+      float g1 = load_decay(0), g2 = load_decay(1);
+      if (nch > 0) decays(0, g1, 0);
+      g1 = g2;
+      g2 = load_decay(2);
+      for (int it = 0; it < nch; ++it) {
+        barrier_lds();
         const float g = g1;
         g1 = g2;
-        if (it + 3 < nch) g2 = load_decay(chunk_of(it + 3));
-        decays(g, (it & 1) ^ 1);
+        g2 = load_decay(it + 3);
+        if (it + 1 < nch) decays(it + 1, g, (it & 1) ^ 1);
       }
-      if constexpr (L::NBUF == 1) barrier_lds();
+      if (!FULL && lane == 0 && tile == 0)
+        W.seg_decay[(seg_slot(A, n, bos) + seg) * A.H + h] = (float)sum;
+      return;
     }
-    if (!FULL && lane == 0 && tile == 0)
-      W.seg_decay[(seg_slot(A, n, bos) + seg) * A.H + h] = (float)sum;
-    return;
-  }
-
-  if constexpr (!WIDE) {
-    if (w == WV::copy) {
-      // ================================================= copy wave
-      constexpr int OPS = L::buf / 1024;  // instructions a chunk
-      static_assert(L::NBUF == 3 && 2 * OPS < 64, "two chunks in flight");
-      const int sb = (int)(W.b.stride * 2), sc = (int)(W.c.stride * 2);
-      auto issue = [&](int it) {
-        const int c = chunk_of(it);
-        const int rows = rows_in(c);
-        const int64_t tok0 = (int64_t)bos + c * C;
-        char* p = buf_of(it);
-        copy_rows<KD>(rows_of(W.b, true, tok0, rows, h, KD, 0, KD), p, sb, rows, rev, lane);
-        copy_rows<CT>(rows_of(W.c, true, tok0, rows, h, CD, tile * CT, CT), p + L::off_c, sc, rows,
-                      rev, lane);
+    if (w >= WV::copy) {
+      // ================================================= copy waves: a and b, half of c each
+      const int half = w - WV::copy;
+      constexpr int OPS = (FULL ? L::AB : L::AB / 2) / 1024 + L::CC / 2048;  // instructions a chunk
+      static_assert(2 * OPS < 64, "two chunks in flight");
+      const Operand& ab = FULL && half == 0 ? W.a : W.b;
+      const Rows ab_rows(ab, true, bos, h, KD, 0, KD), c_rows(W.c, true, bos, h, CD, tile * CT, CT);
+      auto issue = [&](int it, int slot) {
+        const int c = chunk_of(it), rows = rows_in(it);
+        char* p = lds + slot * L::buf;
+        if constexpr (FULL)
+          copy_rows<KD, 1>(ab_rows.of(c, rows), p + half * L::off_b, ab_rows.stride, rows, rev, lane, 0);
+        else
+          copy_rows<KD, 2>(ab_rows.of(c, rows), p + L::off_b, ab_rows.stride, rows, rev, lane, 32 * half);
+        copy_rows<CT, 2>(c_rows.of(c, rows), p + L::off_c, c_rows.stride, rows, rev, lane, 32 * half);
       };
-      if (nch > 0) issue(0);
-      if (nch > 1) issue(1);
+      // chunks it .. it + NBUF - 2 are asked for before barrier `it`; the buffer of
+      // chunk it - 1 is free behind it
+      if (nch > 0) issue(0, 0);
+      if (NBUF == 3 && nch > 0) issue(1, 1);
+      int slot = NBUF - 1;  // (it + NBUF - 1) % NBUF
       for (int it = 0; it < nch; ++it) {
-        // chunk `it` has arrived; the one behind it may be on its way
-        if (it + 1 < nch) wait_vm_le<OPS>();
-        else wait_vm_le<0>();
+        wait_vm_le<(NBUF - 2) * OPS>();  // chunk `it` has arrived
         chunk::barrier_nofence();
-        if (it + 2 < nch) issue(it + 2);  // into the buffer of chunk it - 1, which has been read
+        issue(it + NBUF - 1, slot);      // (none behind the last chunk: reads zeros)
+        slot = slot + 1 == NBUF ? 0 : slot + 1;
       }
+      wait_vm_le<0>();
       return;
     }
   }
 
   if constexpr (FULL) {
     // =================================================== output waves
-    const int i = w - WV::out;          // row tile
-    const int orow = 16 * i + lr;       // this lane's row
-    const int swB = swz<KD>(lr);        // row reads: rows 16 x + lr
-    const int sa = (int)(W.a.stride * (a_bf ? 2 : 4));
+    // row tiles T0 and T1 (fixed at compile time: no branches inside, so that the
+    // loads of one product can be placed among the arithmetic of another),
+    // column tiles 2 jh and 2 jh + 1
+    const int jh = w & 1;
     const bool x_bf = !WIDE || W.x.bf16, o_bf = W.out_bf16;
     float* const dots = DOTS ? W.dots : nullptr;
-    u32x4 ra[KK][WIDE ? 2 : 1], ra_next[KK][WIDE ? 2 : 1];
-    auto load_a = [&](int c, u32x4 (&r4)[KK][WIDE ? 2 : 1]) {
-      const int rows = rows_in(c);
-      const __amdgpu_buffer_rsrc_t r = rows_of(W.a, a_bf, (int64_t)bos + c * C, rows, h, KD, 0, KD);
-      const int tok = rev ? rows - 1 - orow : orow;
+    const Rows a_rows(W.a, a_bf, bos, h, KD, 0, KD);
+    const Rows x_rows(W.x, x_bf, bos, h, CD, tile * CT + 32 * jh, 32);
+    Operand out_op;
+    out_op.p = W.out;
+    out_op.stride = (int64_t)A.H * CD;
+    const Rows o_rows(out_op, o_bf, bos, h, CD, tile * CT + 32 * jh, 32);
+    int my_k[KK], my_c[2];              // the lane's part of the reads of b and of c^T
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk)
-        load_block<WIDE>(r, orow < rows ? tok * sa + (4 * kk + lg) * (a_bf ? 16 : 32) : kOutside,
-                         a_bf, r4[kk]);
+    for (int kk = 0; kk < KK; ++kk) my_k[kk] = lr * (KD * 2) + (((4 * kk + lg) ^ swz<KD>(lr)) << 4);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) my_c[j] = lane_c(2 * jh + j);
+
+    auto output = [&](auto half_of) {
+      constexpr int T[2] = {decltype(half_of)::value, 3 - decltype(half_of)::value};
+      constexpr int NU = T[1] + 1;      // token tiles up to the rows
+      u32x4 ra[2][KK][WIDE ? 2 : 1], ra_next[2][KK][WIDE ? 2 : 1];
+      auto load_a = [&](int it, u32x4 (&r4)[2][KK][WIDE ? 2 : 1]) {
+        const int rows = rows_in(it);
+        const __amdgpu_buffer_rsrc_t r = a_rows.of(chunk_of(it), rows);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int row = 16 * T[t] + lr;
+          const int tok = rev ? rows - 1 - row : row;
+#pragma unroll
+          for (int kk = 0; kk < KK; ++kk)
+            load_block<WIDE>(r, tok * a_rows.stride + (4 * kk + lg) * (a_bf ? 16 : 32), a_bf,
+                             r4[t][kk]);
+        }
+      };
+      if (nch > 0) {
+        if constexpr (WIDE) load_a(0, ra);
+      }
+      int slot = 0;  // it % NBUF
+      for (int it = 0; it < nch; ++it) {
+        const int c = chunk_of(it);
+        const int rows = rows_in(it);
+        const int gb = it & 1;
+        const char* const ba = lds + slot * L::buf;
+        const char* const bb = ba + L::off_b;
+        const char* const sp =
+            lds + L::off_s + (L::NSB == 2 ? gb : 0) * (NPS * L::SS) + jh * (2 * KK * 1024) + lane * 16;
+        bf16x8 fa[2][KK][NPL];
+        if constexpr (WIDE) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) planes_of<WIDE>(ra[t][kk], a_bf, fa[t][kk]);
+          load_a(it + 1, ra_next);
+        }
+        u32x4 xr[2][2];  // x of this lane's rows, for the dots
+        if constexpr (DOTS) {
+          const __amdgpu_buffer_rsrc_t r = x_rows.of(c, dots ? rows : 0);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int row = 16 * T[t] + lr;
+            const int tok = rev ? rows - 1 - row : row;
+            for (int j = 0; j < 2; ++j) {  // eight bf16, or four of eight fp32
+              xr[t][j] = u32x4{0, 0, 0, 0};
+              if (j == 0 || !x_bf)
+                xr[t][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                    r, tok * x_rows.stride + (x_bf ? 16 * lg : 32 * lg + 16 * j), 0, 0));
+            }
+          }
+        }
+        barrier_lds();
+
+        // ---- scores against token tile u, transposed
+        bf16x8 fk[NU][KK][NPL], fs[2][KK][NPS], fc[2][2][NPL], fp[2][2][NPP];
+        f32x4 p[2][NU], acc[2][2];
+        auto read_k = [&](int u) {
+#pragma unroll
+          for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+            for (int q = 0; q < NPL; ++q)
+              fk[u][kk][q] = *reinterpret_cast<const bf16x8*>(
+                  bb + my_k[kk] + (q * L::AB + 16 * u * (KD * 2)));
+        };
+        // token tiles u0 and u0 + 1
+        auto mul_k = [&](int u0) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int u = u0; u < u0 + 2; ++u)
+              if (u <= T[t]) p[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int kk = 0; kk < KK; ++kk)
+            for_planes<NPL, NPL>([&](int i, int j) {
+#pragma unroll
+              for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int u = u0; u < u0 + 2; ++u)
+                  if (u <= T[t])  // not behind the rows
+                    p[t][u] = mma_bf16(fk[u][kk][i], fa[t][kk][j], p[t][u]);
+            });
+        };
+        auto read_s = [&](int kk0, int kk1) {
+#pragma unroll
+          for (int kk = kk0; kk < kk1; ++kk)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int k = 0; k < NPS; ++k)
+                fs[j][kk][k] =
+                    *reinterpret_cast<const bf16x8*>(sp + k * L::SS + (j * KK + kk) * 1024);
+        };
+        auto mul_s = [&](int kk0, int kk1) {
+#pragma unroll
+          for (int kk = kk0; kk < kk1; ++kk)
+            for_planes<NPS, NPL>([&](int i, int k) {
+#pragma unroll
+              for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  acc[t][j] = mma_bf16(fs[j][kk][i], fa[t][kk][k], acc[t][j]);
+            });
+        };
+        // Decays of the scores.  Tokens before row tile i: e^(gamma_r - gamma_i)
+        // e^(gamma_i - gamma_s), both at most 1; tokens of the tile itself: the
+        // difference of the sums, masked.
+        float rowf[2], tilef[2], rh[2], rl[2], diag[2];
+        f32x4 tokf[2][3], sh[2], sl[2];
+        auto read_w = [&](int t) {
+          const int row = 16 * T[t] + lr, own = 16 * T[t] + 4 * lg;
+          rowf[t] = s_row[gb][row];
+          tilef[t] = s_tile[gb][T[t]];
+          rh[t] = s_gh[gb][row];
+          rl[t] = s_gl[gb][row];
+          sh[t] = *reinterpret_cast<const f32x4*>(&s_gh[gb][own]);
+          sl[t] = *reinterpret_cast<const f32x4*>(&s_gl[gb][own]);
+#pragma unroll
+          for (int u = 0; u < T[t]; ++u)
+            tokf[t][u] = *reinterpret_cast<const f32x4*>(&s_tok[gb][T[t] - 1][16 * u + 4 * lg]);
+        };
+        auto weigh = [&](int t) {
+          const int row = 16 * T[t] + lr;
+#pragma unroll
+          for (int u = 0; u <= T[t]; ++u) {
+            const int s0 = 16 * u + 4 * lg;
+            if (u < T[t]) {
+              p[t][u] *= tokf[t][u < 3 ? u : 0] * rowf[t];
+            } else {
+              diag[t] = 0.f;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float x = p[t][u][e] * A.scale * ex2((rh[t] - sh[t][e]) + (rl[t] - sl[t][e]));
+                if constexpr (DOTS) {
+                  if (s0 + e == row) diag[t] = x;
+                  p[t][u][e] = (dots ? s0 + e < row : s0 + e <= row) ? x : 0.f;
+                } else {
+                  p[t][u][e] = s0 + e <= row ? x : 0.f;
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int ks = 0; 2 * ks <= T[t]; ++ks) {
+            const f32x4 lo = p[t][2 * ks];
+            f32x4 hi = {0.f, 0.f, 0.f, 0.f};
+            if (2 * ks + 1 <= T[t]) hi = p[t][2 * ks + 1];
+            split8<NPP>(f32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}, fp[t][ks]);
+          }
+        };
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (!WIDE) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+              fa[t][kk][0] = *reinterpret_cast<const bf16x8*>(ba + my_k[kk] + 16 * T[t] * (KD * 2));
+        }
+        auto read_c2 = [&] {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) read_c(ba + my_c[j], ks, fc[j][ks]);
+        };
+        if constexpr (PL == 1) {
+          read_k(0);
+          read_k(1);
+          read_k(2);
+          if constexpr (NU == 4) read_k(3);
+          read_s(0, KK);
+          read_w(0);
+          read_w(1);
+          mul_k(0);
+          mul_k(2);
+          read_c2();
+          weigh(0);
+          weigh(1);
+          mul_s(0, KK);
+        } else {
+          // one group of operands after the other: all at once they do not fit the registers
+          read_k(0);
+          read_k(1);
+          read_w(0);
+          read_w(1);
+          mul_k(0);
+          read_k(2);
+          if constexpr (NU == 4) read_k(3);
+          weigh(0);
+          mul_k(2);
+          read_s(0, KK / 2);
+          weigh(1);
+          mul_s(0, KK / 2);
+          read_s(KK / 2, KK);
+          read_c2();
+          mul_s(KK / 2, KK);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float f = rowf[t] * tilef[t];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[t][j] *= f;
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+          for_planes<NPL, NPP>([&](int i, int k) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                if (2 * ks <= T[t]) acc[t][j] = mma_bf16(fc[j][ks][i], fp[t][ks][k], acc[t][j]);
+          });
+        if constexpr (DOTS) {
+          if (dots) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int row = 16 * T[t] + lr;
+              const int tok = rev ? rows - 1 - row : row;
+              // x_t . out_t over the wave's columns, then the pair (t, t)
+              float dot = 0.f;
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                f32x4 xv = __builtin_bit_cast(f32x4, xr[t][j]);
+                if (x_bf) {
+                  const uint32_t x0 = xr[t][0][2 * j], x1 = xr[t][0][2 * j + 1];
+                  xv = f32x4{__uint_as_float(x0 << 16), __uint_as_float(x0 & 0xffff0000u),
+                             __uint_as_float(x1 << 16), __uint_as_float(x1 & 0xffff0000u)};
+                }
+                dot += (xv[0] * acc[t][j][0] + xv[1] * acc[t][j][1]) +
+                       (xv[2] * acc[t][j][2] + xv[3] * acc[t][j][3]);
+              }
+              dot += __shfl_xor(dot, 16);
+              dot += __shfl_xor(dot, 32);
+              if (lg == 0 && row < rows)
+                dots[(((int64_t)bos + c * C + tok) * A.H + h) * 4 + 2 * tile + jh] = dot;
+              // + P[t,t] c_t: the lane that holds the pair hands it to the others of its row
+              const float pd = __shfl(diag[t], lr + 16 * (lr >> 2));
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int cc = 32 * jh + 8 * lg + 4 * j;
+                const char* cp = ba + L::off_c + row * (CT * 2) + (((cc >> 3) ^ swz<CT>(row)) << 4) +
+                                 ((cc & 7) << 1);
+#pragma unroll
+                for (int q = 0; q < NPL; ++q) {
+                  const u16x4 b = *reinterpret_cast<const u16x4*>(cp + q * L::CC);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) acc[t][j][e] += pd * bf16_bits_to_f32(b[e]);
+                }
+              }
+            }
+          }
+        }
+        if constexpr (WIDE) barrier_lds();
+        // the next a before the stores: loads behind them would be waited for with them
+        if constexpr (WIDE) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                ra[t][kk][e] = ra_next[t][kk][e];
+                hold(ra[t][kk][e]);
+              }
+        }
+        slot = slot + 1 == NBUF ? 0 : slot + 1;
+        const __amdgpu_buffer_rsrc_t ow = o_rows.of(c, rows);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int row = 16 * T[t] + lr;
+          const int off = (rev ? rows - 1 - row : row) * o_rows.stride + 8 * lg * (o_bf ? 2 : 4);
+          if (o_bf) {
+            u16x8 b;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) b[e] = f32_to_bf16_bits(acc[t][e >> 2][e & 3]);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, b), ow, off, 0, 0);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[t][j]), ow,
+                                                     off + 16 * j, 0, 0);
+          }
+        }
+      }
     };
-    if (nch > 0) load_a(chunk_of(0), ra);
-    for (int it = 0; it < nch; ++it) {
-      const int c = chunk_of(it);
-      const int rows = rows_in(c);
-      const int gb = it & 1;
-      const char* bb = buf_of(it);
-      const char* bc = bb + L::off_c;
-      const int64_t tok0 = (int64_t)bos + c * C;
-      const int tok = rev ? rows - 1 - orow : orow;
-      bf16x8 fa[KK][NPL];
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk) planes_of<WIDE>(ra[kk], a_bf, fa[kk]);
-      if (it + 1 < nch) load_a(chunk_of(it + 1), ra_next);
-      u32x4 xr[JT];  // x of this lane's row, for the dots
-      if constexpr (DOTS) {
-        if (dots) {
-          const __amdgpu_buffer_rsrc_t r = rows_of(W.x, x_bf, tok0, rows, h, CD, tile * CT, CT);
-          const int xs = (int)(W.x.stride * (x_bf ? 2 : 4));
-#pragma unroll
-          for (int j = 0; j < JT; ++j) {
-            if (x_bf) {
-              const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(
-                  r, orow < rows ? tok * xs + (16 * j + 4 * lg) * 2 : kOutside, 0, 0));
-              xr[j] = u32x4{v[0], v[1], 0, 0};
-            } else {
-              xr[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                  r, orow < rows ? tok * xs + (16 * j + 4 * lg) * 4 : kOutside, 0, 0));
-            }
-          }
-        }
-      }
-      barrier_lds();
-      // ---- scores of row tile i against the tokens 0 .. 16i + 15, transposed
-      bf16x8 fp[2][NPP];
-      float diag = 0.f;
-      const float rh = s_gh[gb][orow], rl = s_gl[gb][orow];
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        if (2 * ks > i) continue;
-        f32x4 p0 = {0.f, 0.f, 0.f, 0.f}, p1 = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-          const int blk = ((4 * kk + lg) ^ swB) << 4;
-          bf16x8 f0[NPL], f1[NPL];
-#pragma unroll
-          for (int p = 0; p < NPL; ++p) {
-            f0[p] = *reinterpret_cast<const bf16x8*>(bb + p * L::BB + (32 * ks + lr) * (KD * 2) + blk);
-            f1[p] = *reinterpret_cast<const bf16x8*>(bb + p * L::BB + (32 * ks + 16 + lr) * (KD * 2) + blk);
-          }
-          mma_planes<NPL, NPL>(f0, fa[kk], p0);
-          mma_planes<NPL, NPL>(f1, fa[kk], p1);  // masked where it lies behind the rows
-        }
-        f32x8 pv;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int s0 = 32 * ks + 16 * half + 4 * lg;
-          const f32x4 sh = *reinterpret_cast<const f32x4*>(&s_gh[gb][s0]);
-          const f32x4 sl = *reinterpret_cast<const f32x4*>(&s_gl[gb][s0]);
-          const f32x4 v = half ? p1 : p0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = v[e] * A.scale * ex2((rh - sh[e]) + (rl - sl[e]));
-            if constexpr (DOTS) {
-              if (s0 + e == orow) diag = x;
-              pv[4 * half + e] = (dots ? s0 + e < orow : s0 + e <= orow) ? x : 0.f;
-            } else {
-              pv[4 * half + e] = s0 + e <= orow ? x : 0.f;
-            }
-          }
-        }
-        split8<NPP>(pv, fp[ks]);
-      }
-      // ---- out^T = S^T a^T, the rows' decay, + c^T P^T
-      f32x4 acc[JT];
-      const float rowf = s_row[gb][orow];
-      const char* sp = lds + L::off_s + (L::NSB == 1 ? 0 : gb) * (NPS * L::SS) + lane * 16;
-#pragma unroll
-      for (int j = 0; j < JT; ++j) {
-        acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-          bf16x8 fs[NPS];
-#pragma unroll
-          for (int k = 0; k < NPS; ++k)
-            fs[k] = *reinterpret_cast<const bf16x8*>(sp + k * L::SS + (j * KK + kk) * 1024);
-          mma_planes<NPS, NPL>(fs, fa[kk], acc[j]);
-        }
-        acc[j] *= rowf;
-      }
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        if (2 * ks > i) continue;
-#pragma unroll
-        for (int j = 0; j < JT; ++j) {
-          bf16x8 fc[NPL];
-          read_c(bc, j, ks, fc);
-          mma_planes<NPL, NPP>(fc, fp[ks], acc[j]);
-        }
-      }
-      if constexpr (DOTS) {
-        if (dots) {
-          // x_t . out_t over the tile's columns, then the pair (t, t)
-          float dot = 0.f;
-#pragma unroll
-          for (int j = 0; j < JT; ++j) {
-            f32x4 xv = __builtin_bit_cast(f32x4, xr[j]);
-            if (x_bf) {
-              xv = f32x4{__uint_as_float(xr[j][0] << 16), __uint_as_float(xr[j][0] & 0xffff0000u),
-                         __uint_as_float(xr[j][1] << 16), __uint_as_float(xr[j][1] & 0xffff0000u)};
-            }
-            dot += (xv[0] * acc[j][0] + xv[1] * acc[j][1]) + (xv[2] * acc[j][2] + xv[3] * acc[j][3]);
-          }
-          dot += __shfl_xor(dot, 16);
-          dot += __shfl_xor(dot, 32);
-          if (lg == 0 && orow < rows) dots[((tok0 + tok) * A.H + h) * 2 + tile] = dot;
-          // + P[t,t] c_t: the lane that holds the pair hands it to the others of its row
-          const float pd = __shfl(diag, lr + 16 * (lr >> 2));
-#pragma unroll
-          for (int j = 0; j < JT; ++j) {
-            const int cc = 16 * j + 4 * lg;
-            const char* cp = bc + orow * (CT * 2) + (((cc >> 3) ^ swz<CT>(orow)) << 4) + ((cc & 7) << 1);
-#pragma unroll
-            for (int p = 0; p < NPL; ++p) {
-              const u16x4 b = *reinterpret_cast<const u16x4*>(cp + p * L::CC);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[j][e] += pd * bf16_bits_to_f32(b[e]);
-            }
-          }
-        }
-      }
-      if constexpr (L::NBUF == 1) barrier_lds();
-      const int64_t ld = (int64_t)A.H * CD;
-      const int out_es = o_bf ? 2 : 4;
-      const __amdgpu_buffer_rsrc_t ow =
-          buffer_over(static_cast<char*>(W.out) + (tok0 * ld + (int64_t)h * CD + tile * CT) * out_es,
-                      (uint32_t)(((rows - 1) * ld + CT) * out_es));
-      const int off = orow < rows ? (int)((tok * ld + 4 * lg) * out_es) : kOutside;
-      if (o_bf) {
-#pragma unroll
-        for (int j = 0; j < JT; ++j) {
-          const u16x4 b = {f32_to_bf16_bits(acc[j][0]), f32_to_bf16_bits(acc[j][1]),
-                           f32_to_bf16_bits(acc[j][2]), f32_to_bf16_bits(acc[j][3])};
-          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, b), ow, off + 32 * j, 0, 0);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < JT; ++j)
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[j]), ow, off + 64 * j,
-                                                 0, 0);
-      }
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-        for (int e = 0; e < (WIDE ? 2 : 1); ++e) ra[kk][e] = ra_next[kk][e];
-    }
+    if (w & 2) output(std::integral_constant<int, 1>{});
+    else output(std::integral_constant<int, 0>{});
   }
 }
 
@@ -777,7 +1048,7 @@ __global__ void __launch_bounds__(NTHR) scan_kernel(Args A) {
   const int nseg = (nch + A.seg_chunks - 1) / A.seg_chunks;
   const int64_t slot0 = seg_slot(A, n, bos);
   const int ch = 32 * (t >> 1) + 8 * lg + 4 * (t & 1);
-  const int col = tile * CT + 16 * w + lr;
+  const int col = tile * CT + 32 * (w >> 1) + 8 * (lr >> 2) + 4 * (w & 1) + (lr & 3);  // as in the walk
   f32x4 S = {0.f, 0.f, 0.f, 0.f};
   if (W.s_in) {
     const int64_t sl = W.in_idx ? (int64_t)W.in_idx[n] : n;
@@ -864,10 +1135,12 @@ __global__ void __launch_bounds__(NTHR) dg_kernel(Args A, const float* dotq, con
   for (int hi = t_hi; hi > t_lo; hi -= NTHR) {
     const int t = hi - 1 - tid;
     double x = 0.0;
-    if (t >= t_lo) {  // one partial dot a column tile of 64 channels
-      const int64_t at = (((int64_t)bos + t) * A.H + h) * 2;
-      x = (double)dotq[at] - (double)dotk[at];
-      if (dk > CT) x += (double)dotq[at + 1] - (double)dotk[at + 1];
+    if (t >= t_lo) {  // one partial dot per 32 channels
+      const int64_t at = (((int64_t)bos + t) * A.H + h) * 4;
+      const f32x4 a = *reinterpret_cast<const f32x4*>(dotq + at);
+      const f32x4 b = *reinterpret_cast<const f32x4*>(dotk + at);
+      x = ((double)a[0] - (double)b[0]) + ((double)a[1] - (double)b[1]);
+      if (dk > CT) x += ((double)a[2] - (double)b[2]) + ((double)a[3] - (double)b[3]);
     }
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -946,25 +1219,31 @@ __global__ void __launch_bounds__(NTHR) group_sum_kernel(Args A, const float* hq
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-template <bool WIDE, int KD, bool FULL, bool DOTS>
+template <bool WIDE, int KD, bool FULL, bool DOTS, int PL>
 hipError_t launch_walk_kd(const Args& A, int walks, hipStream_t s) {
   const int64_t blocks =
-      cdiv((int64_t)A.N * A.nseg * A.H, 8) * 8 * (A.walk[0].s_elems / KD / CT);
+      (int64_t)A.N * A.nseg * cdiv(A.H, 8) * 8 * (A.walk[0].s_elems / KD / CT);
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  walk_kernel<WIDE, KD, FULL, DOTS><<<dim3((unsigned)blocks, walks),
-                                      Waves<WIDE, FULL>::threads, 0, s>>>(A);
+  walk_kernel<WIDE, KD, FULL, DOTS, PL><<<dim3((unsigned)blocks, walks),
+                                          Waves<WIDE, FULL>::threads, 0, s>>>(A);
   return hipGetLastError();
 }
-// `walks` walks of one contraction width kd
+// `walks` walks of one contraction width kd.  exact: S and P as two bf16 values
+// for out too (fp32 outputs, and the dots that dg is made of).
 template <bool DOTS>
-hipError_t launch_walk(const Args& A, int walks, bool wide, int kd, bool full, hipStream_t s) {
-#define KDA_LW(WD, KDV)                                             \
-  return full ? launch_walk_kd<WD, KDV, true, DOTS>(A, walks, s)    \
-              : launch_walk_kd<WD, KDV, false, false>(A, walks, s)
-  if (wide && kd == 128) KDA_LW(true, 128);
-  if (wide) KDA_LW(true, 64);
-  if (kd == 128) KDA_LW(false, 128);
-  KDA_LW(false, 64);
+hipError_t launch_walk(const Args& A, int walks, bool wide, int kd, bool full, bool exact,
+                       hipStream_t s) {
+#define KDA_LW(KDV)                                                              \
+  do {                                                                           \
+    if (wide)                                                                    \
+      return full ? launch_walk_kd<true, KDV, true, DOTS, 3>(A, walks, s)        \
+                  : launch_walk_kd<true, KDV, false, false, 3>(A, walks, s);     \
+    if (!full) return launch_walk_kd<false, KDV, false, false, 1>(A, walks, s);  \
+    if (DOTS || exact) return launch_walk_kd<false, KDV, true, DOTS, 2>(A, walks, s); \
+    if constexpr (!DOTS) return launch_walk_kd<false, KDV, true, false, 1>(A, walks, s); \
+  } while (0)
+  if (kd == 128) KDA_LW(128);
+  KDA_LW(64);
 #undef KDA_LW
 }
 
@@ -1020,8 +1299,8 @@ struct BackwardWs {
   BackwardWs(void* ws, int64_t T_tot, int N, int H, int Hk, int dk, int dv, int seg, bool cut) {
     Carve c{static_cast<char*>(ws)};
     const int64_t slots = slots_of(T_tot, N, seg), st = slots * H * dk * dv;
-    dotq = c.take(T_tot * H * 2);
-    dotk = c.take(T_tot * H * 2);
+    dotq = c.take(T_tot * H * 4);
+    dotk = c.take(T_tot * H * 4);
     ends_s = c.take(st);
     ends_d = c.take(st);
     dg_part = c.take(slots * H * 2);
@@ -1091,11 +1370,11 @@ hipError_t launch_prefill(const Problem& p, const Operand& q, const Operand& k, 
     W.seg_decay = f.decay;
   }
   if (A.nseg > 1) {
-    hipError_t e = launch_walk<false>(A, 1, wide, p.dk, false, s);
+    hipError_t e = launch_walk<false>(A, 1, wide, p.dk, false, !o_bf16, s);
     if (e == hipSuccess) e = launch_scan(A, 1, p.dk, s);
     if (e != hipSuccess) return e;
   }
-  return launch_walk<false>(A, 1, wide, p.dk, true, s);
+  return launch_walk<false>(A, 1, wide, p.dk, true, !o_bf16, s);
 }
 
 namespace {
@@ -1168,19 +1447,17 @@ hipError_t launch_backward(const Problem& p, const Operand& q, const Operand& k,
   const bool wide = !(q.bf16 && k.bf16 && v.bf16 && (d_o.bf16 || !d_o.p));
   A.walk[0] = wq;
   A.walk[1] = wk;
-  A.walk[2] = wv;
-  Args B = A;  // dk != dv: the walk of dv contracts over another width
+  Args B = A;  // dv needs no dots (and for dk != dv contracts over another width)
   B.walk[0] = wv;
-  const bool same = DK == DV;
   for (int phase = A.nseg > 1 ? 0 : 2; phase < 3; ++phase) {
     hipError_t e;
     if (phase == 1) {
-      e = launch_scan(A, same ? 3 : 2, DV, s);
-      if (e == hipSuccess && !same) e = launch_scan(B, 1, DK, s);
+      e = launch_scan(A, 2, DV, s);
+      if (e == hipSuccess) e = launch_scan(B, 1, DK, s);
     } else {
       const bool full = phase == 2;
-      e = launch_walk<true>(A, same ? 3 : 2, wide, DV, full, s);
-      if (e == hipSuccess && !same) e = launch_walk<true>(B, 1, wide, DK, full, s);
+      e = launch_walk<true>(A, 2, wide, DV, full, true, s);
+      if (e == hipSuccess) e = launch_walk<false>(B, 1, wide, DK, full, !grad_bf16, s);
     }
     if (e != hipSuccess) return e;
   }

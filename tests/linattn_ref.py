@@ -14,9 +14,12 @@ rounding, where rel counts, per term and in units of u = 2^-24 (fp32):
   - the decays: the exponent is a difference of fp32 pairs whose size matters up
     to 104 (exp(-104) is 0 in fp32), 104 u, through two such factors, and an ulp
     or two of the exponential: 256
-  - factors that enter the products as p bf16 values: 2^-8 per value, 2^-8p.  For
-    bf16 inputs the scores and the state in the readout have p = 2 (2^-16 each,
-    2^-15 together); everything else p = 3 (a few u).
+  - factors that enter the products as p bf16 values are off by 2^-8 per value,
+    2^-8p of themselves.  For bf16 inputs each term of o holds one such factor, an
+    element of the scores or of the state: p = 1 where the output is bf16 (2^-8),
+    p = 2 where it is fp32 (2^-16, 2^-15 with what the first product passes on to the
+    second).  dq and dk, whose dots make dg, have p = 2 whatever their type; dv is
+    like o.  Everything else has p = 3 (a few u).
 """
 import torch
 
@@ -91,10 +94,15 @@ def _abs(x):
     return None if x is None else x.double().abs()
 
 
-def rel_of(q, v, cu, wide):
+def rel_of(q, v, cu, values):
+    """values: bf16 values a factor of the output's products is made of."""
     d = max(q.shape[2], v.shape[2])
     chunks = max([-(-(b - a) // 64) for a, b in zip(cu, cu[1:])] + [1])
-    return (2 * d + 64 + 4 * chunks + 256) * U + (0.0 if wide else 2.0 ** -15)
+    return (2 * d + 64 + 4 * chunks + 256) * U + {1: 2.0 ** -8, 2: 2.0 ** -15, 3: 0.0}[values]
+
+
+def _values(wide, dtype):
+    return 3 if wide else 1 if dtype == torch.bfloat16 else 2
 
 
 def check(name, got, want, size, rel, dtype):
@@ -112,12 +120,12 @@ def check_forward(o, S, q, k, v, g, cu, S0=None, scale=1.0, o_rows=None):
     want, want_S = forward(q, k, v, g, cu, S0, scale)
     size, size_S = forward(_abs(q), _abs(k), _abs(v), g, cu, _abs(S0), abs(scale))
     wide = q.dtype == torch.float32
-    rel = rel_of(q, v, cu, wide)
+    rel = rel_of(q, v, cu, _values(wide, o.dtype))
     m = want.shape[0] if o_rows is None else o_rows
     r = [check("o", o[:m], want[:m], size[:m], rel, o.dtype)]
     if S is not None:
-        # the state itself never passes a two-value rounding
-        r.append(check("state", S, want_S, size_S, rel_of(q, v, cu, True), S.dtype))
+        # the state itself is made of three-value factors
+        r.append(check("state", S, want_S, size_S, rel_of(q, v, cu, 3), S.dtype))
     return r
 
 
@@ -126,9 +134,10 @@ def check_backward(got, q, k, v, g, cu, d_o=None, S0=None, dS=None, scale=1.0):
     size = backward(_abs(q), _abs(k), _abs(v), g, cu, _abs(d_o), _abs(S0), _abs(dS), abs(scale),
                     signs=False)
     wide = q.dtype == torch.float32 or (d_o is not None and d_o.dtype == torch.float32)
-    rel = rel_of(q, v, cu, wide)
+    rel = rel_of(q, v, cu, 3 if wide else 2)
     # dg: 128 more fp32 terms a dot and the state's inner product of 16,384 / 256 a lane
-    rels = [rel, rel, rel, rel + 256 * U, rel_of(q, v, cu, True)]
+    rels = [rel, rel, rel_of(q, v, cu, _values(wide, got[2].dtype)), rel + 256 * U,
+            rel_of(q, v, cu, 3)]
     out = []
     for name, x, w, s, r in zip(("dq", "dk", "dv", "dg", "dS0"), got, want, size, rels):
         if x is not None:

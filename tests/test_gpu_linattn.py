@@ -161,7 +161,7 @@ def test_pool_prefill_then_decode(sdt):
     keep = [i for i in range(3) if idx[i] >= 0]
     _, wantS = ref.forward(q, k, v, g, cu, S0)
     _, absS = ref.forward(q.abs(), k.abs(), v.abs(), g, cu, S0.abs())
-    ref.check("pool", got, wantS[keep], absS[keep], ref.rel_of(q, v, cu, True), sdt)
+    ref.check("pool", got, wantS[keep], absS[keep], ref.rel_of(q, v, cu, 3), sdt)
     for step in range(3):
         q1, k1, v1, g1, _, _ = _draw([N], H, Hk, 128, 128, BF, "mild", 50 + step, state=False)
         before = P.cpu()
