@@ -40,9 +40,13 @@
 //                 nothing else: under load a wave spends thousands of cycles in
 //                 the issue of its loads, which no other wave then waits for.
 //   decay wave    the next chunk's decays.
-// S is the only thing handed between the kinds, so one barrier a chunk is
-// enough.  (fp32 operands, three values each: the state waves copy, with one
-// buffer and a second barrier.)
+// S is the only thing handed between the kinds, so with two of its buffers one
+// barrier a chunk is enough.  The walks with dots keep S as three values, and two
+// buffers of those do not fit: there the output waves read S first, and a second
+// barrier lets the state waves overwrite it while the scores are made (a second
+// buffer in the place of a's, which then goes straight to registers: backward of
+// T = 4096 x 96 679 against 545 us).  fp32 operands, three values each: the state
+// waves copy, with one buffer and a second barrier.
 // What bounds it: a layer of 96 heads gives 192 workgroups for 256 CUs, each with
 // T / 64 chunks to go through one after the other; in a chunk LDS moves about
 // 250 KB at 128 B a cycle (stores into it at 79), and the matrix and the vector
@@ -64,10 +68,10 @@
 // that add up to them).  The decayed c, of which the fp32 state is made, enters as
 // three bf16 values; S and P, of which out is made, as one where out is bf16 (each
 // element is then off by at most 2^-8 of itself, as the rounding of out is), as
-// two where out is fp32 or makes dg;
-// accumulators, decays and the state are fp32, gamma is summed in 64 bits and
-// kept as two fp32 values, so that a strong decay early in a chunk costs the
-// weak ones behind it no digits.
+// two where out is fp32, as three where it makes dg (launch_walk).  Accumulators,
+// decays and the state are fp32; gamma is summed in 64 bits and kept as two fp32
+// values, so that a strong decay early in a chunk costs the weak ones behind it no
+// digits.
 #include <type_traits>
 
 #include "chunk_common.hpp"
@@ -223,19 +227,21 @@ __device__ __forceinline__ int64_t seg_slot(const Args& A, int n, int bos) {
   return bos / (C * A.seg_chunks) + n;
 }
 
-template <bool WIDE, int KD, int PL>
+// PS: bf16 values of a state's element (see walk_kernel)
+template <bool WIDE, int KD, bool DOTS, int PS>
 struct Lds {
   static constexpr int NPL = WIDE ? 3 : 1;          // planes of an operand
-  static constexpr int NBUF = WIDE ? 1 : PL == 1 ? 3 : 2;  // chunks of a, b and c
-  static constexpr int NSB = WIDE ? 1 : 2;          // states
+  static constexpr int NBUF = WIDE ? 1 : PS == 1 ? 3 : 2;  // chunks of a, b and c
+  static constexpr int NSB = PS == 3 ? 1 : 2;       // states
   static constexpr int AB = C * KD * 2;             // one plane of a or b
   static constexpr int CC = C * CT * 2;             // one plane of c
   static constexpr int SS = KD * CT * 2;            // one plane of the state
   static constexpr int off_b = WIDE ? 0 : AB;       // (fp32: a goes straight to registers)
   static constexpr int off_c = off_b + NPL * AB;
-  static constexpr int buf = off_c + NPL * CC;
+  static constexpr int off_x = off_c + NPL * CC;    // x of the dots (fp32: straight to registers)
+  static constexpr int buf = off_x + (DOTS && !WIDE ? CC : 0);
   static constexpr int off_s = NBUF * buf;
-  static constexpr int total = off_s + NSB * PL * SS;
+  static constexpr int total = off_s + NSB * PS * SS;
 };
 // Waves of a workgroup: state waves 0 .. 3, output waves 4 .. 7, then the helpers.
 template <bool WIDE, bool FULL>
@@ -362,7 +368,7 @@ __device__ __forceinline__ void wait_vm_le() {
 // element of S and P in the products for out.
 template <bool WIDE, int KD, bool FULL, bool DOTS, int PL>
 __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(Args A) {
-  using L = Lds<WIDE, KD, PL>;
+  using L = Lds<WIDE, KD, DOTS, PL>;
   using WV = Waves<WIDE, FULL>;
   constexpr int NPL = L::NPL, NBUF = L::NBUF;
   constexpr int NPS = PL, NPP = PL, NPC = 3;
@@ -625,7 +631,7 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
         });
         }
       if (ends && !rev) dump(c);
-      if constexpr (WIDE) barrier_lds();
+      if constexpr (WIDE || (FULL && L::NSB == 1)) barrier_lds();
       write_state(L::NSB == 2 ? gb ^ 1 : 0);
       if constexpr (WIDE) {
         write_chunk(lds, rb[0], rc[0]);
@@ -674,6 +680,7 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
       g2 = load_decay(2);
       for (int it = 0; it < nch; ++it) {
         barrier_lds();
+        if constexpr (FULL && L::NSB == 1) barrier_lds();
         const float g = g1;
         g1 = g2;
         g2 = load_decay(it + 3);
@@ -686,10 +693,11 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
     if (w >= WV::copy) {
       // ================================================= copy waves: a and b, half of c each
       const int half = w - WV::copy;
-      constexpr int OPS = (FULL ? L::AB : L::AB / 2) / 1024 + L::CC / 2048;  // instructions a chunk
+      constexpr int OPS = (FULL ? L::AB : L::AB / 2) / 1024 + L::CC / 2048 * (DOTS ? 2 : 1);
       static_assert(2 * OPS < 64, "two chunks in flight");
       const Operand& ab = FULL && half == 0 ? W.a : W.b;
       const Rows ab_rows(ab, true, bos, h, KD, 0, KD), c_rows(W.c, true, bos, h, CD, tile * CT, CT);
+      const Rows x_rows(W.x, true, bos, h, CD, tile * CT, CT);
       auto issue = [&](int it, int slot) {
         const int c = chunk_of(it), rows = rows_in(it);
         char* p = lds + slot * L::buf;
@@ -698,6 +706,8 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
         else
           copy_rows<KD, 2>(ab_rows.of(c, rows), p + L::off_b, ab_rows.stride, rows, rev, lane, 32 * half);
         copy_rows<CT, 2>(c_rows.of(c, rows), p + L::off_c, c_rows.stride, rows, rev, lane, 32 * half);
+        if constexpr (DOTS)
+          copy_rows<CT, 2>(x_rows.of(c, rows), p + L::off_x, x_rows.stride, rows, rev, lane, 32 * half);
       };
       // chunks it .. it + NBUF - 2 are asked for before barrier `it`; the buffer of
       // chunk it - 1 is free behind it
@@ -708,6 +718,7 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
         wait_vm_le<(NBUF - 2) * OPS>();  // chunk `it` has arrived
         chunk::barrier_nofence();
         issue(it + NBUF - 1, slot);      // (none behind the last chunk: reads zeros)
+        if constexpr (FULL && L::NSB == 1) chunk::barrier_nofence();
         slot = slot + 1 == NBUF ? 0 : slot + 1;
       }
       wait_vm_le<0>();
@@ -773,7 +784,7 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
           load_a(it + 1, ra_next);
         }
         u32x4 xr[2][2];  // x of this lane's rows, for the dots
-        if constexpr (DOTS) {
+        if constexpr (DOTS && WIDE) {
           const __amdgpu_buffer_rsrc_t r = x_rows.of(c, dots ? rows : 0);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -916,6 +927,25 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
           weigh(0);
           weigh(1);
           mul_s(0, KK);
+        } else if constexpr (L::NSB == 1 && !WIDE) {
+          // the products with the state first: behind the second barrier the state
+          // waves overwrite it
+          read_s(0, KK / 2);
+          mul_s(0, KK / 2);
+          read_s(KK / 2, KK);
+          mul_s(KK / 2, KK);
+          barrier_lds();
+          read_k(0);
+          read_k(1);
+          read_w(0);
+          read_w(1);
+          mul_k(0);
+          read_k(2);
+          if constexpr (NU == 4) read_k(3);
+          weigh(0);
+          mul_k(2);
+          read_c2();
+          weigh(1);
         } else {
           // one group of operands after the other: all at once they do not fit the registers
           read_k(0);
@@ -961,6 +991,9 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
               for (int j = 0; j < 2; ++j) {
                 f32x4 xv = __builtin_bit_cast(f32x4, xr[t][j]);
                 if (x_bf) {
+                  if constexpr (!WIDE)
+                    xr[t][0] = *reinterpret_cast<const u32x4*>(
+                        ba + L::off_x + row * (CT * 2) + (((4 * jh + lg) ^ swz<CT>(row)) << 4));
                   const uint32_t x0 = xr[t][0][2 * j], x1 = xr[t][0][2 * j + 1];
                   xv = f32x4{__uint_as_float(x0 << 16), __uint_as_float(x0 & 0xffff0000u),
                              __uint_as_float(x1 << 16), __uint_as_float(x1 & 0xffff0000u)};
@@ -1228,19 +1261,28 @@ hipError_t launch_walk_kd(const Args& A, int walks, hipStream_t s) {
                                           Waves<WIDE, FULL>::threads, 0, s>>>(A);
   return hipGetLastError();
 }
-// `walks` walks of one contraction width kd.  exact: S and P as two bf16 values
-// for out too (fp32 outputs, and the dots that dg is made of).
+// `walks` walks of one contraction width kd.  S and P enter the products for out as
+//   three values  with dots: dg is a small difference of their sums, and for one
+//                 decay a head a sum of those; with two values it was up to 3e-5 off
+//   two           out is fp32, or bf16 and the call has at most one chunk of tokens,
+//                 which costs nothing there (H = 96: T = 64 7.6 against 7.5 us, T = 256
+//                 14.3 against 13.3, T = 4096 146 against 124) and where the few
+//                 roundings do not average out
+//   one           out is bf16: off by 2.3e-3 of its norm where bf16's own rounding is
+//                 1.7e-3 off
 template <bool DOTS>
-hipError_t launch_walk(const Args& A, int walks, bool wide, int kd, bool full, bool exact,
+hipError_t launch_walk(const Args& A, int walks, bool wide, int kd, bool full, bool out_bf16,
                        hipStream_t s) {
+  const bool two = !out_bf16 || A.T_tot <= C;
 #define KDA_LW(KDV)                                                              \
   do {                                                                           \
     if (wide)                                                                    \
       return full ? launch_walk_kd<true, KDV, true, DOTS, 3>(A, walks, s)        \
                   : launch_walk_kd<true, KDV, false, false, 3>(A, walks, s);     \
     if (!full) return launch_walk_kd<false, KDV, false, false, 1>(A, walks, s);  \
-    if (DOTS || exact) return launch_walk_kd<false, KDV, true, DOTS, 2>(A, walks, s); \
-    if constexpr (!DOTS) return launch_walk_kd<false, KDV, true, false, 1>(A, walks, s); \
+    if constexpr (DOTS) return launch_walk_kd<false, KDV, true, true, 3>(A, walks, s); \
+    else if (two) return launch_walk_kd<false, KDV, true, false, 2>(A, walks, s); \
+    else return launch_walk_kd<false, KDV, true, false, 1>(A, walks, s);         \
   } while (0)
   if (kd == 128) KDA_LW(128);
   KDA_LW(64);
@@ -1370,11 +1412,11 @@ hipError_t launch_prefill(const Problem& p, const Operand& q, const Operand& k, 
     W.seg_decay = f.decay;
   }
   if (A.nseg > 1) {
-    hipError_t e = launch_walk<false>(A, 1, wide, p.dk, false, !o_bf16, s);
+    hipError_t e = launch_walk<false>(A, 1, wide, p.dk, false, o_bf16, s);
     if (e == hipSuccess) e = launch_scan(A, 1, p.dk, s);
     if (e != hipSuccess) return e;
   }
-  return launch_walk<false>(A, 1, wide, p.dk, true, !o_bf16, s);
+  return launch_walk<false>(A, 1, wide, p.dk, true, o_bf16, s);
 }
 
 namespace {
@@ -1456,8 +1498,8 @@ hipError_t launch_backward(const Problem& p, const Operand& q, const Operand& k,
       if (e == hipSuccess) e = launch_scan(B, 1, DK, s);
     } else {
       const bool full = phase == 2;
-      e = launch_walk<true>(A, 2, wide, DV, full, true, s);
-      if (e == hipSuccess) e = launch_walk<false>(B, 1, wide, DK, full, !grad_bf16, s);
+      e = launch_walk<true>(A, 2, wide, DV, full, grad_bf16, s);
+      if (e == hipSuccess) e = launch_walk<false>(B, 1, wide, DK, full, grad_bf16, s);
     }
     if (e != hipSuccess) return e;
   }

@@ -18,8 +18,8 @@ rounding, where rel counts, per term and in units of u = 2^-24 (fp32):
     2^-8p of themselves.  For bf16 inputs each term of o holds one such factor, an
     element of the scores or of the state: p = 1 where the output is bf16 (2^-8),
     p = 2 where it is fp32 (2^-16, 2^-15 with what the first product passes on to the
-    second).  dq and dk, whose dots make dg, have p = 2 whatever their type; dv is
-    like o.  Everything else has p = 3 (a few u).
+    second).  dv is like o; dq and dk, whose dots make dg, and everything else
+    have p = 3 (a few u).
 """
 import torch
 
@@ -134,7 +134,7 @@ def check_backward(got, q, k, v, g, cu, d_o=None, S0=None, dS=None, scale=1.0):
     size = backward(_abs(q), _abs(k), _abs(v), g, cu, _abs(d_o), _abs(S0), _abs(dS), abs(scale),
                     signs=False)
     wide = q.dtype == torch.float32 or (d_o is not None and d_o.dtype == torch.float32)
-    rel = rel_of(q, v, cu, 3 if wide else 2)
+    rel = rel_of(q, v, cu, 3)
     # dg: 128 more fp32 terms a dot and the state's inner product of 16,384 / 256 a lane
     rels = [rel, rel, rel_of(q, v, cu, _values(wide, got[2].dtype)), rel + 256 * U,
             rel_of(q, v, cu, 3)]
