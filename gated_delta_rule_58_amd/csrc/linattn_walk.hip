@@ -181,6 +181,14 @@ __device__ __forceinline__ double of_lane(double x, int l) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
+// sum of x over the lanes l, l ^ 16, l ^ 32, l ^ 48
+__device__ __forceinline__ float sum_rows(float x) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
 struct Walk {
   Operand a, b, c, x;       // x: the tensor of the dots (with dots)
   const void* s_in;         // entry states, or null (zeros)
@@ -199,7 +207,8 @@ struct Walk {
 };
 
 struct Args {
-  Walk walk[2];
+  Walk walk[3];
+  int first;           // walk of blockIdx.y = 0
   Decay g;
   const int32_t* cu;   // null: equal lengths
   int N, T_tot, H, eq_len;
@@ -242,6 +251,17 @@ struct Lds {
   static constexpr int buf = off_x + (DOTS && !WIDE ? CC : 0);
   static constexpr int off_s = NBUF * buf;
   static constexpr int total = off_s + NSB * PS * SS;
+};
+// Decays of a chunk (of two, in turn), with gamma_i the sum up to row tile i's
+// first row; behind everything else in LDS.
+struct alignas(16) Decays {
+  float gh[2][C], gl[2][C];  // gamma as two floats
+  float row[2][C];           // e^(gamma_r - gamma_i), r in tile i
+  float tok[2][3][C];        // scale e^(gamma_i - gamma_s), tile i = 1 ..
+  float col[2][C];           // e^(gamma_end - gamma_s)
+  float tile[2][4];          // e^gamma_i
+  float end[2];              // e^gamma_end
+  int seq[2];
 };
 // Waves of a workgroup: state waves 0 .. 3, output waves 4 .. 7, then the helpers.
 template <bool WIDE, bool FULL>
@@ -367,31 +387,33 @@ __device__ __forceinline__ void wait_vm_le() {
 // and decay.  DOTS: the backward's walks.  PL: bf16 values that stand for an
 // element of S and P in the products for out.
 template <bool WIDE, int KD, bool FULL, bool DOTS, int PL>
-__global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(Args A) {
+constexpr int lds_bytes() {
+  using L = Lds<WIDE, KD, DOTS, PL>;
+  return (FULL ? L::total : L::off_s) + (int)sizeof(Decays);
+}
+template <bool WIDE, int KD, bool FULL, bool DOTS, int PL>
+__device__ __forceinline__ void walk(const Args& A, const Walk& W, int block, char* lds) {
   using L = Lds<WIDE, KD, DOTS, PL>;
   using WV = Waves<WIDE, FULL>;
   constexpr int NPL = L::NPL, NBUF = L::NBUF;
   constexpr int NPS = PL, NPP = PL, NPC = 3;
   constexpr int KK = KD / 32;   // contraction steps over the channels
   constexpr int NT = KD / 16;   // state tiles a wave
-  __shared__ __attribute__((aligned(16))) char lds[FULL ? L::total : L::off_s];
-  // the chunk's decays, with gamma_i the sum up to row tile i's first row:
-  __shared__ __attribute__((aligned(16))) float s_gh[2][C], s_gl[2][C];  // gamma as two floats
-  __shared__ __attribute__((aligned(16))) float s_row[2][C];     // e^(gamma_r - gamma_i), r in tile i
-  __shared__ __attribute__((aligned(16))) float s_tok[2][3][C];  // scale e^(gamma_i - gamma_s), tile i = 1 ..
-  __shared__ __attribute__((aligned(16))) float s_col[2][C];     // e^(gamma_end - gamma_s)
-  __shared__ float s_tile[2][4];                                 // e^gamma_i
-  __shared__ float s_end[2];                                     // e^gamma_end
-  __shared__ int s_seq[1];
-
-  const Walk& W = A.walk[blockIdx.y];
+  Decays& D = *reinterpret_cast<Decays*>(lds + (FULL ? L::total : L::off_s));
+  auto& s_gh = D.gh;
+  auto& s_gl = D.gl;
+  auto& s_row = D.row;
+  auto& s_tok = D.tok;
+  auto& s_col = D.col;
+  auto& s_tile = D.tile;
+  auto& s_end = D.end;
   const int tid = threadIdx.x;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lane = tid & 63, lr = lane & 15, lg = lane >> 4;
   const bool rev = W.reverse;
   const bool a_bf = !WIDE || W.a.bf16, b_bf = !WIDE || W.b.bf16, c_bf = !WIDE || W.c.bf16;
 
-  // ---- blockIdx.x -> (sequence, segment, head, tile).  Workgroups go to the XCDs
+  // ---- block -> (sequence, segment, head, tile).  Workgroups go to the XCDs
   // in turn; an XCD gets hb = ceil(H / 8) consecutive heads of every segment, with
   // their tiles.  (Every eighth head instead: the tokens of a head are H rows
   // apart, so for H a multiple of 16 its rows and those of the heads 16 further
@@ -399,15 +421,15 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
   const int CD = static_cast<int>(W.s_elems / KD);
   const int ntile = CD / CT;
   const int hb = (A.H + 7) >> 3;
-  int id = blockIdx.x >> 3;
+  int id = block >> 3;
   const int tile = id % ntile;
   id /= ntile;
-  const int h = (blockIdx.x & 7) * hb + id % hb;
+  const int h = (block & 7) * hb + id % hb;
   id /= hb;
   const int seg = id % A.nseg;
   int n = id / A.nseg;
   if (h >= A.H) return;
-  if (A.cu) n = chunk::lpt_sequence(A.cu, A.N, A.T_tot, n, s_seq);
+  if (A.cu) n = chunk::lpt_sequence(A.cu, A.N, A.T_tot, n, D.seq);
   n = __builtin_amdgcn_readfirstlane(n);
   int bos, len;
   seq_range(A, n, bos, len);
@@ -733,7 +755,6 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
     // column tiles 2 jh and 2 jh + 1
     const int jh = w & 1;
     const bool x_bf = !WIDE || W.x.bf16, o_bf = W.out_bf16;
-    float* const dots = DOTS ? W.dots : nullptr;
     const Rows a_rows(W.a, a_bf, bos, h, KD, 0, KD);
     const Rows x_rows(W.x, x_bf, bos, h, CD, tile * CT + 32 * jh, 32);
     Operand out_op;
@@ -785,7 +806,7 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
         }
         u32x4 xr[2][2];  // x of this lane's rows, for the dots
         if constexpr (DOTS && WIDE) {
-          const __amdgpu_buffer_rsrc_t r = x_rows.of(c, dots ? rows : 0);
+          const __amdgpu_buffer_rsrc_t r = x_rows.of(c, rows);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const int row = 16 * T[t] + lr;
@@ -853,7 +874,8 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
         // Decays of the scores.  Tokens before row tile i: e^(gamma_r - gamma_i)
         // e^(gamma_i - gamma_s), both at most 1; tokens of the tile itself: the
         // difference of the sums, masked.
-        float rowf[2], tilef[2], rh[2], rl[2], diag[2];
+        float rowf[2], tilef[2], rh[2], rl[2];
+        bf16x8 fd[2][NPP];  // with dots: the pairs (t, t), which the dots leave out
         f32x4 tokf[2][3], sh[2], sl[2];
         auto read_w = [&](int t) {
           const int row = 16 * T[t] + lr, own = 16 * T[t] + 4 * lg;
@@ -875,17 +897,18 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
             if (u < T[t]) {
               p[t][u] *= tokf[t][u < 3 ? u : 0] * rowf[t];
             } else {
-              diag[t] = 0.f;
+              f32x8 own = {};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const float x = p[t][u][e] * A.scale * ex2((rh[t] - sh[t][e]) + (rl[t] - sl[t][e]));
                 if constexpr (DOTS) {
-                  if (s0 + e == row) diag[t] = x;
-                  p[t][u][e] = (dots ? s0 + e < row : s0 + e <= row) ? x : 0.f;
+                  own[4 * (u & 1) + e] = s0 + e == row ? x : 0.f;
+                  p[t][u][e] = s0 + e < row ? x : 0.f;
                 } else {
                   p[t][u][e] = s0 + e <= row ? x : 0.f;
                 }
               }
+              if constexpr (DOTS) split8<NPP>(own, fd[t]);
             }
           }
 #pragma unroll
@@ -980,47 +1003,37 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
                 if (2 * ks <= T[t]) acc[t][j] = mma_bf16(fc[j][ks][i], fp[t][ks][k], acc[t][j]);
           });
         if constexpr (DOTS) {
-          if (dots) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const int row = 16 * T[t] + lr;
-              const int tok = rev ? rows - 1 - row : row;
-              // x_t . out_t over the wave's columns, then the pair (t, t)
-              float dot = 0.f;
+          for (int t = 0; t < 2; ++t) {
+            const int row = 16 * T[t] + lr;
+            const int tok = rev ? rows - 1 - row : row;
+            // x_t . out_t over the wave's columns
+            float dot = 0.f;
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                f32x4 xv = __builtin_bit_cast(f32x4, xr[t][j]);
-                if (x_bf) {
-                  if constexpr (!WIDE)
-                    xr[t][0] = *reinterpret_cast<const u32x4*>(
-                        ba + L::off_x + row * (CT * 2) + (((4 * jh + lg) ^ swz<CT>(row)) << 4));
-                  const uint32_t x0 = xr[t][0][2 * j], x1 = xr[t][0][2 * j + 1];
-                  xv = f32x4{__uint_as_float(x0 << 16), __uint_as_float(x0 & 0xffff0000u),
-                             __uint_as_float(x1 << 16), __uint_as_float(x1 & 0xffff0000u)};
-                }
-                dot += (xv[0] * acc[t][j][0] + xv[1] * acc[t][j][1]) +
-                       (xv[2] * acc[t][j][2] + xv[3] * acc[t][j][3]);
+            for (int j = 0; j < 2; ++j) {
+              f32x4 xv = __builtin_bit_cast(f32x4, xr[t][j]);
+              if (x_bf) {
+                if constexpr (!WIDE)
+                  xr[t][0] = *reinterpret_cast<const u32x4*>(
+                      ba + L::off_x + row * (CT * 2) + (((4 * jh + lg) ^ swz<CT>(row)) << 4));
+                const uint32_t x0 = xr[t][0][2 * j], x1 = xr[t][0][2 * j + 1];
+                xv = f32x4{__uint_as_float(x0 << 16), __uint_as_float(x0 & 0xffff0000u),
+                           __uint_as_float(x1 << 16), __uint_as_float(x1 & 0xffff0000u)};
               }
-              dot += __shfl_xor(dot, 16);
-              dot += __shfl_xor(dot, 32);
-              if (lg == 0 && row < rows)
-                dots[(((int64_t)bos + c * C + tok) * A.H + h) * 4 + 2 * tile + jh] = dot;
-              // + P[t,t] c_t: the lane that holds the pair hands it to the others of its row
-              const float pd = __shfl(diag[t], lr + 16 * (lr >> 2));
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int cc = 32 * jh + 8 * lg + 4 * j;
-                const char* cp = ba + L::off_c + row * (CT * 2) + (((cc >> 3) ^ swz<CT>(row)) << 4) +
-                                 ((cc & 7) << 1);
-#pragma unroll
-                for (int q = 0; q < NPL; ++q) {
-                  const u16x4 b = *reinterpret_cast<const u16x4*>(cp + q * L::CC);
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) acc[t][j][e] += pd * bf16_bits_to_f32(b[e]);
-                }
-              }
+              dot += (xv[0] * acc[t][j][0] + xv[1] * acc[t][j][1]) +
+                     (xv[2] * acc[t][j][2] + xv[3] * acc[t][j][3]);
             }
+            dot = sum_rows(dot);
+            if (lg == 0 && row < rows)
+              W.dots[(((int64_t)bos + c * C + tok) * A.H + h) * 4 + 2 * tile + jh] = dot;
           }
+          for_planes<NPL, NPP>([&](int i, int k) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                acc[t][j] = mma_bf16(fc[j][T[t] >> 1][i], fd[t][k], acc[t][j]);
+          });
         }
         if constexpr (WIDE) barrier_lds();
         // the next a before the stores: loads behind them would be waited for with them
@@ -1060,13 +1073,35 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
   }
 }
 
+template <bool WIDE, int KD, bool FULL, bool DOTS, int PL>
+__global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(Args A) {
+  __shared__ __attribute__((aligned(16))) char lds[lds_bytes<WIDE, KD, FULL, DOTS, PL>()];
+  walk<WIDE, KD, FULL, DOTS, PL>(A, A.walk[A.first + blockIdx.y], blockIdx.x, lds);
+}
+
+// The three walks of the backward in one launch, the longer ones of dq and dk
+// first: at one workgroup a CU, dv's fill the CUs that those leave idle at their
+// end.  n_qk: workgroups of dq's walk.
+template <int DK, int DV, int PLV>
+__global__ void __launch_bounds__((Waves<false, true>::threads), 1) gradient_kernel(Args A, int n_qk) {
+  constexpr int a = lds_bytes<false, DV, true, true, 3>(), b = lds_bytes<false, DK, true, false, PLV>();
+  __shared__ __attribute__((aligned(16))) char lds[a > b ? a : b];
+  const int block = blockIdx.x;
+  if (block < 2 * n_qk) {
+    const int y = block >= n_qk;
+    walk<false, DV, true, true, 3>(A, A.walk[y], block - y * n_qk, lds);
+  } else {
+    walk<false, DK, true, false, PLV>(A, A.walk[2], block - 2 * n_qk, lds);
+  }
+}
+
 // Cut sequences: the segments' own states become their entry states, and the
 // exit state is written.  One workgroup per (sequence, head, tile) and walk;
 // the threads own the elements in the walk kernel's order.
 template <int KD>
 __global__ void __launch_bounds__(NTHR) scan_kernel(Args A) {
   constexpr int NT = KD / 16;
-  const Walk& W = A.walk[blockIdx.y];
+  const Walk& W = A.walk[A.first + blockIdx.y];
   const int CD = static_cast<int>(W.s_elems / KD);
   const int ntile = CD / CT;
   const int t = blockIdx.x % NT;          // state tile
@@ -1252,16 +1287,19 @@ __global__ void __launch_bounds__(NTHR) group_sum_kernel(Args A, const float* hq
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// workgroups of a walk of contraction width kd (see walk)
+int64_t walk_blocks(const Args& A, int kd) {
+  return (int64_t)A.N * A.nseg * cdiv(A.H, 8) * 8 * (A.walk[0].s_elems / kd / CT);
+}
 template <bool WIDE, int KD, bool FULL, bool DOTS, int PL>
 hipError_t launch_walk_kd(const Args& A, int walks, hipStream_t s) {
-  const int64_t blocks =
-      (int64_t)A.N * A.nseg * cdiv(A.H, 8) * 8 * (A.walk[0].s_elems / KD / CT);
+  const int64_t blocks = walk_blocks(A, KD);
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   walk_kernel<WIDE, KD, FULL, DOTS, PL><<<dim3((unsigned)blocks, walks),
                                           Waves<WIDE, FULL>::threads, 0, s>>>(A);
   return hipGetLastError();
 }
-// `walks` walks of one contraction width kd.  S and P enter the products for out as
+// `walks` walks of one contraction width kd from A.first on.  S and P enter the products for out as
 //   three values  with dots: dg is a small difference of their sums, and for one
 //                 decay a head a sum of those; with two values it was up to 3e-5 off
 //   two           out is fp32, or bf16 and the call has at most one chunk of tokens,
@@ -1270,10 +1308,11 @@ hipError_t launch_walk_kd(const Args& A, int walks, hipStream_t s) {
 //                 roundings do not average out
 //   one           out is bf16: off by 2.3e-3 of its norm where bf16's own rounding is
 //                 1.7e-3 off
+bool two_values(const Args& A, bool out_bf16) { return !out_bf16 || A.T_tot <= C; }
 template <bool DOTS>
 hipError_t launch_walk(const Args& A, int walks, bool wide, int kd, bool full, bool out_bf16,
                        hipStream_t s) {
-  const bool two = !out_bf16 || A.T_tot <= C;
+  const bool two = two_values(A, out_bf16);
 #define KDA_LW(KDV)                                                              \
   do {                                                                           \
     if (wide)                                                                    \
@@ -1287,6 +1326,23 @@ hipError_t launch_walk(const Args& A, int walks, bool wide, int kd, bool full, b
   if (kd == 128) KDA_LW(128);
   KDA_LW(64);
 #undef KDA_LW
+}
+
+template <int DK, int DV>
+hipError_t launch_gradients_kd(const Args& A, bool two, hipStream_t s) {
+  const int64_t qk = walk_blocks(A, DV), blocks = 2 * qk + walk_blocks(A, DK);
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)blocks), block(Waves<false, true>::threads);
+  if (two) gradient_kernel<DK, DV, 2><<<grid, block, 0, s>>>(A, (int)qk);
+  else gradient_kernel<DK, DV, 1><<<grid, block, 0, s>>>(A, (int)qk);
+  return hipGetLastError();
+}
+// all walks of the backward, bf16 operands
+hipError_t launch_gradients(const Args& A, int dk, int dv, bool out_bf16, hipStream_t s) {
+  const bool two = two_values(A, out_bf16);
+  if (dk == 128)
+    return dv == 128 ? launch_gradients_kd<128, 128>(A, two, s) : launch_gradients_kd<128, 64>(A, two, s);
+  return dv == 128 ? launch_gradients_kd<64, 128>(A, two, s) : launch_gradients_kd<64, 64>(A, two, s);
 }
 
 hipError_t launch_scan(const Args& A, int walks, int kd, hipStream_t s) {
@@ -1489,13 +1545,16 @@ hipError_t launch_backward(const Problem& p, const Operand& q, const Operand& k,
   const bool wide = !(q.bf16 && k.bf16 && v.bf16 && (d_o.bf16 || !d_o.p));
   A.walk[0] = wq;
   A.walk[1] = wk;
+  A.walk[2] = wv;
   Args B = A;  // dv needs no dots (and for dk != dv contracts over another width)
-  B.walk[0] = wv;
+  B.first = 2;
   for (int phase = A.nseg > 1 ? 0 : 2; phase < 3; ++phase) {
     hipError_t e;
     if (phase == 1) {
       e = launch_scan(A, 2, DV, s);
       if (e == hipSuccess) e = launch_scan(B, 1, DK, s);
+    } else if (phase == 2 && !wide) {
+      e = launch_gradients(A, DK, DV, grad_bf16, s);
     } else {
       const bool full = phase == 2;
       e = launch_walk<true>(A, 2, wide, DV, full, grad_bf16, s);
