@@ -105,15 +105,37 @@ __device__ __forceinline__ float sum8(f32x8 x) {
   return ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
 }
 
+template <int CTRL>
+__device__ __forceinline__ float moved(float x) {  // x of the lane that CTRL names
+  return __uint_as_float(
+      __builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), CTRL, 0xf, 0xf, true));
+}
+// Sum over aligned groups of L (8 .. 64) lanes, in all of them.  Moves between
+// registers: an LDS permute takes some 60 clocks, and a row waits for its sums.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float x) {
+  x += moved<0xb1>(x);                                  // lane ^ 1
+  x += moved<0x4e>(x);                                  // lane ^ 2
+  x += moved<0x141>(x);                                 // 7 - lane of eight: the other four
+  if constexpr (L >= 16) x += moved<0x140>(x);          // 15 - lane of sixteen: the other eight
+  if constexpr (L >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if constexpr (L >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return x;
+}
+
 // Sums of NS values over the L lanes of a row; every lane gets them.  Rows of
 // a whole workgroup (L = its size) go through LDS, double-buffered by `turn`
 // so that one barrier a sum is enough.
 template <int L, int NS>
 __device__ __forceinline__ void row_sum(float (&x)[NS], float* s_part, int& turn) {
 #pragma unroll
-  for (int off = (L < 64 ? L : 64) / 2; off > 0; off >>= 1)
-#pragma unroll
-    for (int i = 0; i < NS; ++i) x[i] += __shfl_xor(x[i], off);
+  for (int i = 0; i < NS; ++i) x[i] = lanes_sum<(L < 64 ? L : 64)>(x[i]);
   if constexpr (L > 64) {
     constexpr int W = L / 64;
     float* p = s_part + turn * (2 * W);
@@ -135,24 +157,35 @@ __device__ __forceinline__ void row_sum(float (&x)[NS], float* s_part, int& turn
 template <int L>
 constexpr int threads() { return L > 256 ? L : 256; }
 
-// mean and 1/sqrt(var + eps) of the row in x (columns past d hold 0)
-template <int L, int M>
-__device__ __forceinline__ void statistics(f32x8 (&x)[M], const int (&left)[M], float inv_d,
-                                           float eps, float* s_part, int& turn, float& rstd) {
-  float s[1] = {0.f};
+// x (columns past d hold 0) becomes x - mean; rstd = 1/sqrt(var + eps).  With
+// T > 0 the sums of t[] and of t (x - mean) come along with the two sums.
+template <int L, int M, int T>
+__device__ __forceinline__ void statistics(f32x8 (&x)[M], const f32x8 (&t)[T ? M : 1],
+                                           const int (&left)[M], float inv_d, float eps,
+                                           float* s_part, int& turn, float& rstd, float& st,
+                                           float& stx) {
+  float s[1 + T] = {};
 #pragma unroll
-  for (int m = 0; m < M; ++m) s[0] += sum8(x[m]);
-  row_sum<L, 1>(s, s_part, turn);
+  for (int m = 0; m < M; ++m) {
+    s[0] += sum8(x[m]);
+    if constexpr (T) s[1] += sum8(t[m]);
+  }
+  row_sum<L, 1 + T>(s, s_part, turn);
   const float mu = s[0] * inv_d;
-  s[0] = 0.f;
+  float v[1 + T] = {};
 #pragma unroll
   for (int m = 0; m < M; ++m) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[m][e] = e < left[m] ? x[m][e] - mu : 0.f;
-    s[0] += sum8(x[m] * x[m]);
+    v[0] += sum8(x[m] * x[m]);
+    if constexpr (T) v[1] += sum8(t[m] * x[m]);
   }
-  row_sum<L, 1>(s, s_part, turn);
-  rstd = 1.0f / sqrtf(s[0] * inv_d + eps);
+  row_sum<L, 1 + T>(v, s_part, turn);
+  rstd = 1.0f / sqrtf(v[0] * inv_d + eps);
+  if constexpr (T) {
+    st = s[1];
+    stx = v[1];
+  }
 }
 
 // Row owner q of Q walks rows q, q + Q, ... (Q a multiple of groups).
@@ -190,8 +223,9 @@ __global__ void __launch_bounds__(threads<L>()) forward_kernel(
     if (r + Q < rows)
 #pragma unroll
       for (int m = 0; m < M; ++m) raw[m].load(x, (r + Q) * d + (m * L + l) * 8, left[m]);
-    float rstd;
-    statistics<L, M>(v, left, inv_d, eps, s_part, turn, rstd);
+    float rstd, none;
+    const f32x8 no_t[1] = {};
+    statistics<L, M, 0>(v, no_t, left, inv_d, eps, s_part, turn, rstd, none, none);
 #pragma unroll
     for (int m = 0; m < M; ++m)
       Eight<YB>::store(y, r * d + (m * L + l) * 8, left[m], v[m] * rstd * ww[m] + bb[m]);
@@ -242,23 +276,20 @@ __global__ void __launch_bounds__(threads<L>()) backward_kernel(
         rx[m].load(x, (r + Q) * d + (m * L + l) * 8, left[m]);
         ry[m].load(dy, (r + Q) * d + (m * L + l) * 8, left[m]);
       }
-    float rstd;
-    statistics<L, M>(v, left, inv_d, eps, s_part, turn, rstd);
-    float s[2] = {0.f, 0.f};  // sums of t and of t xh
+    f32x8 t[M];  // dy w (0 past d: dy is)
+#pragma unroll
+    for (int m = 0; m < M; ++m) t[m] = g[m] * ww[m];
+    float rstd, m0, m1;
+    statistics<L, M, 1>(v, t, left, inv_d, eps, s_part, turn, rstd, m0, m1);
+    m0 *= inv_d;
+    m1 *= inv_d * rstd;
 #pragma unroll
     for (int m = 0; m < M; ++m) {
       v[m] *= rstd;  // xh
       db[m] += g[m];
       dw[m] += g[m] * v[m];
-      g[m] *= ww[m];  // t (0 past d: dy is)
-      s[0] += sum8(g[m]);
-      s[1] += sum8(g[m] * v[m]);
+      Eight<XB>::store(dx, r * d + (m * L + l) * 8, left[m], rstd * (t[m] - m0 - v[m] * m1));
     }
-    row_sum<L, 2>(s, s_part, turn);
-    const float m0 = s[0] * inv_d, m1 = s[1] * inv_d;
-#pragma unroll
-    for (int m = 0; m < M; ++m)
-      Eight<XB>::store(dx, r * d + (m * L + l) * 8, left[m], rstd * (g[m] - m0 - v[m] * m1));
   }
   if (part) {
     float* pw = part + q * 2 * d;
@@ -282,7 +313,16 @@ __global__ void __launch_bounds__(1024) partials_kernel(const float* __restrict_
   const int64_t grp = blockIdx.y;
   float acc = 0.f;
   if (c < 2 * (int64_t)d)
-    for (int64_t q = grp + groups * k; q < owners; q += groups * 16) acc += part[q * 2 * d + c];
+    for (int64_t q = grp + groups * k; q < owners; q += groups * 16 * 8) {
+      float x[8];  // eight loads on their way
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t at = q + groups * 16 * j;
+        x[j] = at < owners ? part[at * 2 * d + c] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc += x[j];
+    }
   s[k][cl] = acc;
   __syncthreads();
   if (k == 0 && c < 2 * (int64_t)d) {
@@ -293,20 +333,27 @@ __global__ void __launch_bounds__(1024) partials_kernel(const float* __restrict_
 }
 
 // Row owners: enough lanes for the card, at most one a row, a multiple of groups.
-int64_t owners(int64_t rows, int64_t groups, int L, int64_t lanes) {
-  int64_t q = lanes / L;
-  if (q < 1) q = 1;
-  if (q > rows) q = rows;
-  q = (q + groups - 1) / groups * groups;
-  return q;
+int64_t owners(int64_t rows, int64_t groups, int64_t most) {
+  const int64_t q = most < 1 ? 1 : most > rows ? rows : most;
+  return (q + groups - 1) / groups * groups;
 }
-constexpr int64_t kForwardLanes = 256 * 2048;
-constexpr int64_t kBackwardLanes = 256 * 512;
+int64_t forward_owners(int64_t rows, int64_t groups, int L) {
+  return owners(rows, groups, 256 * (L <= 256 ? 4096 : 2048) / L);
+}
+// Every owner of the backward also writes 2 d sums, which are read again: at
+// least eight rows each, unless that leaves CUs without a workgroup.
+int64_t backward_owners(int64_t rows, int64_t groups, int L, int M) {
+  const int64_t one_each = 256 * (L < 256 ? 256 / L : 1);  // a workgroup a CU
+  int64_t q = 256 * 1024 / (L * M);
+  if (q > rows / 8) q = rows / 8;
+  return owners(rows, groups, q < one_each ? one_each : q);
+}
 
 int lanes_of(int d) {
   return d <= 64 ? 8 : d <= 128 ? 16 : d <= 256 ? 32 : d <= 1024 ? 64 : d <= 4096 ? 256
          : d <= 8192 ? 512 : 1024;
 }
+int runs_of(int d) { return (d + lanes_of(d) * 8 - 1) / (lanes_of(d) * 8); }
 
 }  // namespace
 
@@ -327,7 +374,7 @@ hipError_t launch_forward(const void* x, bool x_bf16, const float* w, const floa
                           int64_t groups, void* y, bool y_bf16, int64_t rows, int d, float eps,
                           hipStream_t s) {
   if (rows == 0) return hipSuccess;
-  const int64_t Q = owners(rows, groups, lanes_of(d), kForwardLanes);
+  const int64_t Q = forward_owners(rows, groups, lanes_of(d));
 #define KDA_LN_F(XB, YB, L, M)                                                                 \
   forward_kernel<XB, YB, L, M><<<dim3((unsigned)((Q * L + threads<L>() - 1) / threads<L>())), \
                                  threads<L>(), 0, s>>>(x, w, b, groups, y, rows, d, eps, Q)
@@ -344,7 +391,7 @@ hipError_t launch_forward(const void* x, bool x_bf16, const float* w, const floa
 
 size_t backward_workspace_bytes(int64_t rows, int64_t groups, int d) {
   if (rows == 0) return 0;
-  return (size_t)owners(rows, groups, lanes_of(d), kBackwardLanes) * 2 * d * sizeof(float);
+  return (size_t)backward_owners(rows, groups, lanes_of(d), runs_of(d)) * 2 * d * sizeof(float);
 }
 
 hipError_t launch_backward(const void* dy, bool dy_bf16, const void* x, bool x_bf16,
@@ -354,7 +401,7 @@ hipError_t launch_backward(const void* dy, bool dy_bf16, const void* x, bool x_b
   float* part = sums ? static_cast<float*>(ws) : nullptr;
   int64_t Q = 0;
   if (rows > 0) {
-    Q = owners(rows, groups, lanes_of(d), kBackwardLanes);
+    Q = backward_owners(rows, groups, lanes_of(d), runs_of(d));
 #define KDA_LN_B(YB, XB, L, M)                                                                  \
   backward_kernel<YB, XB, L, M><<<dim3((unsigned)((Q * L + threads<L>() - 1) / threads<L>())), \
                                   threads<L>(), 0, s>>>(dy, x, w, groups, dx, part, rows, d, eps, Q)

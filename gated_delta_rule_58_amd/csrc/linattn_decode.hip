@@ -21,7 +21,7 @@ template <bool S_BF16, int DK, int DV, int CT, int NTHR>
 __global__ void __launch_bounds__(NTHR) decode_kernel(
     Operand q, Operand k, Operand v, Decay gd, void* __restrict__ pool,
     const int32_t* __restrict__ slots, int64_t num_slots, void* __restrict__ o, bool o_bf16,
-    int H, float scale) {
+    int H, int64_t blocks, float scale) {
   constexpr int ES = S_BF16 ? 2 : 4;
   constexpr int CPT = 16 / ES;
   constexpr int NV = CPT / 4;
@@ -37,8 +37,14 @@ __global__ void __launch_bounds__(NTHR) decode_kernel(
 
   const int t = threadIdx.x;
   const int cg = t % NCG, rs = t / NCG;
-  const int64_t pair = blockIdx.x / NT;
-  const int tile = blockIdx.x % NT;
+  // Workgroups go to the XCDs in turn: each XCD walks a range of the states of its
+  // own (256 x 96 states of 64 KB: 554 us, 5.8 TB/s; in the order of the states
+  // 581).
+  const int64_t per_xcd = gridDim.x >> 3;
+  const int64_t id = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  if (id >= blocks) return;
+  const int64_t pair = id / NT;
+  const int tile = id % NT;
   const int64_t n = pair / H;
   const int h = static_cast<int>(pair - n * H);
   const int64_t slot = slots ? static_cast<int64_t>(slots[n]) : n;
@@ -126,14 +132,14 @@ hipError_t launch(const Operand& q, const Operand& k, const Operand& v, const De
   const int64_t pairs = (int64_t)N * H;
   const bool tiled = pairs < 512;
   const int64_t blocks = pairs * (tiled ? DV / 32 : 1);
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks));
+  if (blocks > 0x7ffffff8) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>((blocks + 7) / 8 * 8));
   if (tiled)
     decode_kernel<S_BF16, DK, DV, 32, 256><<<grid, 256, 0, s>>>(q, k, v, g, pool, slots, num_slots,
-                                                              o, o_bf16, H, scale);
+                                                              o, o_bf16, H, blocks, scale);
   else
     decode_kernel<S_BF16, DK, DV, DV, 512><<<grid, 512, 0, s>>>(q, k, v, g, pool, slots, num_slots,
-                                                              o, o_bf16, H, scale);
+                                                              o, o_bf16, H, blocks, scale);
   return hipGetLastError();
 }
 

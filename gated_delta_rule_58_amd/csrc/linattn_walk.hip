@@ -94,7 +94,7 @@ namespace {
 constexpr int C = 64;        // tokens a chunk
 constexpr int CT = 64;       // columns a workgroup
 constexpr int NTHR = 256;    // threads of the small kernels, and of the state waves
-constexpr int kMinSegChunks = 8;   // shortest segment of a cut sequence
+constexpr int kMinSegChunks = 4;   // shortest segment of a cut sequence
 constexpr int kBorderChunks = 32;  // segments of dg's sums when sequences are walked whole
 
 // swizzle of the 16-byte block index of a row (rows of 128 / 64 channels)
@@ -206,6 +206,8 @@ struct Walk {
   bool in_bf16, out_state_bf16, out_bf16, reverse;
 };
 
+__host__ __device__ __forceinline__ int heads_per_xcd(int H) { return H < 16 ? 1 : H / 8; }
+
 struct Args {
   Walk walk[3];
   int first;           // walk of blockIdx.y = 0
@@ -236,8 +238,8 @@ __device__ __forceinline__ int64_t seg_slot(const Args& A, int n, int bos) {
   return bos / (C * A.seg_chunks) + n;
 }
 
-// PS: bf16 values of a state's element (see walk_kernel)
-template <bool WIDE, int KD, bool DOTS, int PS>
+// PS: bf16 values of a state's element (see walk)
+template <bool WIDE, int KD, bool FULL, bool DOTS, int PS>
 struct Lds {
   static constexpr int NPL = WIDE ? 3 : 1;          // planes of an operand
   static constexpr int NBUF = WIDE ? 1 : PS == 1 ? 3 : 2;  // chunks of a, b and c
@@ -245,7 +247,7 @@ struct Lds {
   static constexpr int AB = C * KD * 2;             // one plane of a or b
   static constexpr int CC = C * CT * 2;             // one plane of c
   static constexpr int SS = KD * CT * 2;            // one plane of the state
-  static constexpr int off_b = WIDE ? 0 : AB;       // (fp32: a goes straight to registers)
+  static constexpr int off_b = FULL && !WIDE ? AB : 0;  // (fp32: a goes straight to registers)
   static constexpr int off_c = off_b + NPL * AB;
   static constexpr int off_x = off_c + NPL * CC;    // x of the dots (fp32: straight to registers)
   static constexpr int buf = off_x + (DOTS && !WIDE ? CC : 0);
@@ -388,12 +390,12 @@ __device__ __forceinline__ void wait_vm_le() {
 // element of S and P in the products for out.
 template <bool WIDE, int KD, bool FULL, bool DOTS, int PL>
 constexpr int lds_bytes() {
-  using L = Lds<WIDE, KD, DOTS, PL>;
+  using L = Lds<WIDE, KD, FULL, DOTS, PL>;
   return (FULL ? L::total : L::off_s) + (int)sizeof(Decays);
 }
 template <bool WIDE, int KD, bool FULL, bool DOTS, int PL>
 __device__ __forceinline__ void walk(const Args& A, const Walk& W, int block, char* lds) {
-  using L = Lds<WIDE, KD, DOTS, PL>;
+  using L = Lds<WIDE, KD, FULL, DOTS, PL>;
   using WV = Waves<WIDE, FULL>;
   constexpr int NPL = L::NPL, NBUF = L::NBUF;
   constexpr int NPS = PL, NPP = PL, NPC = 3;
@@ -414,21 +416,22 @@ __device__ __forceinline__ void walk(const Args& A, const Walk& W, int block, ch
   const bool a_bf = !WIDE || W.a.bf16, b_bf = !WIDE || W.b.bf16, c_bf = !WIDE || W.c.bf16;
 
   // ---- block -> (sequence, segment, head, tile).  Workgroups go to the XCDs
-  // in turn; an XCD gets hb = ceil(H / 8) consecutive heads of every segment, with
-  // their tiles.  (Every eighth head instead: the tokens of a head are H rows
+  // in turn; an XCD gets hb = H / 8 consecutive heads (of 8 hb in the list of all
+  // segments' heads) with their tiles.  (Every eighth head instead: the tokens of a head are H rows
   // apart, so for H a multiple of 16 its rows and those of the heads 16 further
   // share one channel of the XCD's L2, and the XCD used two channels of sixteen.)
   const int CD = static_cast<int>(W.s_elems / KD);
   const int ntile = CD / CT;
-  const int hb = (A.H + 7) >> 3;
+  const int hb = heads_per_xcd(A.H);
   int id = block >> 3;
   const int tile = id % ntile;
   id /= ntile;
-  const int h = (block & 7) * hb + id % hb;
-  id /= hb;
+  id = (id / hb * 8 + (block & 7)) * hb + id % hb;
+  const int h = id % A.H;
+  id /= A.H;
   const int seg = id % A.nseg;
   int n = id / A.nseg;
-  if (h >= A.H) return;
+  if (n >= A.N) return;
   if (A.cu) n = chunk::lpt_sequence(A.cu, A.N, A.T_tot, n, D.seq);
   n = __builtin_amdgcn_readfirstlane(n);
   int bos, len;
@@ -1131,14 +1134,24 @@ __global__ void __launch_bounds__(NTHR) scan_kernel(Args A) {
     return W.seg_state + ((slot * A.H + h) * ntile + tile) * (int64_t)(KD * CT) +
            (w * 64 + lane) * 4 + t * (NTHR * 4);
   };
-  f32x4 next = S;
-  if (nseg > 0) next = *reinterpret_cast<const f32x4*>(at(0));
-  for (int j = 0; j < nseg; ++j) {
-    const f32x4 own = next;
-    if (j + 1 < nseg) next = *reinterpret_cast<const f32x4*>(at(j + 1));
-    const int64_t slot = slot0 + (W.reverse ? nseg - 1 - j : j);
-    *reinterpret_cast<f32x4*>(at(j)) = S;
-    S = S * ex2(W.seg_decay[slot * A.H + h]) + own;
+  // AHEAD segments' loads at a time: the chain itself is short
+  constexpr int AHEAD = 8;
+  for (int j0 = 0; j0 < nseg; j0 += AHEAD) {
+    f32x4 own[AHEAD];
+    float decay[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int j = j0 + i < nseg ? j0 + i : nseg - 1;
+      own[i] = *reinterpret_cast<const f32x4*>(at(j));
+      decay[i] = W.seg_decay[(slot0 + (W.reverse ? nseg - 1 - j : j)) * A.H + h];
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (j0 + i < nseg) {
+        *reinterpret_cast<f32x4*>(at(j0 + i)) = S;
+        S = S * ex2(decay[i]) + own[i];
+      }
+    }
   }
   if (W.s_out) {
     const int64_t sl = W.out_idx ? (int64_t)W.out_idx[n] : n;
@@ -1289,7 +1302,8 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // workgroups of a walk of contraction width kd (see walk)
 int64_t walk_blocks(const Args& A, int kd) {
-  return (int64_t)A.N * A.nseg * cdiv(A.H, 8) * 8 * (A.walk[0].s_elems / kd / CT);
+  const int hb = heads_per_xcd(A.H);
+  return cdiv((int64_t)A.N * A.nseg * A.H, 8 * hb) * 8 * hb * (A.walk[0].s_elems / kd / CT);
 }
 template <bool WIDE, int KD, bool FULL, bool DOTS, int PL>
 hipError_t launch_walk_kd(const Args& A, int walks, hipStream_t s) {
@@ -1319,7 +1333,7 @@ hipError_t launch_walk(const Args& A, int walks, bool wide, int kd, bool full, b
       return full ? launch_walk_kd<true, KDV, true, DOTS, 3>(A, walks, s)        \
                   : launch_walk_kd<true, KDV, false, false, 3>(A, walks, s);     \
     if (!full) return launch_walk_kd<false, KDV, false, false, 1>(A, walks, s);  \
-    if constexpr (DOTS) return launch_walk_kd<false, KDV, true, true, 3>(A, walks, s); \
+    if constexpr (DOTS) return hipErrorInvalidValue; /* launch_gradients */      \
     else if (two) return launch_walk_kd<false, KDV, true, false, 2>(A, walks, s); \
     else return launch_walk_kd<false, KDV, true, false, 1>(A, walks, s);         \
   } while (0)
@@ -1354,14 +1368,25 @@ hipError_t launch_scan(const Args& A, int walks, int kd, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Chunks a segment when sequences are cut, 0 when they are walked whole: with
-// `walkers` workgroups a segment, cut when whole sequences are too few for the
-// card and long enough; segments then give about two workgroups a CU.
-int cut_chunks(int64_t T_tot, int64_t N, int64_t walkers) {
-  if (N * walkers >= 192) return 0;
-  const int64_t chunks = cdiv(T_tot, C);
-  if (chunks < N * 2 * kMinSegChunks) return 0;
-  const int64_t sc = cdiv(chunks * walkers, 512);
+// Chunks a segment when sequences are cut, 0 when they are walked whole.  A CU
+// holds one workgroup, so whole sequences take the time of the longest one or, if
+// that is more, of an even share of all chunks (`walkers` workgroups each); cut
+// they take the even share for out, nearly as much again for the segments' own
+// states, and two more launches.  Whole against cut, us, one sequence, dk = dv =
+// 128: H = 1, T = 4096 106 / 23; H = 16, T = 512 18 / 22, T = 1024 32 / 25, T =
+// 131072 3290 / 785; H = 32, T = 8192 211 / 105; H = 48, T = 4096 110 / 98; H =
+// 64, T = 16384 422 / 417; H = 80, T = 16384 429 / 530.
+// rounds: segments a CU gets in all.  One forward (fewer states to hand on; 1
+// against 2: H = 16, T = 4096 40 / 47, H = 1, T = 131072 84 / 113, H = 16, T =
+// 131072 788 / 779); two backward, where workgroups of different length even out
+// (H = 8, T = 32768 609 / 556).
+constexpr int64_t kCus = 256;
+int cut_chunks(int64_t T_tot, int64_t N, int64_t walkers, int64_t longest, int rounds) {
+  const int64_t chunks = cdiv(T_tot, C), all = chunks * walkers, even = cdiv(all, kCus);
+  // (the bounds on N keep the workspace small: a state per sequence and segment)
+  if (chunks < N * 4 * kMinSegChunks || N * walkers >= 4 * kCus) return 0;
+  if (4 * longest < 9 * even + 12 * kMinSegChunks) return 0;
+  const int64_t sc = cdiv(all, rounds * kCus);
   return static_cast<int>(sc > kMinSegChunks ? sc : kMinSegChunks);
 }
 
@@ -1413,20 +1438,24 @@ struct BackwardWs {
   }
 };
 
-// longest sequence: from the host copy, or the most it can be
-int64_t longest(const Args& A, const int32_t* cu_host) {
-  if (!A.cu) return A.eq_len;
-  if (!cu_host) return A.T_tot;
+// chunks of the longest sequence: from the host copy, or the most it can be
+int64_t longest_chunks(const Problem& p) {
+  if (!p.cu) return cdiv(p.T_tot / p.N, C);
+  if (!p.cu_host) return cdiv(p.T_tot, C);
   int64_t m = 0;
-  for (int n = 0; n < A.N; ++n)
-    m = cu_host[n + 1] - cu_host[n] > m ? cu_host[n + 1] - cu_host[n] : m;
-  return m;
+  for (int n = 0; n < p.N; ++n)
+    m = p.cu_host[n + 1] - p.cu_host[n] > m ? p.cu_host[n + 1] - p.cu_host[n] : m;
+  return cdiv(m, C);
+}
+// the same to decide by: lengths that are not known are taken as equal
+int64_t longest_guess(const Problem& p) {
+  return p.cu && !p.cu_host ? cdiv(p.T_tot / p.N, C) : longest_chunks(p);
 }
 
 }  // namespace
 
 size_t prefill_workspace_bytes(int64_t T_tot, int N, int H, int dk, int dv) {
-  const int seg = cut_chunks(T_tot, N, (int64_t)H * (dv / CT));
+  const int seg = cut_chunks(T_tot, N, (int64_t)H * (dv / CT), cdiv(T_tot, C), 1);
   return seg ? ForwardWs(nullptr, T_tot, N, H, dk, dv, seg).bytes : 0;
 }
 
@@ -1458,11 +1487,11 @@ hipError_t launch_prefill(const Problem& p, const Operand& q, const Operand& k, 
   W.out = o;
   W.out_bf16 = o_bf16;
   const bool wide = !(q.bf16 && k.bf16 && v.bf16);
-  const int seg = cut_chunks(p.T_tot, p.N, (int64_t)p.H * (p.dv / CT));
+  const int seg = cut_chunks(p.T_tot, p.N, (int64_t)p.H * (p.dv / CT), longest_guess(p), 1);
   const ForwardWs f(ws, p.T_tot, p.N, p.H, p.dk, p.dv, seg);
   if (seg && ws && ws_bytes >= f.bytes) {
     A.seg_chunks = seg;
-    A.nseg = static_cast<int>(cdiv(cdiv(longest(A, p.cu_host), C), seg));
+    A.nseg = static_cast<int>(cdiv(longest_chunks(p), seg));
     if (A.nseg < 1) A.nseg = 1;
     W.seg_state = f.state;
     W.seg_decay = f.decay;
@@ -1476,17 +1505,21 @@ hipError_t launch_prefill(const Problem& p, const Operand& q, const Operand& k, 
 }
 
 namespace {
-int border_chunks(int64_t T_tot, int N, int H, int dk, int dv, bool* cut) {
-  const int seg = cut_chunks(T_tot, N, (int64_t)H * (2 * (dk / CT) + dv / CT));
+// chunks a segment of dg's sums, and whether the walks are cut there
+int border_chunks(int64_t T_tot, int N, int H, int dk, int dv, int64_t longest, bool* cut) {
+  const int seg = cut_chunks(T_tot, N, (int64_t)H * (2 * (dk / CT) + dv / CT), longest, 2);
   *cut = seg > 0;
   return seg ? seg : kBorderChunks;
 }
 }  // namespace
 
 size_t backward_workspace_bytes(int64_t T_tot, int N, int H, int Hk, int dk, int dv) {
+  // by the longest that a sequence can be; where they turn out even, they are walked whole
   bool cut;
-  const int seg = border_chunks(T_tot, N, H, dk, dv, &cut);
-  return BackwardWs(nullptr, T_tot, N, H, Hk, dk, dv, seg, cut).bytes;
+  const int seg = border_chunks(T_tot, N, H, dk, dv, cdiv(T_tot, C), &cut);
+  const size_t a = BackwardWs(nullptr, T_tot, N, H, Hk, dk, dv, seg, cut).bytes;
+  const size_t b = BackwardWs(nullptr, T_tot, N, H, Hk, dk, dv, kBorderChunks, false).bytes;
+  return a > b ? a : b;
 }
 
 hipError_t launch_backward(const Problem& p, const Operand& q, const Operand& k, const Operand& v,
@@ -1495,7 +1528,7 @@ hipError_t launch_backward(const Problem& p, const Operand& q, const Operand& k,
                            hipStream_t s) {
   const int DK = p.dk, DV = p.dv, group = p.H / p.Hk;
   bool cut;
-  const int seg = border_chunks(p.T_tot, p.N, p.H, DK, DV, &cut);
+  const int seg = border_chunks(p.T_tot, p.N, p.H, DK, DV, longest_guess(p), &cut);
   const BackwardWs b(ws, p.T_tot, p.N, p.H, p.Hk, DK, DV, seg, cut);
   Args A{};
   A.g = p.g;
@@ -1506,7 +1539,7 @@ hipError_t launch_backward(const Problem& p, const Operand& q, const Operand& k,
   A.eq_len = p.cu ? 0 : static_cast<int>(p.T_tot / p.N);
   A.scale = p.scale;
   A.seg_chunks = seg;
-  const int64_t max_chunks = cdiv(longest(A, p.cu_host), C);
+  const int64_t max_chunks = longest_chunks(p);
   const int nseg = static_cast<int>(max_chunks ? cdiv(max_chunks, seg) : 1);
   A.nseg = cut ? nseg : 1;
 
