@@ -5,10 +5,13 @@
 //             dw = sum_rows dy xh,  db = sum_rows dy
 //
 // HBM-bound: x (and dy) are read once, y (dx) is written once, the row stays
-// in registers between.  L lanes own a row: a part of a wave up to d = 512, a
-// wave up to 1,024, a workgroup beyond that; lane l holds the M runs of eight columns
-// (m L + l) 8 .. + 7.  The lanes of a row then walk down rows of the SAME
-// weight row (row % groups), so that w, b and the gradients' sums stay in
+// in registers between.  Measured, bf16: forward of 393216 rows of 128 (96 weight
+// rows) 38 us, 5.3 TB/s; backward 62 us, 4.9 TB/s; backward of 2048 x 5003, 32 us,
+// where a row's chain (loads, two sums over 512 lanes) leaves the card idle.
+//
+// L lanes own a row: a part of a wave up to d = 256, a wave up to 1,024, a workgroup
+// beyond that; lane l holds the M runs of eight columns (m L + l) 8 .. + 7.  The
+// lanes of a row then walk down rows of the SAME weight row (row % groups), so that w, b and the gradients' sums stay in
 // registers: row q, q + Q, q + 2Q, ... with Q a multiple of groups.
 // Neighbouring lanes own neighbouring rows, so a wave's access is contiguous
 // whatever L is.  The next row is loaded before this one is worked on.
@@ -158,17 +161,18 @@ template <int L>
 constexpr int threads() { return L > 256 ? L : 256; }
 
 // x (columns past d hold 0) becomes x - mean; rstd = 1/sqrt(var + eps).  With
-// T > 0 the sums of t[] and of t (x - mean) come along with the two sums.
+// T = 1 the sums of t = dy w and of t (x - mean) come along with the two sums
+// (t is formed where it is needed: the registers do not hold it too).
 template <int L, int M, int T>
-__device__ __forceinline__ void statistics(f32x8 (&x)[M], const f32x8 (&t)[T ? M : 1],
-                                           const int (&left)[M], float inv_d, float eps,
-                                           float* s_part, int& turn, float& rstd, float& st,
-                                           float& stx) {
+__device__ __forceinline__ void statistics(f32x8 (&x)[M], const f32x8 (&dy)[T ? M : 1],
+                                           const f32x8 (&w)[T ? M : 1], const int (&left)[M],
+                                           float inv_d, float eps, float* s_part, int& turn,
+                                           float& rstd, float& st, float& stx) {
   float s[1 + T] = {};
 #pragma unroll
   for (int m = 0; m < M; ++m) {
     s[0] += sum8(x[m]);
-    if constexpr (T) s[1] += sum8(t[m]);
+    if constexpr (T) s[1] += sum8(dy[m] * w[m]);
   }
   row_sum<L, 1 + T>(s, s_part, turn);
   const float mu = s[0] * inv_d;
@@ -178,7 +182,7 @@ __device__ __forceinline__ void statistics(f32x8 (&x)[M], const f32x8 (&t)[T ? M
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[m][e] = e < left[m] ? x[m][e] - mu : 0.f;
     v[0] += sum8(x[m] * x[m]);
-    if constexpr (T) v[1] += sum8(t[m] * x[m]);
+    if constexpr (T) v[1] += sum8(dy[m] * w[m] * x[m]);
   }
   row_sum<L, 1 + T>(v, s_part, turn);
   rstd = 1.0f / sqrtf(v[0] * inv_d + eps);
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(threads<L>()) forward_kernel(
       for (int m = 0; m < M; ++m) raw[m].load(x, (r + Q) * d + (m * L + l) * 8, left[m]);
     float rstd, none;
     const f32x8 no_t[1] = {};
-    statistics<L, M, 0>(v, no_t, left, inv_d, eps, s_part, turn, rstd, none, none);
+    statistics<L, M, 0>(v, no_t, no_t, left, inv_d, eps, s_part, turn, rstd, none, none);
 #pragma unroll
     for (int m = 0; m < M; ++m)
       Eight<YB>::store(y, r * d + (m * L + l) * 8, left[m], v[m] * rstd * ww[m] + bb[m]);
@@ -256,31 +260,31 @@ __global__ void __launch_bounds__(threads<L>()) backward_kernel(
   }
   const float inv_d = 1.0f / d;
   int turn = 0;
+  // The next row on its way while this one is worked on; 1,024 lanes have 128
+  // registers each, enough for one row only (512 x 12288 bf16: with the next one,
+  // spilled, 34 us, without 27).
+  constexpr bool AHEAD = L < 1024;
   Eight<XB> rx[M];
   Eight<YB> ry[M];
+  auto load = [&](int64_t r) {
 #pragma unroll
-  for (int m = 0; m < M; ++m) {
-    rx[m].load(x, q * d + (m * L + l) * 8, left[m]);
-    ry[m].load(dy, q * d + (m * L + l) * 8, left[m]);
-  }
+    for (int m = 0; m < M; ++m) {
+      rx[m].load(x, r * d + (m * L + l) * 8, left[m]);
+      ry[m].load(dy, r * d + (m * L + l) * 8, left[m]);
+    }
+  };
+  if (AHEAD) load(q);
   for (int64_t r = q; r < rows; r += Q) {
+    if (!AHEAD) load(r);
     f32x8 v[M], g[M];
 #pragma unroll
     for (int m = 0; m < M; ++m) {
       v[m] = rx[m].get();
       g[m] = ry[m].get();
     }
-    if (r + Q < rows)
-#pragma unroll
-      for (int m = 0; m < M; ++m) {
-        rx[m].load(x, (r + Q) * d + (m * L + l) * 8, left[m]);
-        ry[m].load(dy, (r + Q) * d + (m * L + l) * 8, left[m]);
-      }
-    f32x8 t[M];  // dy w (0 past d: dy is)
-#pragma unroll
-    for (int m = 0; m < M; ++m) t[m] = g[m] * ww[m];
-    float rstd, m0, m1;
-    statistics<L, M, 1>(v, t, left, inv_d, eps, s_part, turn, rstd, m0, m1);
+    if (AHEAD && r + Q < rows) load(r + Q);
+    float rstd, m0, m1;  // (past d dy is 0, and so is t)
+    statistics<L, M, 1>(v, g, ww, left, inv_d, eps, s_part, turn, rstd, m0, m1);
     m0 *= inv_d;
     m1 *= inv_d * rstd;
 #pragma unroll
@@ -288,7 +292,7 @@ __global__ void __launch_bounds__(threads<L>()) backward_kernel(
       v[m] *= rstd;  // xh
       db[m] += g[m];
       dw[m] += g[m] * v[m];
-      Eight<XB>::store(dx, r * d + (m * L + l) * 8, left[m], rstd * (t[m] - m0 - v[m] * m1));
+      Eight<XB>::store(dx, r * d + (m * L + l) * 8, left[m], rstd * (g[m] * ww[m] - m0 - v[m] * m1));
     }
   }
   if (part) {
@@ -337,11 +341,17 @@ int64_t owners(int64_t rows, int64_t groups, int64_t most) {
   const int64_t q = most < 1 ? 1 : most > rows ? rows : most;
   return (q + groups - 1) / groups * groups;
 }
+// lanes for the card: us at 2,048 / 4,096 a CU: 393216 x 128 bf16 36 / 31, 65536 x
+// 1024 44 / 42, 16384 x 4096 44 / 42; 8192 x 5000, where a row takes a workgroup of
+// 512, 35 / 38
 int64_t forward_owners(int64_t rows, int64_t groups, int L) {
   return owners(rows, groups, 256 * (L <= 256 ? 4096 : 2048) / L);
 }
-// Every owner of the backward also writes 2 d sums, which are read again: at
-// least eight rows each, unless that leaves CUs without a workgroup.
+// Every owner of the backward also writes 2 d sums, which are read again: fewer
+// lanes (1,024 a CU and run of eight columns; us with half of that / that / twice:
+// 393216 x 128 bf16 74 / 61 / 70, 65536 x 1024 91 / 91 / 113), and at least eight
+// rows each (1024 x 4096: 16, with two rows each 20) unless that leaves CUs without
+// a workgroup (512 x 12288 fp32: 128 owners 59, 256 48).
 int64_t backward_owners(int64_t rows, int64_t groups, int L, int M) {
   const int64_t one_each = 256 * (L < 256 ? 256 / L : 1);  // a workgroup a CU
   int64_t q = 256 * 1024 / (L * M);

@@ -130,7 +130,11 @@ hipError_t launch(const Operand& q, const Operand& k, const Operand& v, const De
                   int64_t num_slots, const int32_t* slots, void* o, bool o_bf16, int N, int H,
                   float scale, hipStream_t s) {
   const int64_t pairs = (int64_t)N * H;
-  const bool tiled = pairs < 512;
+  // Few states: 32 columns a workgroup, so that more CUs take part; many: a whole
+  // state each.  us whole / tiled at 128 x 128: fp32 96 states 4.2 / 3.9, 384 8.0 /
+  // 7.8, 768 13.7 / 17.9; bf16, where 32 columns are half a cache line, 32 states
+  // 3.8 / 3.5, 96 4.0 / 4.1, 384 5.5 / 6.7.
+  const bool tiled = pairs < (S_BF16 ? 96 : 512);
   const int64_t blocks = pairs * (tiled ? DV / 32 : 1);
   if (blocks > 0x7ffffff8) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>((blocks + 7) / 8 * 8));

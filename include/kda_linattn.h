@@ -59,10 +59,13 @@ extern "C" {
  *         them; a NULL or smaller workspace is allowed, the sequences are then
  *         walked whole (the same result to rounding, with fewer workgroups).
  * Accuracy: products run on bf16 MFMA with fp32 accumulation.  bf16 q, k and v
- * enter exactly and the states and the decayed factors as sums of two or three
- * bf16 values, so o and the state agree with an fp64 recurrence to about 3e-6
- * of their norm plus their own rounding; fp32 q, k and v enter as three bf16
- * values each (about 1e-6).
+ * enter exactly and the values that make the state as sums of three bf16 values:
+ * the state agrees with an fp64 recurrence to about 3e-7 of its norm.  The scores
+ * and states that make o enter as one bf16 value where o is bf16 and the call has
+ * more than 64 tokens (each off by at most 2^-8 of itself: o is 2.3e-3 of its norm
+ * off, where bf16's own rounding makes 1.7e-3), else as two (o fp32: about 3e-6).
+ * fp32 q, k and v enter as three bf16 values each, and so does everything that
+ * they meet (about 3e-7).
  */
 kda_status kda_linattn_chunk_prefill(const void* q, int64_t q_stride, const void* k,
                                      int64_t k_stride, const void* v, int64_t v_stride,
@@ -94,6 +97,9 @@ size_t kda_linattn_chunk_prefill_workspace_bytes(int64_t T_tot, int32_t N, int32
  * may be NULL (zero).  Rows behind the last sequence are left as they were.
  * A g below -110 gets the gradient of the recurrence at -110.
  * The sums run in a fixed order: the same call gives the same bits.
+ * Accuracy: dv as o above; dq, dk and d_initial_state 3e-7 of their norm plus
+ * their rounding; dg is a small difference of sums of products, formed from
+ * three-value factors and summed in 64 bits: 1e-6 to 5e-6 of its norm.
  * workspace: kda_linattn_chunk_prefill_backward_workspace_bytes, 256-byte
  * aligned, KDA_ERR_WORKSPACE below it.
  */
