@@ -50,7 +50,13 @@
 // What bounds it: a layer of 96 heads gives 192 workgroups for 256 CUs, each with
 // T / 64 chunks to go through one after the other; in a chunk LDS moves about
 // 250 KB at 128 B a cycle (stores into it at 79), and the matrix and the vector
-// units of a SIMD take about 2,000 cycles each.
+// units of a SIMD take about 2,000 cycles each.  Measured, dk = dv = 128, bf16:
+// T = 4096 x 96 heads 119 us (1.65 us a chunk of a lone workgroup; 3.5 TB/s of what
+// has to be read and written), 8 sequences of 32,768 tokens together x 96 843 us
+// (4.0 TB/s), one of 131,072 x 16 heads, in segments, 764 us; backward of T = 4096 x
+// 96 430 us.  On the way there: scores and readout in the state's waves 302 us, waves
+// of two kinds 253, copies and decays in waves of their own 167, one value of S and P
+// and eight output columns a store 119.
 //
 // Fragments (16x16x32: lane = (lr, lg), lr the row or column, k = 8 lg + e):
 //   scores     computed transposed, b a^T: the accumulators of two row tiles of
@@ -95,6 +101,7 @@ constexpr int C = 64;        // tokens a chunk
 constexpr int CT = 64;       // columns a workgroup
 constexpr int NTHR = 256;    // threads of the small kernels, and of the state waves
 constexpr int kMinSegChunks = 4;   // shortest segment of a cut sequence
+constexpr int64_t kCus = 256;
 constexpr int kBorderChunks = 32;  // segments of dg's sums when sequences are walked whole
 
 // swizzle of the 16-byte block index of a row (rows of 128 / 64 channels)
@@ -199,7 +206,7 @@ struct Walk {
   const int32_t* out_idx;
   int64_t in_slots, out_slots;
   void* out;                // [T, H, CD]
-  float* dots;              // [T, H, 4]: x_t . out_t without the pair (t, t), per 32 columns
+  float* dots;              // [H, T, 4]: x_t . out_t without the pair (t, t), per 32 columns
   float* ends;              // states at the segments' ends (dg), slot-major, or null
   float* seg_state;         // cut sequences: each segment's own state, then its entry state
   float* seg_decay;         // cut sequences: each segment's summed log2-decay [slot, H]
@@ -1028,7 +1035,7 @@ __device__ __forceinline__ void walk(const Args& A, const Walk& W, int block, ch
             }
             dot = sum_rows(dot);
             if (lg == 0 && row < rows)
-              W.dots[(((int64_t)bos + c * C + tok) * A.H + h) * 4 + 2 * tile + jh] = dot;
+              W.dots[((int64_t)h * A.T_tot + bos + c * C + tok) * 4 + 2 * tile + jh] = dot;
           }
           for_planes<NPL, NPP>([&](int i, int k) {
 #pragma unroll
@@ -1082,19 +1089,20 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
   walk<WIDE, KD, FULL, DOTS, PL>(A, A.walk[A.first + blockIdx.y], blockIdx.x, lds);
 }
 
-// The three walks of the backward in one launch, the longer ones of dq and dk
-// first: at one workgroup a CU, dv's fill the CUs that those leave idle at their
-// end.  n_qk: workgroups of dq's walk.
+// The three walks of the backward in one launch, at one workgroup a CU: dq, the
+// first v1 workgroups of dv, dk, the rest of dv.  n_qk, n_v: workgroups of dq's and
+// of dv's walk; they and v1 are multiples of 8.
 template <int DK, int DV, int PLV>
-__global__ void __launch_bounds__((Waves<false, true>::threads), 1) gradient_kernel(Args A, int n_qk) {
+__global__ void __launch_bounds__((Waves<false, true>::threads), 1)
+    gradient_kernel(Args A, int n_qk, int v1) {
   constexpr int a = lds_bytes<false, DV, true, true, 3>(), b = lds_bytes<false, DK, true, false, PLV>();
   __shared__ __attribute__((aligned(16))) char lds[a > b ? a : b];
   const int block = blockIdx.x;
-  if (block < 2 * n_qk) {
+  if (block < n_qk || (block >= n_qk + v1 && block < 2 * n_qk + v1)) {
     const int y = block >= n_qk;
-    walk<false, DV, true, true, 3>(A, A.walk[y], block - y * n_qk, lds);
+    walk<false, DV, true, true, 3>(A, A.walk[y], block - (y ? n_qk + v1 : 0), lds);
   } else {
-    walk<false, DK, true, false, PLV>(A, A.walk[2], block - 2 * n_qk, lds);
+    walk<false, DK, true, false, PLV>(A, A.walk[2], block - (block < n_qk + v1 ? 1 : 2) * n_qk, lds);
   }
 }
 
@@ -1172,12 +1180,15 @@ __global__ void __launch_bounds__(NTHR) scan_kernel(Args A) {
 }
 
 // dg of one segment of one (sequence, head): suffix sums of q.dq - k.dk, plus
-// <S, dL/dS> at the segment's end.  In 64 bits (a few thousand terms).
-__global__ void __launch_bounds__(NTHR) dg_kernel(Args A, const float* dotq, const float* dotk,
+// <S, dL/dS> at the segment's end.  In 64 bits (a few thousand terms).  512 lanes:
+// a segment of 2,048 tokens is few trips to memory (the whole backward of T = 4096
+// x 96 with 256 / 512 / 1,024: 436 / 431 / 433 us; of T = 128 x 4, 12.9 / 13.6 / 14.6).
+constexpr int DGT = 512;
+__global__ void __launch_bounds__(DGT) dg_kernel(Args A, const float* dotq, const float* dotk,
                                                   const float* ends_s, const float* ends_d,
                                                   int dk, int dv, bool has_final, float* dg,
                                                   float* dg_part, int nseg_max) {
-  __shared__ double s_w[4];
+  __shared__ double s_w[DGT / 64];
   const int h = blockIdx.x % A.H;
   const int seg = (blockIdx.x / A.H) % nseg_max;
   const int n = blockIdx.x / A.H / nseg_max;
@@ -1196,14 +1207,20 @@ __global__ void __launch_bounds__(NTHR) dg_kernel(Args A, const float* dotq, con
     const f32x4* a = reinterpret_cast<const f32x4*>(ends_s + (slot * A.H + h) * elems);
     const f32x4* b = reinterpret_cast<const f32x4*>(ends_d + (slot * A.H + h) * elems);
     f32x4 p = {0.f, 0.f, 0.f, 0.f};
-    for (int i = tid; i < elems / 4; i += NTHR) p += a[i] * b[i];
+    for (int i = tid; i < elems / 4; i += DGT) p += a[i] * b[i];
     m = ((double)p[0] + (double)p[1]) + ((double)p[2] + (double)p[3]);
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) m += __shfl_xor(m, off);
   if (lane == 0) s_w[w] = m;
   __syncthreads();
-  const double border = (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
+  auto all_waves = [&] {
+    double x = 0.0;
+#pragma unroll
+    for (int j = 0; j < DGT / 64; ++j) x += s_w[j];
+    return x;
+  };
+  const double border = all_waves();
   __syncthreads();
   const int t_lo = seg * A.seg_chunks * C;
   const int t_hi = t_lo + A.seg_chunks * C < len ? t_lo + A.seg_chunks * C : len;
@@ -1213,11 +1230,11 @@ __global__ void __launch_bounds__(NTHR) dg_kernel(Args A, const float* dotq, con
     run *= exp((double)clamp_log_decay(g));
   }
   double total = 0.0;
-  for (int hi = t_hi; hi > t_lo; hi -= NTHR) {
+  for (int hi = t_hi; hi > t_lo; hi -= DGT) {
     const int t = hi - 1 - tid;
     double x = 0.0;
     if (t >= t_lo) {  // one partial dot per 32 channels
-      const int64_t at = (((int64_t)bos + t) * A.H + h) * 4;
+      const int64_t at = ((int64_t)h * A.T_tot + bos + t) * 4;
       const f32x4 a = *reinterpret_cast<const f32x4*>(dotq + at);
       const f32x4 b = *reinterpret_cast<const f32x4*>(dotk + at);
       x = ((double)a[0] - (double)b[0]) + ((double)a[1] - (double)b[1]);
@@ -1233,7 +1250,7 @@ __global__ void __launch_bounds__(NTHR) dg_kernel(Args A, const float* dotq, con
     double before = run;
     for (int j = 0; j < w; ++j) before += s_w[j];
     x += before;
-    run += (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
+    run += all_waves();
     __syncthreads();
     if (t >= t_lo) {
       if (A.g.per_token) dg[((int64_t)bos + t) * A.H + h] = (float)x;
@@ -1246,7 +1263,7 @@ __global__ void __launch_bounds__(NTHR) dg_kernel(Args A, const float* dotq, con
     if (lane == 0) s_w[w] = total;
     __syncthreads();
     if (tid == 0) {
-      const double s = (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
+      const double s = all_waves();
       dg_part[2 * (slot * A.H + h)] = (float)s;
       dg_part[2 * (slot * A.H + h) + 1] = (float)(s - (double)(float)s);
     }
@@ -1344,11 +1361,18 @@ hipError_t launch_walk(const Args& A, int walks, bool wide, int kd, bool full, b
 
 template <int DK, int DV>
 hipError_t launch_gradients_kd(const Args& A, bool two, hipStream_t s) {
-  const int64_t qk = walk_blocks(A, DV), blocks = 2 * qk + walk_blocks(A, DK);
+  const int64_t qk = walk_blocks(A, DV), v = walk_blocks(A, DK), blocks = 2 * qk + v;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  // A workgroup of dq or dk takes about half as long again as one of dv.  Where a
+  // third round of workgroups would leave more than half of the CUs idle, two
+  // thirds of dv's go before dk's: the CUs then get two of the long ones or three of
+  // the short ones each (T = 4096 x 96: 427 us, in the order dq, dk, dv 450; with
+  // more rounds, 8 sequences x 96, 3640 against 3515).
+  const bool mixed = qk == v && blocks > 2 * kCus && blocks <= 5 * kCus / 2;
+  const int v1 = mixed ? (int)(v / 12 * 8) : 0;
   const dim3 grid((unsigned)blocks), block(Waves<false, true>::threads);
-  if (two) gradient_kernel<DK, DV, 2><<<grid, block, 0, s>>>(A, (int)qk);
-  else gradient_kernel<DK, DV, 1><<<grid, block, 0, s>>>(A, (int)qk);
+  if (two) gradient_kernel<DK, DV, 2><<<grid, block, 0, s>>>(A, (int)qk, v1);
+  else gradient_kernel<DK, DV, 1><<<grid, block, 0, s>>>(A, (int)qk, v1);
   return hipGetLastError();
 }
 // all walks of the backward, bf16 operands
@@ -1380,7 +1404,6 @@ hipError_t launch_scan(const Args& A, int walks, int kd, hipStream_t s) {
 // against 2: H = 16, T = 4096 40 / 47, H = 1, T = 131072 84 / 113, H = 16, T =
 // 131072 788 / 779); two backward, where workgroups of different length even out
 // (H = 8, T = 32768 609 / 556).
-constexpr int64_t kCus = 256;
 int cut_chunks(int64_t T_tot, int64_t N, int64_t walkers, int64_t longest, int rounds) {
   const int64_t chunks = cdiv(T_tot, C), all = chunks * walkers, even = cdiv(all, kCus);
   // (the bounds on N keep the workspace small: a state per sequence and segment)
@@ -1597,7 +1620,7 @@ hipError_t launch_backward(const Problem& p, const Operand& q, const Operand& k,
   }
   const int64_t blocks = (int64_t)p.N * nseg * p.H;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  dg_kernel<<<dim3((unsigned)blocks), NTHR, 0, s>>>(A, b.dotq, b.dotk, b.ends_s, b.ends_d, DK, DV,
+  dg_kernel<<<dim3((unsigned)blocks), DGT, 0, s>>>(A, b.dotq, b.dotk, b.ends_s, b.ends_d, DK, DV,
                                                     dS != nullptr, dg, b.dg_part, nseg);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
