@@ -23,6 +23,11 @@
  * g_len == H); other lengths are refused (KDA_ERR_SHAPE).  A g below -110 is
  * taken as -110: exp(-110) is 0 beside any fp32 value that is not tiny.
  *
+ * q, k, v, d_o and the states must be finite: a NaN or an infinity of one token
+ * may reach every token of its chunk of 64 of that sequence and head, those
+ * before it too.  A NaN in g is carried on.  (Rows of q, k, v and g that belong
+ * to no sequence may hold anything.)
+ *
  * Strides: q, k and v give the distance between tokens (sequences, in the
  * decode) in elements: at least heads * dim, so that they may be slices of a
  * fused projection; heads and channels are dense.  Rows are 16-byte aligned.

@@ -254,6 +254,45 @@ def test_backward_long(H):
     say(ref.check_backward(got, q, k, v, g, cu, do, S0, dS))
 
 
+# lens, H, Hk, dk, dv: more heads than the card's XCDs but no multiple of them, and the
+# backward's workgroups in mixed order (88 heads); one long sequence of several, cut
+# into segments, with heads that fill the XCDs unevenly; the same with dk != dv
+UNEVEN = [
+    ([70, 3], 88, 44, 128, 128),
+    ([3200, 5, 7], 12, 3, 64, 64),
+    ([1300, 0, 40], 9, 9, 128, 64),
+]
+
+
+@pytest.mark.parametrize("case", range(len(UNEVEN)))
+def test_uneven_heads_and_lengths(case):
+    need_gpu()
+    lens, H, Hk, dk, dv = UNEVEN[case]
+    say("linattn uneven", UNEVEN[case])
+    q, k, v, g, cu, S0 = _draw(lens, H, Hk, dk, dv, BF, "mild", 550 + case)
+    o, S = kda.linattn_chunk_prefill(*_gpu(q, k, v, g), **_cu(cu), initial_state=S0.to(DEV))
+    say(ref.check_forward(o, S, q, k, v, g, cu, S0))
+    gen = torch.Generator().manual_seed(case)
+    do = torch.randn(cu[-1], H, dv, generator=gen).to(BF)
+    dS = torch.randn(len(lens), H, dk, dv, generator=gen)
+    got = kda.linattn_chunk_prefill_backward(*_gpu(q, k, v, g, do), **_cu(cu),
+                                             initial_state=S0.to(DEV), d_final_state=dS.to(DEV))
+    say(ref.check_backward(got, q, k, v, g, cu, do, S0, dS))
+
+
+@pytest.mark.parametrize("decay", ["mild", "head"])
+def test_a_first_token_has_no_decay_gradient(decay):
+    """Sequences of one token from zeros: nothing decays, so dg is exactly 0 (its sums leave
+    the pairs of a token with itself out, they do not cancel)."""
+    need_gpu()
+    say("linattn first tokens", decay)
+    q, k, v, g, cu, _ = _draw([1, 0, 1, 1], 3, 3, 128, 64, BF, decay, 560, state=False)
+    do = torch.randn(cu[-1], 3, 64, generator=torch.Generator().manual_seed(6)).to(BF)
+    got = kda.linattn_chunk_prefill_backward(*_gpu(q, k, v, g, do), **_cu(cu))
+    assert torch.equal(got[3].cpu(), torch.zeros_like(g))
+    say(ref.check_backward(got[:3], q, k, v, g, cu, do))
+
+
 def test_backward_is_deterministic_and_leaves_rows_behind():
     need_gpu()
     say("linattn backward twice")
