@@ -104,11 +104,16 @@ constexpr int kMinSegChunks = 4;   // shortest segment of a cut sequence
 constexpr int64_t kCus = 256;
 constexpr int kBorderChunks = 32;  // segments of dg's sums when sequences are walked whole
 
-// swizzle of the 16-byte block index of a row (rows of 128 / 64 channels)
+// Swizzle of the 16-byte block index of a row (rows of 128 / 64 channels).  A read
+// of 16 bytes a lane goes through 64 banks in four steps, and a step takes rows 0-3
+// and 12-15 of one k block with rows 4-11 of the next: the low bits of rows 0-3 and
+// 12-15 are therefore made to differ in bit 0 only, so that a step's 16 blocks are
+// all different.  (Low bits row >> 2: every such read took twice as long.)
 template <int W>
 __device__ __forceinline__ int swz(int row) {
-  if constexpr (W == 128) return ((row & 3) << 2) | ((row >> 2) & 3);
-  else return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+  const int x = (row >> 2) & 3, low = ((x & 1) << 1) ^ ((x >> 1) * 3);  // 0, 2, 3, 1
+  if constexpr (W == 128) return ((row & 3) << 2) | low;
+  else return (((row >> 1) & 1) << 2) | low;
 }
 
 __device__ __forceinline__ f32x8 widen8(bf16x8 x) { return __builtin_convertvector(x, f32x8); }
