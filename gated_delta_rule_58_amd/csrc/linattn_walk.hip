@@ -48,13 +48,14 @@
 // T = 4096 x 96 679 against 545 us).  fp32 operands, three values each: the state
 // waves copy, with one buffer and a second barrier.
 // What bounds it: a layer of 96 heads gives 192 workgroups for 256 CUs, each with
-// T / 64 chunks to go through one after the other; in a chunk LDS moves about
-// 250 KB at 128 B a cycle (stores into it at 79), and the matrix and the vector
-// units of a SIMD take about 2,000 cycles each.  Measured, dk = dv = 128, bf16:
-// T = 4096 x 96 heads 119 us (1.65 us a chunk of a lone workgroup; 3.5 TB/s of what
-// has to be read and written), 8 sequences of 32,768 tokens together x 96 843 us
-// (4.0 TB/s), one of 131,072 x 16 heads, in segments, 764 us; backward of T = 4096 x
-// 96 430 us.  On the way there: scores and readout in the state's waves 302 us, waves
+// T / 64 chunks to go through one after the other, about 4,000 cycles each.  Of
+// those LDS is busy for 1,600 (16-byte reads at 256 B a cycle, transposing ones at
+// 128, stores at 80 to 128) and the matrix units of a SIMD for 1,400; the rest is
+// the chain scores -> decays -> c^T P^T of an output wave.  Measured, dk = dv = 128, bf16:
+// T = 4096 x 96 heads 117 us (1.65 us a chunk of a lone workgroup; 3.5 TB/s of what
+// has to be read and written), 8 sequences of 32,768 tokens together x 96 833 us
+// (4.0 TB/s), one of 131,072 x 16 heads, in segments, 761 us; backward of T = 4096 x
+// 96 432 us.  On the way there: scores and readout in the state's waves 302 us, waves
 // of two kinds 253, copies and decays in waves of their own 167, one value of S and P
 // and eight output columns a store 119.
 //
@@ -768,6 +769,10 @@ __device__ __forceinline__ void walk(const Args& A, const Walk& W, int block, ch
     // row tiles T0 and T1 (fixed at compile time: no branches inside, so that the
     // loads of one product can be placed among the arithmetic of another),
     // column tiles 2 jh and 2 jh + 1
+    // the longest chain of a chunk is theirs: before the state waves of their SIMDs
+    // (without: 8 sequences x 96 heads 882 against 865 us on one card, T = 4096 126
+    // against 120)
+    __builtin_amdgcn_s_setprio(2);
     const int jh = w & 1;
     const bool x_bf = !WIDE || W.x.bf16, o_bf = W.out_bf16;
     const Rows a_rows(W.a, a_bf, bos, h, KD, 0, KD);
