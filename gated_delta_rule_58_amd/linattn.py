@@ -108,6 +108,12 @@ def _sequences(rows, cu_seqlens, cu_seqlens_host, num_seqs):
     return N, cu_seqlens_host.contiguous()
 
 
+def _new_rows(cu_seqlens, cu_seqlens_host):
+    """The allocator of outputs that the library writes the rows of sequences of.  Without the
+    host's lengths the last sequence may end before the last row; those rows are zeros."""
+    return torch.zeros if cu_seqlens is not None and cu_seqlens_host is None else torch.empty
+
+
 def _host_ptr(t):
     return None if t is None else ctypes.cast(t.data_ptr(), _vp)
 
@@ -138,6 +144,8 @@ def linattn_chunk_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
     bfloat16, or with state_indices (int32 [N] on the device) pools
     [num_slots, H, dk, dv], in which final_state (possibly initial_state itself) is
     written only when passed.  workspace: uint8; None allocates what the library asks for.
+    Rows behind the last sequence (cu_seqlens[N] < T, which needs cu_seqlens_host to be
+    missing) stay as they were in `out`, and are zeros when out is None.
     Returns (o [T, H, dv], final state or None)."""
     T, H, Hk, dk, dv = _inputs(q, k, v, g)
     dev = q.device
@@ -152,7 +160,8 @@ def linattn_chunk_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
         _shape("state_indices", state_indices, N)
         output_final_state = False  # a pool is written only when passed as final_state
     if out is None:
-        out = torch.empty((T, H, dv), dtype=o_dtype or q.dtype, device=dev)
+        out = _new_rows(cu_seqlens, cu_seqlens_host)((T, H, dv), dtype=o_dtype or q.dtype,
+                                                     device=dev)
     _shape("out", out, T, H, dv)
     if final_state is None and output_final_state:
         final_state = torch.empty((N, H, dk, dv), dtype=state_dtype, device=dev)
@@ -195,6 +204,8 @@ def linattn_chunk_prefill_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Te
                                    workspace: Optional[torch.Tensor] = None, num_seqs: int = 1):
     """kda_linattn_chunk_prefill_backward: gradients of linattn_chunk_prefill's (o,
     final state) against d_o [T, H, dv] (None: zero) and d_final_state (None: zero).
+    The gradients of rows behind the last sequence (cu_seqlens[N] < T, which needs
+    cu_seqlens_host to be missing) are zeros.
 
     Returns (dq, dk [T, Hk, dk], dv [T, H, dv] in grad_dtype (default: q's), dg in g's
     shape, float32, d_initial_state [N, H, dk, dv] float32 or None)."""
@@ -208,10 +219,11 @@ def linattn_chunk_prefill_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Te
         _dtype(name, t, torch.float32)
         _shape(name, t, N, H, dk, dv)
     gdt = grad_dtype or q.dtype
-    dq = torch.empty((T, Hk, dk), dtype=gdt, device=dev)
-    dk_ = torch.empty((T, Hk, dk), dtype=gdt, device=dev)
-    dv_ = torch.empty((T, H, dv), dtype=gdt, device=dev)
-    dg = torch.empty(tuple(g.shape), dtype=torch.float32, device=dev)
+    rows = _new_rows(cu_seqlens, cu_seqlens_host)
+    dq = rows((T, Hk, dk), dtype=gdt, device=dev)
+    dk_ = rows((T, Hk, dk), dtype=gdt, device=dev)
+    dv_ = rows((T, H, dv), dtype=gdt, device=dev)
+    dg = rows(tuple(g.shape), dtype=torch.float32, device=dev)
     dS0 = (torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
            if want_d_initial_state else None)
     if workspace is None:
