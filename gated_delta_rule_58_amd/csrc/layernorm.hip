@@ -16,9 +16,12 @@
 // Neighbouring lanes own neighbouring rows, so a wave's access is contiguous
 // whatever L is.  The next row is loaded before this one is worked on.
 //
-// The statistics are two sums over the registers (mean, then the mean square
-// of the differences), so large means cost no digits.  The backward forms them
-// again from x, which it reads anyway, rather than read stored ones.
+// The statistics are two sums over the registers: the mean, then the differences
+// from it and their squares.  The mean of fp32 sums is a few ulps off, which beside a
+// spread far below the mean is not small (a row of 1000.0, d = 1000: every value 6e-5
+// off, times 1 / sqrt(eps)); the sum of the differences gives that error, which comes
+// off the values and off the mean square.  The backward forms the statistics again
+// from x, which it reads anyway, rather than read stored ones.
 //
 // dw and db: each row owner adds its rows into registers in order and writes
 // one partial row; a second kernel adds the partials of a weight row in a fixed
@@ -113,13 +116,13 @@ __device__ __forceinline__ float moved(float x) {  // x of the lane that CTRL na
   return __uint_as_float(
       __builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), CTRL, 0xf, 0xf, true));
 }
-// Sum over aligned groups of L (8 .. 64) lanes, in all of them.  Moves between
+// Sum over aligned groups of L (4 .. 64) lanes, in all of them.  Moves between
 // registers: an LDS permute takes some 60 clocks, and a row waits for its sums.
 template <int L>
 __device__ __forceinline__ float lanes_sum(float x) {
   x += moved<0xb1>(x);                                  // lane ^ 1
   x += moved<0x4e>(x);                                  // lane ^ 2
-  x += moved<0x141>(x);                                 // 7 - lane of eight: the other four
+  if constexpr (L >= 8) x += moved<0x141>(x);           // 7 - lane of eight: the other four
   if constexpr (L >= 16) x += moved<0x140>(x);          // 15 - lane of sixteen: the other eight
   if constexpr (L >= 32) {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -132,42 +135,44 @@ __device__ __forceinline__ float lanes_sum(float x) {
   return x;
 }
 
+constexpr int kSums = 3;  // most values of one row_sum
+
 // Sums of NS values over the L lanes of a row; every lane gets them.  Rows of
 // a whole workgroup (L = its size) go through LDS, double-buffered by `turn`
 // so that one barrier a sum is enough.
 template <int L, int NS>
 __device__ __forceinline__ void row_sum(float (&x)[NS], float* s_part, int& turn) {
+  static_assert(NS <= kSums, "size of s_part");
 #pragma unroll
   for (int i = 0; i < NS; ++i) x[i] = lanes_sum<(L < 64 ? L : 64)>(x[i]);
   if constexpr (L > 64) {
     constexpr int W = L / 64;
-    float* p = s_part + turn * (2 * W);
+    float* p = s_part + turn * (kSums * W);
     turn ^= 1;
     if ((threadIdx.x & 63) == 0)
 #pragma unroll
       for (int i = 0; i < NS; ++i) p[i * W + (threadIdx.x >> 6)] = x[i];
     barrier_lds();
+    // each lane takes one wave's part: a read and a few moves.  (W reads a lane: 512 x
+    // 12288 fp32 backward 52 us against 28, 16 waves' registers run out; 8192 x 5000
+    // bf16, 8 waves, 92 against 94.)
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      float s = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) s += p[i * W + w];
-      x[i] = s;
-    }
+    for (int i = 0; i < NS; ++i) x[i] = lanes_sum<W>(p[i * W + (threadIdx.x & (W - 1))]);
   }
 }
 
 template <int L>
 constexpr int threads() { return L > 256 ? L : 256; }
 
-// x (columns past d hold 0) becomes x - mean; rstd = 1/sqrt(var + eps).  With
-// T = 1 the sums of t = dy w and of t (x - mean) come along with the two sums
-// (t is formed where it is needed: the registers do not hold it too).
+// x (columns past d hold 0) becomes x less its computed mean, with x rstd + shift the
+// normalised value (past d something finite); rstd = 1/sqrt(var + eps).  With T = 1 the
+// sums of t = dy w and of t (x - mean) come along with the two sums (t is formed where it
+// is needed: the registers do not hold it too).
 template <int L, int M, int T>
 __device__ __forceinline__ void statistics(f32x8 (&x)[M], const f32x8 (&dy)[T ? M : 1],
                                            const f32x8 (&w)[T ? M : 1], const int (&left)[M],
                                            float inv_d, float eps, float* s_part, int& turn,
-                                           float& rstd, float& st, float& stx) {
+                                           float& rstd, float& shift, float& st, float& stx) {
   float s[1 + T] = {};
 #pragma unroll
   for (int m = 0; m < M; ++m) {
@@ -176,19 +181,23 @@ __device__ __forceinline__ void statistics(f32x8 (&x)[M], const f32x8 (&dy)[T ? 
   }
   row_sum<L, 1 + T>(s, s_part, turn);
   const float mu = s[0] * inv_d;
-  float v[1 + T] = {};
+  float v[2 + T] = {};
 #pragma unroll
   for (int m = 0; m < M; ++m) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[m][e] = e < left[m] ? x[m][e] - mu : 0.f;
     v[0] += sum8(x[m] * x[m]);
-    if constexpr (T) v[1] += sum8(dy[m] * w[m] * x[m]);
+    v[1] += sum8(x[m]);
+    if constexpr (T) v[2] += sum8(dy[m] * w[m] * x[m]);
   }
-  row_sum<L, 1 + T>(v, s_part, turn);
-  rstd = 1.0f / sqrtf(v[0] * inv_d + eps);
+  row_sum<L, 2 + T>(v, s_part, turn);
+  const float off = v[1] * inv_d;  // the mean's own error
+  const float var = v[0] * inv_d - off * off;
+  rstd = 1.0f / sqrtf((var < 0.f ? 0.f : var) + eps);  // (a NaN stays one)
+  shift = -off * rstd;
   if constexpr (T) {
     st = s[1];
-    stx = v[1];
+    stx = v[2] - off * st;
   }
 }
 
@@ -198,7 +207,7 @@ __global__ void __launch_bounds__(threads<L>()) forward_kernel(
     const void* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b,
     int64_t groups, void* __restrict__ y, int64_t rows, int d, float eps, int64_t Q) {
   constexpr int RPB = threads<L>() / L;
-  __shared__ float s_part[L > 64 ? 4 * (L / 64) : 1];
+  __shared__ float s_part[L > 64 ? 2 * kSums * (L / 64) : 1];
   const int l = threadIdx.x % L;
   const int64_t q = (int64_t)blockIdx.x * RPB + threadIdx.x / L;
   if (q >= Q || q >= rows) return;  // whole rows of lanes leave together (L > 64: the workgroup)
@@ -227,12 +236,13 @@ __global__ void __launch_bounds__(threads<L>()) forward_kernel(
     if (r + Q < rows)
 #pragma unroll
       for (int m = 0; m < M; ++m) raw[m].load(x, (r + Q) * d + (m * L + l) * 8, left[m]);
-    float rstd, none;
+    float rstd, shift, none;
     const f32x8 no_t[1] = {};
-    statistics<L, M, 0>(v, no_t, no_t, left, inv_d, eps, s_part, turn, rstd, none, none);
+    statistics<L, M, 0>(v, no_t, no_t, left, inv_d, eps, s_part, turn, rstd, shift, none, none);
 #pragma unroll
     for (int m = 0; m < M; ++m)
-      Eight<YB>::store(y, r * d + (m * L + l) * 8, left[m], v[m] * rstd * ww[m] + bb[m]);
+      Eight<YB>::store(y, r * d + (m * L + l) * 8, left[m],
+                       (v[m] * rstd + shift) * ww[m] + bb[m]);
   }
 }
 
@@ -242,7 +252,7 @@ __global__ void __launch_bounds__(threads<L>()) backward_kernel(
     int64_t groups, void* __restrict__ dx, float* __restrict__ part, int64_t rows, int d,
     float eps, int64_t Q) {
   constexpr int RPB = threads<L>() / L;
-  __shared__ float s_part[L > 64 ? 4 * (L / 64) : 1];
+  __shared__ float s_part[L > 64 ? 2 * kSums * (L / 64) : 1];
   const int l = threadIdx.x % L;
   const int64_t q = (int64_t)blockIdx.x * RPB + threadIdx.x / L;
   if (q >= Q || q >= rows) return;
@@ -283,13 +293,13 @@ __global__ void __launch_bounds__(threads<L>()) backward_kernel(
       g[m] = ry[m].get();
     }
     if (AHEAD && r + Q < rows) load(r + Q);
-    float rstd, m0, m1;  // (past d dy is 0, and so is t)
-    statistics<L, M, 1>(v, g, ww, left, inv_d, eps, s_part, turn, rstd, m0, m1);
+    float rstd, shift, m0, m1;  // (past d dy is 0, and so is t)
+    statistics<L, M, 1>(v, g, ww, left, inv_d, eps, s_part, turn, rstd, shift, m0, m1);
     m0 *= inv_d;
     m1 *= inv_d * rstd;
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      v[m] *= rstd;  // xh
+      v[m] = v[m] * rstd + shift;  // xh
       db[m] += g[m];
       dw[m] += g[m] * v[m];
       Eight<XB>::store(dx, r * d + (m * L + l) * 8, left[m], rstd * (g[m] * ww[m] - m0 - v[m] * m1));

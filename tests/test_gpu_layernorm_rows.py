@@ -1,0 +1,93 @@
+"""GPU: layer norm of rows whose spread is small beside their mean, against 64-bit
+formulas.
+
+Bounds, in u = 2^-24 per fp32 rounding and with l = log2 d + 10 roundings on the way of
+a sum (a thread adds up to 16 values in turn, the rest are pairwise) and of the division
+by d.  A = max |x|, c = x - mean, r = 1 / sqrt(var + eps).
+  The first mean is off by e1 = l u A at most.  x - mean' is rounded once, relative to
+  |c| + e1.  The mean of these differences, which is the error e1, is known to l u of
+  their mean absolute value, and taking it off rounds once more:
+     e = u (|c| + e1) + l u (mean|c| + e1) + u (|c| + 2 e1)
+  The mean square of the differences is var + e1^2 to (l + 2) u of itself, and so is its
+  difference with the square of their mean from var; r is off by half of that relative
+  to var + eps:
+     rel = (l + 4) u (var + 2 e1^2) / (var + eps) + 4 u
+  |xh error| <= E = r e + rel |xh|
+From E on the bounds of y, dx, dw and db are those of tests/test_gpu_layernorm.py, with
+mean(t (x - mean)) formed as a sum of t (x - mean') less e1 times the sum of t: 2 l u e1
+mean|t| r more in mean(t xh).
+"""
+import math
+
+import pytest
+import torch
+
+import gated_delta_rule_58_amd as kda
+from tests import linattn_ref as ref
+from tests.gpu_util import DEV, need_gpu, say
+from tests.test_gpu_layernorm import _within
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+U = ref.U
+EPS = 1e-5
+
+
+def _bounds(x, w, b, dy):
+    """Bounds of y, dx, dw, db and xh's reference, as above."""
+    x, dy = x.double(), dy.double()
+    d = x.shape[-1]
+    m = lambda z: z.mean(-1, keepdim=True)  # noqa: E731
+    n = (math.log2(d) + 10) * U
+    c = x - m(x)
+    var = m(c * c)
+    r = 1.0 / torch.sqrt(var + EPS)
+    xh = c * r
+    e1 = n * x.abs().amax(-1, keepdim=True)
+    e = U * (c.abs() + e1) + n * (m(c.abs()) + e1) + U * (c.abs() + 2 * e1)
+    rel = (n + 4 * U) * (var + 2 * e1 * e1) / (var + EPS) + 4 * U
+    E = r * e + rel * xh.abs()
+    aw, ab = w.double().abs(), b.double().abs()
+    y = E * aw + 4 * U * (xh.abs() * aw + ab)
+    t = dy * w.double()
+    L = n + 6 * U
+    mt = L * m((t * xh).abs()) + m(t.abs() * E) + 2 * n * e1 * m(t.abs()) * r
+    dx = r * (4 * U * t.abs() + L * m(t.abs()) + xh.abs() * mt + E * m(t * xh).abs()) + (
+        L + rel) * ref.norm_backward(dy, x, w, EPS)[0].abs()
+    over = tuple(range(x.dim() - w.dim()))
+    rows = (min(x.numel() // d, 4096) + 32) * U
+    dw = (dy.abs() * E).sum(over) + rows * (dy * xh).abs().sum(over)
+    return y, dx, dw, rows * dy.abs().sum(over)
+
+
+def _check(x, w, b, dy):
+    dev = [t.to(DEV) for t in (x, w, b, dy)]
+    y = kda.layernorm(*dev[:3], eps=EPS)
+    dx, dw, db = kda.layernorm_backward(dev[3], dev[0], dev[1], eps=EPS)
+    by, bdx, bdw, bdb = _bounds(x, w, b, dy)
+    want = ref.norm_backward(dy, x, w, EPS)
+    say(_within("y", y, ref.norm(x, w, b, EPS), by, y.dtype),
+        _within("dx", dx, want[0], bdx, dx.dtype), _within("dw", dw, want[1], bdw, F32),
+        _within("db", db, want[2], bdb, F32))
+
+
+@pytest.mark.parametrize("d", [3, 33, 128, 200, 1000, 1500, 5003, 5120, 12288, 16383])
+def test_constant_rows_give_their_bias(d):
+    """A constant row has no spread: xh is 0 to the rounding of its values' differences."""
+    need_gpu()
+    say("layernorm constant rows", d)
+    gen = torch.Generator().manual_seed(d)
+    rnd = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    x = torch.tensor([777.7, 1000.0, 0.1, -53.123, 1e4, 1 / 3]).unsqueeze(1).expand(6, d)
+    _check(x.contiguous(), 1 + 0.3 * rnd(d), rnd(d), rnd(6, d))
+
+
+@pytest.mark.parametrize("d", [100, 777, 4097, 12288])
+@pytest.mark.parametrize("mean", [1e3, 3e4])
+def test_a_spread_far_below_the_mean(d, mean):
+    need_gpu()
+    say("layernorm far means", d, mean)
+    gen = torch.Generator().manual_seed(d)
+    rnd = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    x = (mean + rnd(6, d)).float()
+    _check(x, 1 + 0.3 * rnd(d), rnd(d), rnd(6, d))
