@@ -75,10 +75,10 @@
 // that add up to them).  The decayed c, of which the fp32 state is made, enters as
 // three bf16 values; S and P, of which out is made, as one where out is bf16 (each
 // element is then off by at most 2^-8 of itself, as the rounding of out is), as
-// two where out is fp32, as three where it makes dg (launch_walk).  Accumulators,
-// decays and the state are fp32; gamma is summed in 64 bits and kept as two fp32
-// values, so that a strong decay early in a chunk costs the weak ones behind it no
-// digits.
+// two where out is fp32 or the sequence is one chunk, as three where it makes dg
+// (launch_walk).  Accumulators, decays and the state are fp32; gamma is summed in 64
+// bits and kept as two fp32 values, so that a strong decay early in a chunk costs the
+// weak ones behind it no digits.
 #include <type_traits>
 
 #include "chunk_common.hpp"
@@ -276,7 +276,6 @@ struct alignas(16) Decays {
   float col[2][C];           // e^(gamma_end - gamma_s)
   float tile[2][4];          // e^gamma_i
   float end[2];              // e^gamma_end
-  int seq[2];
 };
 // Waves of a workgroup: state waves 0 .. 3, output waves 4 .. 7, then the helpers.
 template <bool WIDE, bool FULL>
@@ -406,8 +405,39 @@ constexpr int lds_bytes() {
   using L = Lds<WIDE, KD, FULL, DOTS, PL>;
   return (FULL ? L::total : L::off_s) + (int)sizeof(Decays);
 }
+// What a workgroup walks: column tile `tile` of head h of segment seg of sequence n.
+struct Place {
+  int n, bos, len, seg, h, tile;
+};
+// False: nothing (the grid is rounded up).  Every thread of the workgroup calls it.
+//
+// Workgroups go to the XCDs in turn; an XCD gets hb = H / 8 consecutive heads (of 8 hb in
+// the list of all segments' heads) with their tiles.  (Every eighth head instead: the
+// tokens of a head are H rows apart, so for H a multiple of 16 its rows and those of the
+// heads 16 further share one channel of the XCD's L2, and the XCD used two channels of
+// sixteen.)
+template <int KD>
+__device__ __forceinline__ bool locate(const Args& A, const Walk& W, int block, int* s_seq,
+                                       Place& at) {
+  const int ntile = static_cast<int>(W.s_elems / KD) / CT;
+  const int hb = heads_per_xcd(A.H);
+  int id = block >> 3;
+  at.tile = id % ntile;
+  id /= ntile;
+  id = (id / hb * 8 + (block & 7)) * hb + id % hb;
+  at.h = id % A.H;
+  id /= A.H;
+  at.seg = id % A.nseg;
+  int n = id / A.nseg;
+  if (n >= A.N) return false;
+  if (A.cu) n = chunk::lpt_sequence(A.cu, A.N, A.T_tot, n, s_seq);
+  at.n = __builtin_amdgcn_readfirstlane(n);
+  seq_range(A, at.n, at.bos, at.len);
+  return true;
+}
+
 template <bool WIDE, int KD, bool FULL, bool DOTS, int PL>
-__device__ __forceinline__ void walk(const Args& A, const Walk& W, int block, char* lds) {
+__device__ __forceinline__ void walk(const Args& A, const Walk& W, const Place& at, char* lds) {
   using L = Lds<WIDE, KD, FULL, DOTS, PL>;
   using WV = Waves<WIDE, FULL>;
   constexpr int NPL = L::NPL, NBUF = L::NBUF;
@@ -428,27 +458,9 @@ __device__ __forceinline__ void walk(const Args& A, const Walk& W, int block, ch
   const bool rev = W.reverse;
   const bool a_bf = !WIDE || W.a.bf16, b_bf = !WIDE || W.b.bf16, c_bf = !WIDE || W.c.bf16;
 
-  // ---- block -> (sequence, segment, head, tile).  Workgroups go to the XCDs
-  // in turn; an XCD gets hb = H / 8 consecutive heads (of 8 hb in the list of all
-  // segments' heads) with their tiles.  (Every eighth head instead: the tokens of a head are H rows
-  // apart, so for H a multiple of 16 its rows and those of the heads 16 further
-  // share one channel of the XCD's L2, and the XCD used two channels of sixteen.)
+  const int n = at.n, bos = at.bos, len = at.len, seg = at.seg, h = at.h, tile = at.tile;
   const int CD = static_cast<int>(W.s_elems / KD);
   const int ntile = CD / CT;
-  const int hb = heads_per_xcd(A.H);
-  int id = block >> 3;
-  const int tile = id % ntile;
-  id /= ntile;
-  id = (id / hb * 8 + (block & 7)) * hb + id % hb;
-  const int h = id % A.H;
-  id /= A.H;
-  const int seg = id % A.nseg;
-  int n = id / A.nseg;
-  if (n >= A.N) return;
-  if (A.cu) n = chunk::lpt_sequence(A.cu, A.N, A.T_tot, n, D.seq);
-  n = __builtin_amdgcn_readfirstlane(n);
-  int bos, len;
-  seq_range(A, n, bos, len);
   const int nch_all = (len + C - 1) / C;
   int c_lo = 0, c_hi = nch_all;
   if (A.nseg > 1) {
@@ -1093,10 +1105,33 @@ __device__ __forceinline__ void walk(const Args& A, const Walk& W, int block, ch
   }
 }
 
+// S and P as one bf16 value each in the products for out, as two for a sequence of one
+// chunk (kByLength; see launch_walk).
+constexpr int kByLength = 0;
+template <bool WIDE, int KD, bool FULL, bool DOTS, int PL>
+constexpr int lds_of() {
+  if constexpr (PL != kByLength) {
+    return lds_bytes<WIDE, KD, FULL, DOTS, PL>();
+  } else {
+    constexpr int a = lds_bytes<WIDE, KD, FULL, DOTS, 1>(), b = lds_bytes<WIDE, KD, FULL, DOTS, 2>();
+    return a > b ? a : b;
+  }
+}
+template <bool WIDE, int KD, bool FULL, bool DOTS, int PL>
+__device__ __forceinline__ void walk_block(const Args& A, const Walk& W, int block, int* s_seq,
+                                           char* lds) {
+  Place at;
+  if (!locate<KD>(A, W, block, s_seq, at)) return;
+  if constexpr (PL != kByLength) walk<WIDE, KD, FULL, DOTS, PL>(A, W, at, lds);
+  else if (at.len <= C) walk<WIDE, KD, FULL, DOTS, 2>(A, W, at, lds);
+  else walk<WIDE, KD, FULL, DOTS, 1>(A, W, at, lds);
+}
+
 template <bool WIDE, int KD, bool FULL, bool DOTS, int PL>
 __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(Args A) {
-  __shared__ __attribute__((aligned(16))) char lds[lds_bytes<WIDE, KD, FULL, DOTS, PL>()];
-  walk<WIDE, KD, FULL, DOTS, PL>(A, A.walk[A.first + blockIdx.y], blockIdx.x, lds);
+  __shared__ __attribute__((aligned(16))) char lds[lds_of<WIDE, KD, FULL, DOTS, PL>()];
+  __shared__ int s_seq;
+  walk_block<WIDE, KD, FULL, DOTS, PL>(A, A.walk[A.first + blockIdx.y], blockIdx.x, &s_seq, lds);
 }
 
 // The three walks of the backward in one launch, at one workgroup a CU: dq, the
@@ -1105,14 +1140,16 @@ __global__ void __launch_bounds__((Waves<WIDE, FULL>::threads), 1) walk_kernel(A
 template <int DK, int DV, int PLV>
 __global__ void __launch_bounds__((Waves<false, true>::threads), 1)
     gradient_kernel(Args A, int n_qk, int v1) {
-  constexpr int a = lds_bytes<false, DV, true, true, 3>(), b = lds_bytes<false, DK, true, false, PLV>();
+  constexpr int a = lds_of<false, DV, true, true, 3>(), b = lds_of<false, DK, true, false, PLV>();
   __shared__ __attribute__((aligned(16))) char lds[a > b ? a : b];
+  __shared__ int s_seq;
   const int block = blockIdx.x;
   if (block < n_qk || (block >= n_qk + v1 && block < 2 * n_qk + v1)) {
     const int y = block >= n_qk;
-    walk<false, DV, true, true, 3>(A, A.walk[y], block - (y ? n_qk + v1 : 0), lds);
+    walk_block<false, DV, true, true, 3>(A, A.walk[y], block - (y ? n_qk + v1 : 0), &s_seq, lds);
   } else {
-    walk<false, DK, true, false, PLV>(A, A.walk[2], block - (block < n_qk + v1 ? 1 : 2) * n_qk, lds);
+    walk_block<false, DK, true, false, PLV>(A, A.walk[2],
+                                            block - (block < n_qk + v1 ? 1 : 2) * n_qk, &s_seq, lds);
   }
 }
 
@@ -1343,17 +1380,16 @@ hipError_t launch_walk_kd(const Args& A, int walks, hipStream_t s) {
 // `walks` walks of one contraction width kd from A.first on.  S and P enter the products for out as
 //   three values  with dots: dg is a small difference of their sums, and for one
 //                 decay a head a sum of those; with two values it was up to 3e-5 off
-//   two           out is fp32, or bf16 and the call has at most one chunk of tokens,
-//                 which costs nothing there (H = 96: T = 64 7.6 against 7.5 us, T = 256
-//                 14.3 against 13.3, T = 4096 146 against 124) and where the few
-//                 roundings do not average out
+//   two           out is fp32, or bf16 and the sequence has at most one chunk of tokens
+//                 (kByLength), which costs nothing there (H = 96: T = 64 7.6 against 7.5
+//                 us; T = 256 14.3 against 13.3, T = 4096 146 against 124) and where the
+//                 few roundings do not average out.  By the sequence, not by the call: a
+//                 sequence gets the same digits whatever it is packed with
 //   one           out is bf16: off by 2.3e-3 of its norm where bf16's own rounding is
 //                 1.7e-3 off
-bool two_values(const Args& A, bool out_bf16) { return !out_bf16 || A.T_tot <= C; }
 template <bool DOTS>
 hipError_t launch_walk(const Args& A, int walks, bool wide, int kd, bool full, bool out_bf16,
                        hipStream_t s) {
-  const bool two = two_values(A, out_bf16);
 #define KDA_LW(KDV)                                                              \
   do {                                                                           \
     if (wide)                                                                    \
@@ -1361,8 +1397,8 @@ hipError_t launch_walk(const Args& A, int walks, bool wide, int kd, bool full, b
                   : launch_walk_kd<true, KDV, false, false, 3>(A, walks, s);     \
     if (!full) return launch_walk_kd<false, KDV, false, false, 1>(A, walks, s);  \
     if constexpr (DOTS) return hipErrorInvalidValue; /* launch_gradients */      \
-    else if (two) return launch_walk_kd<false, KDV, true, false, 2>(A, walks, s); \
-    else return launch_walk_kd<false, KDV, true, false, 1>(A, walks, s);         \
+    else if (out_bf16) return launch_walk_kd<false, KDV, true, false, kByLength>(A, walks, s); \
+    else return launch_walk_kd<false, KDV, true, false, 2>(A, walks, s);         \
   } while (0)
   if (kd == 128) KDA_LW(128);
   KDA_LW(64);
@@ -1370,7 +1406,7 @@ hipError_t launch_walk(const Args& A, int walks, bool wide, int kd, bool full, b
 }
 
 template <int DK, int DV>
-hipError_t launch_gradients_kd(const Args& A, bool two, hipStream_t s) {
+hipError_t launch_gradients_kd(const Args& A, bool out_bf16, hipStream_t s) {
   const int64_t qk = walk_blocks(A, DV), v = walk_blocks(A, DK), blocks = 2 * qk + v;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   // A workgroup of dq or dk takes about half as long again as one of dv.  Where a
@@ -1381,16 +1417,17 @@ hipError_t launch_gradients_kd(const Args& A, bool two, hipStream_t s) {
   const bool mixed = qk == v && blocks > 2 * kCus && blocks <= 5 * kCus / 2;
   const int v1 = mixed ? (int)(v / 12 * 8) : 0;
   const dim3 grid((unsigned)blocks), block(Waves<false, true>::threads);
-  if (two) gradient_kernel<DK, DV, 2><<<grid, block, 0, s>>>(A, (int)qk, v1);
-  else gradient_kernel<DK, DV, 1><<<grid, block, 0, s>>>(A, (int)qk, v1);
+  if (out_bf16) gradient_kernel<DK, DV, kByLength><<<grid, block, 0, s>>>(A, (int)qk, v1);
+  else gradient_kernel<DK, DV, 2><<<grid, block, 0, s>>>(A, (int)qk, v1);
   return hipGetLastError();
 }
 // all walks of the backward, bf16 operands
 hipError_t launch_gradients(const Args& A, int dk, int dv, bool out_bf16, hipStream_t s) {
-  const bool two = two_values(A, out_bf16);
   if (dk == 128)
-    return dv == 128 ? launch_gradients_kd<128, 128>(A, two, s) : launch_gradients_kd<128, 64>(A, two, s);
-  return dv == 128 ? launch_gradients_kd<64, 128>(A, two, s) : launch_gradients_kd<64, 64>(A, two, s);
+    return dv == 128 ? launch_gradients_kd<128, 128>(A, out_bf16, s)
+                     : launch_gradients_kd<128, 64>(A, out_bf16, s);
+  return dv == 128 ? launch_gradients_kd<64, 128>(A, out_bf16, s)
+                   : launch_gradients_kd<64, 64>(A, out_bf16, s);
 }
 
 hipError_t launch_scan(const Args& A, int walks, int kd, hipStream_t s) {

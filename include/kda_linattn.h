@@ -66,9 +66,11 @@ extern "C" {
  * Accuracy: products run on bf16 MFMA with fp32 accumulation.  bf16 q, k and v
  * enter exactly and the values that make the state as sums of three bf16 values:
  * the state agrees with an fp64 recurrence to about 3e-7 of its norm.  The scores
- * and states that make o enter as one bf16 value where o is bf16 and the call has
- * more than 64 tokens (each off by at most 2^-8 of itself: o is 2.3e-3 of its norm
- * off, where bf16's own rounding makes 1.7e-3), else as two (o fp32: about 3e-6).
+ * and states that make o enter as one bf16 value where o is bf16 and the sequence
+ * has more than 64 tokens (each off by at most 2^-8 of itself: o is 2.3e-3 of its
+ * norm off, where bf16's own rounding makes 1.7e-3), else as two (o fp32: about
+ * 3e-6).  What a sequence is packed with does not change the digits of its o, but
+ * for the last ones of fp32 where a batch is cut into segments.
  * fp32 q, k and v enter as three bf16 values each, and so does everything that
  * they meet (about 3e-7).
  */
