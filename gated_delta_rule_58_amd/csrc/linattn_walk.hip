@@ -251,6 +251,26 @@ __device__ __forceinline__ int64_t seg_slot(const Args& A, int n, int bos) {
   return bos / (C * A.seg_chunks) + n;
 }
 
+// The sequence whose segments begin at or below `slot` (the last such): each step asks
+// for 64 sequences at once, one a lane.
+__device__ __forceinline__ int seq_of_slot(const Args& A, int64_t slot) {
+  int lo = 0, cnt = A.N;  // it is one of lo .. lo + cnt - 1
+  while (cnt > 1) {
+    const int step = (cnt + 63) / 64, off = (int)(threadIdx.x & 63) * step;
+    bool le = false;
+    if (off < cnt) {
+      int bos, len;
+      seq_range(A, lo + off, bos, len);
+      le = seg_slot(A, lo + off, bos) <= slot;
+    }
+    const int k = __popcll(__ballot(le));
+    const int at = k > 0 ? (k - 1) * step : 0;
+    lo += at;
+    cnt = cnt - at < step ? cnt - at : step;
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
 // PS: bf16 values of a state's element (see walk)
 template <bool WIDE, int KD, bool FULL, bool DOTS, int PS>
 struct Lds {
@@ -1227,25 +1247,31 @@ __global__ void __launch_bounds__(NTHR) scan_kernel(Args A) {
 }
 
 // dg of one segment of one (sequence, head): suffix sums of q.dq - k.dk, plus
-// <S, dL/dS> at the segment's end.  In 64 bits (a few thousand terms).  512 lanes:
+// <S, dL/dS> at the segment's end.  In 64 bits (a few thousand terms).  One workgroup
+// per segment slot and head, so that the grid follows the tokens and the sequences and
+// not their product, whatever the host knows of the lengths.  512 lanes:
 // a segment of 2,048 tokens is few trips to memory (the whole backward of T = 4096
 // x 96 with 256 / 512 / 1,024: 436 / 431 / 433 us; of T = 128 x 4, 12.9 / 13.6 / 14.6).
 constexpr int DGT = 512;
 __global__ void __launch_bounds__(DGT) dg_kernel(Args A, const float* dotq, const float* dotk,
                                                   const float* ends_s, const float* ends_d,
                                                   int dk, int dv, bool has_final, float* dg,
-                                                  float* dg_part, int nseg_max) {
+                                                  float* dg_part) {
   __shared__ double s_w[DGT / 64];
   const int h = blockIdx.x % A.H;
-  const int seg = (blockIdx.x / A.H) % nseg_max;
-  const int n = blockIdx.x / A.H / nseg_max;
+  const int64_t slot = blockIdx.x / A.H;
+  const int n = seq_of_slot(A, slot);
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   int bos, len;
   seq_range(A, n, bos, len);
   const int nch = (len + C - 1) / C;
   const int nseg = (nch + A.seg_chunks - 1) / A.seg_chunks;
-  if (seg >= nseg) return;
-  const int64_t slot = seg_slot(A, n, bos) + seg;
+  const int seg = static_cast<int>(slot - seg_slot(A, n, bos));
+  if (seg < 0 || seg >= nseg) {  // no segment's slot
+    if (!A.g.per_token && tid == 0)
+      dg_part[2 * (slot * A.H + h)] = dg_part[2 * (slot * A.H + h) + 1] = 0.f;
+    return;
+  }
   const bool last = seg == nseg - 1;
   // <S, D> over the state, both in the walks' order
   double m = 0.0;
@@ -1317,20 +1343,14 @@ __global__ void __launch_bounds__(DGT) dg_kernel(Args A, const float* dotq, cons
   }
 }
 
-// dg [H] from the segments' sums, in order.  One workgroup per head.
-__global__ void __launch_bounds__(64) dg_heads_kernel(Args A, const float* part, float* dg) {
+// dg [H] from the slots' sums, in order.  One workgroup per head.
+__global__ void __launch_bounds__(64) dg_heads_kernel(Args A, const float* part, int64_t slots,
+                                                      float* dg) {
   const int h = blockIdx.x;
   double sum = 0.0;
-  for (int n = 0; n < A.N; ++n) {
-    int bos, len;
-    seq_range(A, n, bos, len);
-    const int nch = (len + C - 1) / C;
-    const int nseg = (nch + A.seg_chunks - 1) / A.seg_chunks;
-    const int64_t slot0 = seg_slot(A, n, bos);
-    for (int j = threadIdx.x; j < nseg; j += 64) {
-      const int64_t at = 2 * ((slot0 + j) * A.H + h);
-      sum += (double)part[at] + (double)part[at + 1];
-    }
+  for (int64_t j = threadIdx.x; j < slots; j += 64) {
+    const int64_t at = 2 * (j * A.H + h);
+    sum += (double)part[at] + (double)part[at + 1];
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
@@ -1517,7 +1537,12 @@ int64_t longest_chunks(const Problem& p) {
     m = p.cu_host[n + 1] - p.cu_host[n] > m ? p.cu_host[n + 1] - p.cu_host[n] : m;
   return cdiv(m, C);
 }
-// the same to decide by: lengths that are not known are taken as equal
+// segments of seg chunks that a grid over the sequences has to cover
+int segments(const Problem& p, int seg) {
+  const int64_t n = cdiv(longest_chunks(p), seg);
+  return n > 1 ? static_cast<int>(n) : 1;
+}
+// the longest to decide by: lengths that are not known are taken as equal
 int64_t longest_guess(const Problem& p) {
   return p.cu && !p.cu_host ? cdiv(p.T_tot / p.N, C) : longest_chunks(p);
 }
@@ -1561,8 +1586,7 @@ hipError_t launch_prefill(const Problem& p, const Operand& q, const Operand& k, 
   const ForwardWs f(ws, p.T_tot, p.N, p.H, p.dk, p.dv, seg);
   if (seg && ws && ws_bytes >= f.bytes) {
     A.seg_chunks = seg;
-    A.nseg = static_cast<int>(cdiv(longest_chunks(p), seg));
-    if (A.nseg < 1) A.nseg = 1;
+    A.nseg = segments(p, seg);
     W.seg_state = f.state;
     W.seg_decay = f.decay;
   }
@@ -1609,9 +1633,7 @@ hipError_t launch_backward(const Problem& p, const Operand& q, const Operand& k,
   A.eq_len = p.cu ? 0 : static_cast<int>(p.T_tot / p.N);
   A.scale = p.scale;
   A.seg_chunks = seg;
-  const int64_t max_chunks = longest_chunks(p);
-  const int nseg = static_cast<int>(max_chunks ? cdiv(max_chunks, seg) : 1);
-  A.nseg = cut ? nseg : 1;
+  A.nseg = cut ? segments(p, seg) : 1;
 
   Walk wq{}, wk{}, wv{};
   wq.a = d_o; wq.b = v; wq.c = k; wq.x = q;
@@ -1665,14 +1687,13 @@ hipError_t launch_backward(const Problem& p, const Operand& q, const Operand& k,
     }
     if (e != hipSuccess) return e;
   }
-  const int64_t blocks = (int64_t)p.N * nseg * p.H;
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  dg_kernel<<<dim3((unsigned)blocks), DGT, 0, s>>>(A, b.dotq, b.dotk, b.ends_s, b.ends_d, DK, DV,
-                                                    dS != nullptr, dg, b.dg_part, nseg);
+  const int64_t slots = slots_of(p.T_tot, p.N, seg);
+  dg_kernel<<<dim3((unsigned)(slots * p.H)), DGT, 0, s>>>(A, b.dotq, b.dotk, b.ends_s, b.ends_d,
+                                                          DK, DV, dS != nullptr, dg, b.dg_part);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (!A.g.per_token) {
-    dg_heads_kernel<<<dim3(p.H), 64, 0, s>>>(A, b.dg_part, dg);
+    dg_heads_kernel<<<dim3(p.H), 64, 0, s>>>(A, b.dg_part, slots, dg);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -85,3 +85,49 @@ def test_rows_behind_stay_as_they_were_in_given_memory():
     for t, w in zip(outs, want):
         assert torch.all(t[end:] == 7.0)
         assert torch.equal(t[:end], w[:end])
+
+
+def test_gradients_of_many_sequences_without_host_lengths():
+    """65,536 sequences that could each hold all 262,144 tokens as far as the host knows:
+    the same bits as with the host's lengths, and the reference's values."""
+    need_gpu()
+    say("linattn many sequences")
+    N, T = 1 << 16, 1 << 18
+    gen = torch.Generator().manual_seed(33)
+    cu = torch.cat([torch.zeros(1, dtype=torch.long),
+                    torch.randint(0, 9, (N,), generator=gen).cumsum(0)]).clamp(max=T)
+    cu[-1] = T
+    cu = cu.to(torch.int32)
+    rnd = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    q, k, v, do = (rnd(T, 1, 64).to(BF) * 0.3 for _ in range(4))
+    for g in (-0.3 * torch.rand(T, 1, generator=gen), -0.3 * torch.rand(1, generator=gen)):
+        dev = _gpu(q, k, v, g, do, cu)
+        run = lambda **kw: kda.linattn_chunk_prefill_backward(  # noqa: E731
+            *dev[:5], cu_seqlens=dev[5], want_d_initial_state=False, **kw)
+        a, b = run(), run(cu_seqlens_host=cu)
+        for x, y in zip(a[:4], b[:4]):
+            assert torch.equal(x, y)
+        for n0 in (0, 40000, N - 40):  # a few neighbouring sequences
+            c = [int(x) for x in cu[n0:n0 + 41]]
+            lo, hi = c[0], c[-1]
+            got = [x[lo:hi] for x in a[:3]] + [a[3][lo:hi] if g.dim() == 2 else None]
+            ref.check_backward(got, q[lo:hi], k[lo:hi], v[lo:hi],
+                               g[lo:hi] if g.dim() == 2 else g, [x - lo for x in c], do[lo:hi])
+
+
+@pytest.mark.parametrize("lens", [[3000, 0, 0, 100], [5, 0, 2100, 64, 0, 4097], [0, 0, 7], [4500]])
+@pytest.mark.parametrize("decay", ["mild", "head"])
+def test_decay_gradients_with_and_without_host_lengths(lens, decay):
+    """Several segments a sequence, empty sequences between: bit for bit the same dg."""
+    need_gpu()
+    say("linattn host lengths", lens, decay)
+    q, k, v, g, cu, S0 = _draw(lens, 40, 40, 64, 64, BF, decay, 34)
+    gen = torch.Generator().manual_seed(35)
+    do = torch.randn(cu[-1], 40, 64, generator=gen).to(BF)
+    dS = torch.randn(len(lens), 40, 64, 64, generator=gen)
+    dev = _gpu(q, k, v, g, do, S0, dS)
+    h = torch.tensor(cu, dtype=torch.int32)
+    run = lambda **kw: kda.linattn_chunk_prefill_backward(  # noqa: E731
+        *dev[:5], cu_seqlens=h.to(DEV), initial_state=dev[5], d_final_state=dev[6], **kw)
+    for x, y in zip(run(), run(cu_seqlens_host=h)):
+        assert torch.equal(x, y)
