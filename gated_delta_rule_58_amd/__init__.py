@@ -32,6 +32,7 @@ from .linattn import (  # noqa: F401
     linattn_chunk_prefill_backward,
     linattn_chunk_prefill_backward_workspace_bytes,
     linattn_recurrent_decode,
+    zero_rows_behind,
     layernorm,
     layernorm_backward,
     layernorm_backward_workspace_bytes,

@@ -110,7 +110,7 @@ def exported_symbols():
             "kda_gate_backward_workspace_bytes", "kda_linattn_chunk_prefill",
             "kda_linattn_chunk_prefill_workspace_bytes", "kda_linattn_chunk_prefill_backward",
             "kda_linattn_chunk_prefill_backward_workspace_bytes", "kda_linattn_recurrent_decode",
-            "kda_layernorm", "kda_layernorm_backward", "kda_layernorm_backward_workspace_bytes"]
+            "kda_zero_rows_behind", "kda_layernorm", "kda_layernorm_backward", "kda_layernorm_backward_workspace_bytes"]
 
 
 def _check(status: int):

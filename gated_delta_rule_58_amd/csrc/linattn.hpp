@@ -53,6 +53,10 @@ hipError_t launch_backward(const Problem& p, const Operand& q, const Operand& k,
                            void* dv, bool grad_bf16, float* dg, float* dS0, void* ws,
                            hipStream_t s);
 
+constexpr int kMaxCleared = 4;
+hipError_t launch_zero_rows_behind(const int32_t* end, int T_tot, void* const* p,
+                                   const int64_t* row_bytes, int count, hipStream_t s);
+
 }  // namespace linattn
 
 namespace norm {

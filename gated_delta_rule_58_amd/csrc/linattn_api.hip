@@ -322,6 +322,41 @@ kda_status kda_linattn_chunk_prefill_backward(
   });
 }
 
+kda_status kda_zero_rows_behind(const int32_t* cu_seqlens, int32_t N, int64_t T_tot,
+                                void* const* tensors, const int64_t* row_bytes, int32_t count,
+                                void* stream) {
+  const char* fn = "kda_zero_rows_behind";
+  return guarded(fn, [&]() -> kda_status {
+    if (N < 0 || T_tot < 0 || count < 0)
+      return fail(KDA_ERR_INVALID_ARG, "%s: need N, T_tot and count >= 0", fn);
+    if (T_tot > ((int64_t)1 << 31) - 1 || count > kda::linattn::kMaxCleared)
+      return fail(KDA_ERR_UNSUPPORTED, "%s: T_tot must fit in int32, count be at most %d", fn,
+                  kda::linattn::kMaxCleared);
+    if (!cu_seqlens || (count > 0 && (!tensors || !row_bytes)))
+      return fail(KDA_ERR_INVALID_ARG, "%s: cu_seqlens, tensors and row_bytes must be non-NULL", fn);
+    if (!aligned(cu_seqlens, 4))
+      return fail(KDA_ERR_ALIGNMENT, "%s: cu_seqlens must be 4-byte aligned", fn);
+    const Span sc{cu_seqlens, (size_t)(N + (int64_t)1) * 4};
+    for (int32_t i = 0; i < count; ++i) {
+      if (row_bytes[i] < 0 || row_bytes[i] % 4 || row_bytes[i] > ((int64_t)1 << 30))
+        return fail(KDA_ERR_SHAPE, "%s: row_bytes must be a multiple of 4 and at most 2^30", fn);
+      if (!tensors[i] && T_tot * row_bytes[i] > 0)
+        return fail(KDA_ERR_INVALID_ARG, "%s: tensor %d is NULL", fn, i);
+      if (!aligned(tensors[i], 4))
+        return fail(KDA_ERR_ALIGNMENT, "%s: the tensors must be 4-byte aligned", fn);
+      if (overlap(sc, {tensors[i], (size_t)(T_tot * row_bytes[i])}))
+        return fail(KDA_ERR_INVALID_ARG, "%s: tensor %d overlaps cu_seqlens", fn, i);
+    }
+    int64_t bytes = 0;
+    for (int32_t i = 0; i < count; ++i) bytes += T_tot * row_bytes[i];
+    if (bytes == 0) return ok();
+    return kda::api::launched(
+        kda::linattn::launch_zero_rows_behind(cu_seqlens + N, (int)T_tot, tensors, row_bytes, count,
+                                              static_cast<hipStream_t>(stream)),
+        fn);
+  });
+}
+
 kda_status kda_linattn_recurrent_decode(const void* q, int64_t q_stride, const void* k,
                                         int64_t k_stride, const void* v, int64_t v_stride,
                                         kda_dtype qkv_dt, const float* g, int64_t g_len,

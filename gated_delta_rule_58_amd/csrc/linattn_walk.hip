@@ -1382,6 +1382,25 @@ __global__ void __launch_bounds__(NTHR) group_sum_kernel(Args A, const float* hq
   store4(blockIdx.y ? dk : dq, (t * Hk + hk_i) * (int64_t)d + c, s, bf16);
 }
 
+// Zeros from row *end on of up to four tensors of T rows.  blockIdx.y: the tensor.
+struct Cleared {
+  char* p[kMaxCleared];
+  int64_t row_bytes[kMaxCleared];
+};
+__global__ void __launch_bounds__(NTHR) zero_rows_kernel(const int32_t* end, int T, Cleared t) {
+  char* const p = t.p[blockIdx.y];
+  const int64_t row = t.row_bytes[blockIdx.y];
+  const int e = *end;
+  const int64_t from = (e < 0 ? 0 : e > T ? T : e) * row, to = T * row;
+  const int64_t at = (int64_t)blockIdx.x * NTHR + threadIdx.x, step = (int64_t)gridDim.x * NTHR;
+  if (row % 16 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+    for (int64_t i = from + at * 16; i < to; i += step * 16)
+      *reinterpret_cast<u32x4*>(p + i) = u32x4{0, 0, 0, 0};
+  } else {
+    for (int64_t i = from + at * 4; i < to; i += step * 4) *reinterpret_cast<uint32_t*>(p + i) = 0;
+  }
+}
+
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // workgroups of a walk of contraction width kd (see walk)
@@ -1705,6 +1724,22 @@ hipError_t launch_backward(const Problem& p, const Operand& q, const Operand& k,
     e = hipGetLastError();
   }
   return e;
+}
+
+hipError_t launch_zero_rows_behind(const int32_t* end, int T_tot, void* const* p,
+                                   const int64_t* row_bytes, int count, hipStream_t s) {
+  Cleared t{};
+  int64_t most = 0;
+  for (int i = 0; i < count; ++i) {
+    t.p[i] = static_cast<char*>(p[i]);
+    t.row_bytes[i] = row_bytes[i];
+    most = row_bytes[i] > most ? row_bytes[i] : most;
+  }
+  // usually there is little or nothing to clear: no more workgroups than two a CU
+  const int64_t blocks = cdiv(T_tot * most, NTHR * 16);
+  zero_rows_kernel<<<dim3((unsigned)(blocks < 2 * kCus ? blocks : 2 * kCus), count), NTHR, 0, s>>>(
+      end, T_tot, t);
+  return hipGetLastError();
 }
 
 }  // namespace linattn

@@ -24,6 +24,7 @@ _SIGNATURES = {
     "kda_linattn_recurrent_decode": (_int, [
         _vp, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp, _int, _i64, _vp, _vp, _int, _i32,
         _i32, _i32, _i32, _i32, _f32, _vp]),
+    "kda_zero_rows_behind": (_int, [_vp, _i32, _i64, _vp, _vp, _i32, _vp]),
     "kda_layernorm": (_int, [_vp, _int, _vp, _vp, _i64, _vp, _int, _i64, _i32, _f32, _vp]),
     "kda_layernorm_backward": (_int, [_vp, _int, _vp, _int, _vp, _i64, _vp, _vp, _vp, _i64, _i32,
                                       _f32, _vp, _size, _vp]),
@@ -108,14 +109,27 @@ def _sequences(rows, cu_seqlens, cu_seqlens_host, num_seqs):
     return N, cu_seqlens_host.contiguous()
 
 
-def _new_rows(cu_seqlens, cu_seqlens_host):
-    """The allocator of outputs that the library writes the rows of sequences of.  Without the
-    host's lengths the last sequence may end before the last row; those rows are zeros."""
-    return torch.zeros if cu_seqlens is not None and cu_seqlens_host is None else torch.empty
-
-
 def _host_ptr(t):
     return None if t is None else ctypes.cast(t.data_ptr(), _vp)
+
+
+def zero_rows_behind(cu_seqlens: torch.Tensor, *tensors: torch.Tensor):
+    """kda_zero_rows_behind: zeros the rows of up to four [T, ...] tensors that lie behind the
+    last sequence (from cu_seqlens[N] on), without waiting for cu_seqlens on the host."""
+    _dtype("cu_seqlens", cu_seqlens, torch.int32)
+    if not tensors:
+        return
+    dev, T, n = cu_seqlens.device, tensors[0].shape[0], len(tensors)
+    for t in tensors:
+        _same_device(dev, tensor=t)
+        if t.dim() < 1 or t.shape[0] != T:
+            raise ValueError("the tensors must have the same number of rows")
+    ptrs = (_vp * n)(*[_ptr(t) for t in tensors])
+    sizes = (_i64 * n)(*[t.numel() // max(T, 1) * t.element_size() for t in tensors])
+    with _on(dev):
+        st = _fn("kda_zero_rows_behind")(_ptr(cu_seqlens), cu_seqlens.numel() - 1, T, ptrs, sizes,
+                                         n, _stream(dev))
+    _check(st)
 
 
 def linattn_chunk_prefill_workspace_bytes(T_tot: int, N: int, H: int, dk: int = 128,
@@ -159,9 +173,9 @@ def linattn_chunk_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
         _dtype("state_indices", state_indices, torch.int32)
         _shape("state_indices", state_indices, N)
         output_final_state = False  # a pool is written only when passed as final_state
-    if out is None:
-        out = _new_rows(cu_seqlens, cu_seqlens_host)((T, H, dv), dtype=o_dtype or q.dtype,
-                                                     device=dev)
+    new_out = out is None
+    if new_out:
+        out = torch.empty((T, H, dv), dtype=o_dtype or q.dtype, device=dev)
     _shape("out", out, T, H, dv)
     if final_state is None and output_final_state:
         final_state = torch.empty((N, H, dk, dv), dtype=state_dtype, device=dev)
@@ -184,6 +198,8 @@ def linattn_chunk_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
             workspace.numel() * workspace.element_size() if workspace is not None else 0,
             _stream(dev))
     _check(st)
+    if new_out and cu_seqlens is not None and hp is None:
+        zero_rows_behind(cu_seqlens, out)
     return out, final_state
 
 
@@ -219,11 +235,10 @@ def linattn_chunk_prefill_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Te
         _dtype(name, t, torch.float32)
         _shape(name, t, N, H, dk, dv)
     gdt = grad_dtype or q.dtype
-    rows = _new_rows(cu_seqlens, cu_seqlens_host)
-    dq = rows((T, Hk, dk), dtype=gdt, device=dev)
-    dk_ = rows((T, Hk, dk), dtype=gdt, device=dev)
-    dv_ = rows((T, H, dv), dtype=gdt, device=dev)
-    dg = rows(tuple(g.shape), dtype=torch.float32, device=dev)
+    dq = torch.empty((T, Hk, dk), dtype=gdt, device=dev)
+    dk_ = torch.empty((T, Hk, dk), dtype=gdt, device=dev)
+    dv_ = torch.empty((T, H, dv), dtype=gdt, device=dev)
+    dg = torch.empty(tuple(g.shape), dtype=torch.float32, device=dev)
     dS0 = (torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
            if want_d_initial_state else None)
     if workspace is None:
@@ -238,6 +253,8 @@ def linattn_chunk_prefill_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Te
             H, Hk, dk, dv, float(scale), _ptr(workspace),
             workspace.numel() * workspace.element_size(), _stream(dev))
     _check(st)
+    if cu_seqlens is not None and hp is None:
+        zero_rows_behind(cu_seqlens, dq, dk_, dv_, *([dg] if g.dim() == 2 else []))
     return dq, dk_, dv_, dg, dS0
 
 

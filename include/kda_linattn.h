@@ -123,6 +123,19 @@ size_t kda_linattn_chunk_prefill_backward_workspace_bytes(int64_t T_tot, int32_t
                                                           int32_t Hk, int32_t dk, int32_t dv);
 
 /*
+ * kda_zero_rows_behind - zeros the rows behind the last sequence.
+ *
+ * The calls above leave those rows of o and of the gradients as they were; where the
+ * host does not know cu_seqlens[N], this clears them.  For each of `count` (0 to 4)
+ * tensors of T_tot rows, row i has row_bytes[i] bytes (a multiple of 4, pointers 4-byte
+ * aligned): bytes [cu_seqlens[N] * row_bytes[i], T_tot * row_bytes[i]) become 0
+ * (cu_seqlens[N] clamped into [0, T_tot]).  `tensors` and `row_bytes` are host arrays.
+ */
+kda_status kda_zero_rows_behind(const int32_t* cu_seqlens, int32_t N, int64_t T_tot,
+                                void* const* tensors, const int64_t* row_bytes, int32_t count,
+                                void* stream);
+
+/*
  * kda_linattn_recurrent_decode - one token per sequence over a pool of states.
  *
  *   q, k  [N, Hk, dk], v [N, H, dv] dtype qkv_dt, strides between sequences

@@ -131,3 +131,49 @@ def test_decay_gradients_with_and_without_host_lengths(lens, decay):
         *dev[:5], cu_seqlens=h.to(DEV), initial_state=dev[5], d_final_state=dev[6], **kw)
     for x, y in zip(run(), run(cu_seqlens_host=h)):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("end", [-3, 0, 1, 77, 499, 500, 700])
+def test_zero_rows_behind(end):
+    """Rows from cu_seqlens[N] on, of every row size and alignment, and nothing else."""
+    need_gpu()
+    say("zero rows behind", end)
+    T = 500
+    cu = torch.tensor([0, 7, end], dtype=torch.int32, device=DEV)
+    odd = torch.full((T * 6 + 2,), 7.0, dtype=BF, device=DEV)
+    ts = [torch.full((T, 3, 128), 7.0, dtype=BF, device=DEV), torch.full((T, 5), 7.0, device=DEV),
+          odd[2:].view(T, 6), torch.full((T, 4000), 7.0, device=DEV)]
+    kda.zero_rows_behind(cu, *ts)
+    cut = min(max(end, 0), T)
+    for t in ts:
+        assert torch.all(t[:cut] == 7.0) and torch.all(t[cut:] == 0.0)
+    assert torch.all(odd[:2] == 7.0)
+    kda.zero_rows_behind(cu, torch.empty(0, 4, device=DEV))
+
+
+def test_rows_behind_in_a_replayed_graph():
+    """Lengths that change between replays: each replay clears what lies behind its own."""
+    need_gpu()
+    say("linattn rows behind, graph")
+    q, k, v, g, cu, S0 = _draw([100, 60], 2, 2, 128, 128, BF, "mild", 36)
+    dev = _gpu(q, k, v, g, torch.ones(160, 2, 128, dtype=BF))
+    cu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+
+    def run():
+        return (kda.linattn_chunk_prefill(*dev[:4], cu_seqlens=cu)[0],
+                ) + kda.linattn_chunk_prefill_backward(*dev, cu_seqlens=cu)[:4]
+
+    run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = run()
+    for end in (160, 120, 150, 101):
+        cu[2] = end
+        want = run()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(out, want):
+            assert torch.equal(x, y) and not x[end:].any()
