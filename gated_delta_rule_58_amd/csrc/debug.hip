@@ -78,20 +78,23 @@ __global__ void scan_rows_kernel(const void* __restrict__ p, int64_t rows, int64
   if (bad) atomicAdd(word, bad);
 }
 
-// One workgroup per (sequence, head): the state (elems values) of slot idx[n]
+// One workgroup per (sequence, head) in turn: the state (elems values) of slot idx[n]
 // (n without indices); slots outside [0, slots) are skipped.
 template <bool BF16>
 __global__ void scan_states_kernel(const void* __restrict__ p, const int32_t* __restrict__ idx,
-                                   int64_t slots, int H, int elems, uint32_t* word) {
-  const int n = blockIdx.x / H, h = blockIdx.x % H;
-  const int64_t s = idx ? static_cast<int64_t>(idx[n]) : n;
-  if (s < 0 || s >= slots) return;
-  const int64_t base = (s * H + h) * elems;
+                                   int64_t slots, int64_t pairs, int H, int elems,
+                                   uint32_t* word) {
   uint32_t bad = 0;
-  for (int i = threadIdx.x; i < elems; i += blockDim.x) {
-    const float x = BF16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(p)[base + i])
-                         : static_cast<const float*>(p)[base + i];
-    bad += __builtin_isfinite(x) ? 0u : 1u;
+  for (int64_t pair = blockIdx.x; pair < pairs; pair += gridDim.x) {
+    const int64_t n = pair / H, h = pair % H;
+    const int64_t s = idx ? static_cast<int64_t>(idx[n]) : n;
+    if (s < 0 || s >= slots) continue;
+    const int64_t base = (s * H + h) * elems;
+    for (int i = threadIdx.x; i < elems; i += blockDim.x) {
+      const float x = BF16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(p)[base + i])
+                           : static_cast<const float*>(p)[base + i];
+      bad += __builtin_isfinite(x) ? 0u : 1u;
+    }
   }
   if (bad) atomicAdd(word, bad);
 }
@@ -166,9 +169,12 @@ void Session::add_rows(const char* what, const void* p, int64_t rows, int64_t co
 void Session::add_states(const char* what, const void* p, bool bf16, const int32_t* idx,
                          int64_t slots, int N, int H, int elems) {
   if (!p || N <= 0 || H <= 0 || count_ >= kMaxScans) return;
-  const unsigned blocks = (unsigned)((int64_t)N * H);
-  if (bf16) scan_states_kernel<true><<<blocks, 256, 0, stream_>>>(p, idx, slots, H, elems, words_ + count_);
-  else scan_states_kernel<false><<<blocks, 256, 0, stream_>>>(p, idx, slots, H, elems, words_ + count_);
+  const int64_t pairs = (int64_t)N * H;
+  const unsigned blocks = (unsigned)(pairs < 65536 ? pairs : 65536);
+  if (bf16)
+    scan_states_kernel<true><<<blocks, 256, 0, stream_>>>(p, idx, slots, pairs, H, elems, words_ + count_);
+  else
+    scan_states_kernel<false><<<blocks, 256, 0, stream_>>>(p, idx, slots, pairs, H, elems, words_ + count_);
   what_[count_] = what;
   rule_[count_] = kFinite;
   n_[count_] = (int64_t)N * H * elems;

@@ -28,6 +28,9 @@ __device__ __forceinline__ float clamp_log_decay(float g) {
   return g < kMinLogDecay ? kMinLogDecay : g;  // NaN stays NaN
 }
 
+// (sequence, head) pairs of a decode: 512 threads each in a launch of fewer than 2^32, in
+// eights
+constexpr int64_t kMaxDecodePairs = (int64_t(1) << 23) - 8;
 hipError_t launch_decode(const Operand& q, const Operand& k, const Operand& v, const Decay& g,
                          void* pool, bool state_bf16, int64_t num_slots, const int32_t* slots,
                          void* o, bool o_bf16, int N, int H, int dk, int dv, float scale,
@@ -42,6 +45,9 @@ struct Problem {
   int H, Hk, dk, dv;
   float scale;
 };
+// Whether every launch of a call holds its work items (wide: an fp32 operand).
+bool prefill_fits(const Problem& p, bool wide);
+bool backward_fits(const Problem& p, bool wide);
 size_t prefill_workspace_bytes(int64_t T_tot, int N, int H, int dk, int dv);
 // ws may be null or short: sequences are then walked whole.
 hipError_t launch_prefill(const Problem& p, const Operand& q, const Operand& k, const Operand& v,

@@ -87,6 +87,8 @@ kda_status check_inputs(const char* fn, const Inputs& a) {
   if ((a.dk != 64 && a.dk != 128) || (a.dv != 64 && a.dv != 128))
     return fail(KDA_ERR_UNSUPPORTED, "%s: dk and dv must be 64 or 128 (got %d, %d)", fn, a.dk, a.dv);
   if (a.H > kMaxHeads) return fail(KDA_ERR_UNSUPPORTED, "%s: need H <= 16384", fn);
+  if (a.rows > ((int64_t)1 << 31) - 1)
+    return fail(KDA_ERR_UNSUPPORTED, "%s: T_tot must fit in int32", fn);
   if (!finite_scale(a.scale)) return fail(KDA_ERR_INVALID_ARG, "%s: scale must be finite", fn);
   if (a.g_len != a.H && a.g_len != a.rows * a.H)
     return fail(KDA_ERR_SHAPE, "%s: g has %lld values; it must be one per head (%d) or one per "
@@ -113,8 +115,6 @@ kda_status check_inputs(const char* fn, const Inputs& a) {
 kda_status check_batch(const char* fn, int64_t T_tot, int32_t N, int32_t H, const int32_t* cu,
                        const int32_t* cu_host) {
   if (N <= 0) return fail(KDA_ERR_INVALID_ARG, "%s: need N > 0 (got %d)", fn, N);
-  if (T_tot > ((int64_t)1 << 31) - 1)
-    return fail(KDA_ERR_UNSUPPORTED, "%s: T_tot must fit in int32", fn);
   if ((int64_t)N * H > ((int64_t)1 << 24))
     return fail(KDA_ERR_UNSUPPORTED, "%s: need N*H <= 2^24", fn);
   if (!aligned(cu, 4)) return fail(KDA_ERR_ALIGNMENT, "%s: cu_seqlens must be 4-byte aligned", fn);
@@ -134,6 +134,11 @@ kda_status check_batch(const char* fn, int64_t T_tot, int32_t N, int32_t H, cons
         return fail(KDA_ERR_SHAPE, "%s: cu_seqlens decreases at index %d", fn, n);
   }
   return KDA_OK;
+}
+
+kda_status too_large(const char* fn, int32_t N, int32_t H) {
+  return fail(KDA_ERR_UNSUPPORTED, "%s: N = %d sequences of H = %d heads are more than a launch "
+                                   "holds", fn, N, H);
 }
 
 // `out` must not touch any of the others.
@@ -172,6 +177,9 @@ kda_status kda_linattn_chunk_prefill(const void* q, int64_t q_stride, const void
                     scale};
     if (const kda_status st = check_inputs(fn, in)) return st;
     if (const kda_status st = check_batch(fn, T_tot, N, H, cu_seqlens, cu_seqlens_host)) return st;
+    const kda::linattn::Problem p{{g, in.per_token()}, cu_seqlens, cu_seqlens_host, N, T_tot, H,
+                                  Hk, dk, dv, scale};
+    if (!kda::linattn::prefill_fits(p, qkv_dt == KDA_F32)) return too_large(fn, N, H);
     if (!known_dtype(o_dt) || !known_dtype(state_dt))
       return fail(KDA_ERR_DTYPE, "%s: o_dt and state_dt must be KDA_F32 or KDA_BF16", fn);
     if (num_slots < 0)
@@ -209,8 +217,6 @@ kda_status kda_linattn_chunk_prefill(const void* q, int64_t q_stride, const void
     pool.idx = state_indices;
     pool.slots = state_indices ? num_slots : (num_slots < N ? num_slots : N);
     pool.bf16 = state_dt == KDA_BF16;
-    const kda::linattn::Problem p{{g, in.per_token()}, cu_seqlens, cu_seqlens_host, N, T_tot, H,
-                                  Hk, dk, dv, scale};
     const hipStream_t s = static_cast<hipStream_t>(stream);
     return run_checked(
         fn, s,
@@ -256,6 +262,10 @@ kda_status kda_linattn_chunk_prefill_backward(
     if (const kda_status st = check_batch(fn, T_tot, N, H, cu_seqlens, cu_seqlens_host)) return st;
     if (!known_dtype(do_dt) || !known_dtype(grad_dt))
       return fail(KDA_ERR_DTYPE, "%s: do_dt and grad_dt must be KDA_F32 or KDA_BF16", fn);
+    const kda::linattn::Problem p{{g, in.per_token()}, cu_seqlens, cu_seqlens_host, N, T_tot, H,
+                                  Hk, dk_dim, dv_dim, scale};
+    if (!kda::linattn::backward_fits(p, qkv_dt == KDA_F32 || (d_o && do_dt == KDA_F32)))
+      return too_large(fn, N, H);
     if (T_tot > 0 && (!dq || !dk || !dv))
       return fail(KDA_ERR_INVALID_ARG, "%s: dq, dk and dv must be non-NULL", fn);
     if (g_len > 0 && !dg) return fail(KDA_ERR_INVALID_ARG, "%s: dg must be non-NULL", fn);
@@ -290,8 +300,6 @@ kda_status kda_linattn_chunk_prefill_backward(
           return fail(KDA_ERR_INVALID_ARG, "%s: two outputs, or an output and the workspace, overlap",
                       fn);
     }
-    const kda::linattn::Problem p{{g, in.per_token()}, cu_seqlens, cu_seqlens_host, N, T_tot, H,
-                                  Hk, dk_dim, dv_dim, scale};
     const kda::linattn::Operand od{d_o, (int64_t)H * dv_dim, 1, do_dt == KDA_BF16};
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const bool all_rows = !cu_seqlens || cu_seqlens_host;
@@ -384,8 +392,9 @@ kda_status kda_linattn_recurrent_decode(const void* q, int64_t q_stride, const v
       return fail(KDA_ERR_ALIGNMENT, "%s: state and o must be 16-byte aligned", fn);
     if (!aligned(state_indices, 4))
       return fail(KDA_ERR_ALIGNMENT, "%s: state_indices must be 4-byte aligned", fn);
-    if ((int64_t)N * H > ((int64_t)1 << 28))
-      return fail(KDA_ERR_UNSUPPORTED, "%s: need N*H <= 2^28", fn);
+    if ((int64_t)N * H > kda::linattn::kMaxDecodePairs)
+      return fail(KDA_ERR_UNSUPPORTED, "%s: need N*H <= %lld", fn,
+                  (long long)kda::linattn::kMaxDecodePairs);
     const Span sp{state, (size_t)num_slots * H * dk * dv * size_of(state_dt)},
         so{o, (size_t)N * H * dv * size_of(o_dt)},
         sx{state_indices, state_indices ? (size_t)N * 4 : 0}, sg{g, (size_t)g_len * 4};

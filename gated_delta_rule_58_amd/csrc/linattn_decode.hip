@@ -136,7 +136,6 @@ hipError_t launch(const Operand& q, const Operand& k, const Operand& v, const De
   // 3.8 / 3.5, 96 4.0 / 4.1, 384 5.5 / 6.7.
   const bool tiled = pairs < (S_BF16 ? 96 : 512);
   const int64_t blocks = pairs * (tiled ? DV / 32 : 1);
-  if (blocks > 0x7ffffff8) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>((blocks + 7) / 8 * 8));
   if (tiled)
     decode_kernel<S_BF16, DK, DV, 32, 256><<<grid, 256, 0, s>>>(q, k, v, g, pool, slots, num_slots,

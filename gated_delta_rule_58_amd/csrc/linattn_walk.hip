@@ -1408,10 +1408,18 @@ int64_t walk_blocks(const Args& A, int kd) {
   const int hb = heads_per_xcd(A.H);
   return cdiv((int64_t)A.N * A.nseg * A.H, 8 * hb) * 8 * hb * (A.walk[0].s_elems / kd / CT);
 }
+// workgroups of scan_kernel and group_sum_kernel
+int64_t scan_blocks(const Args& A, int kd) {
+  return (int64_t)A.N * A.H * (A.walk[0].s_elems / kd / CT) * (kd / 16);
+}
+int64_t group_sum_blocks(const Problem& p) { return cdiv(p.T_tot * p.Hk * (p.dk / 4), NTHR); }
+
+// A launch holds fewer than 2^32 work items an axis.
+bool fits(int64_t blocks, int threads) { return blocks * threads < (int64_t(1) << 32); }
+
 template <bool WIDE, int KD, bool FULL, bool DOTS, int PL>
 hipError_t launch_walk_kd(const Args& A, int walks, hipStream_t s) {
   const int64_t blocks = walk_blocks(A, KD);
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   walk_kernel<WIDE, KD, FULL, DOTS, PL><<<dim3((unsigned)blocks, walks),
                                           Waves<WIDE, FULL>::threads, 0, s>>>(A);
   return hipGetLastError();
@@ -1447,7 +1455,6 @@ hipError_t launch_walk(const Args& A, int walks, bool wide, int kd, bool full, b
 template <int DK, int DV>
 hipError_t launch_gradients_kd(const Args& A, bool out_bf16, hipStream_t s) {
   const int64_t qk = walk_blocks(A, DV), v = walk_blocks(A, DK), blocks = 2 * qk + v;
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   // A workgroup of dq or dk takes about half as long again as one of dv.  Where a
   // third round of workgroups would leave more than half of the CUs idle, two
   // thirds of dv's go before dk's: the CUs then get two of the long ones or three of
@@ -1470,9 +1477,7 @@ hipError_t launch_gradients(const Args& A, int dk, int dv, bool out_bf16, hipStr
 }
 
 hipError_t launch_scan(const Args& A, int walks, int kd, hipStream_t s) {
-  const int64_t blocks = (int64_t)A.N * A.H * (A.walk[0].s_elems / kd / CT) * (kd / 16);
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)blocks, walks);
+  const dim3 grid((unsigned)scan_blocks(A, kd), walks);
   if (kd == 128) scan_kernel<128><<<grid, NTHR, 0, s>>>(A);
   else scan_kernel<64><<<grid, NTHR, 0, s>>>(A);
   return hipGetLastError();
@@ -1573,6 +1578,17 @@ size_t prefill_workspace_bytes(int64_t T_tot, int N, int H, int dk, int dv) {
   return seg ? ForwardWs(nullptr, T_tot, N, H, dk, dv, seg).bytes : 0;
 }
 
+bool prefill_fits(const Problem& p, bool wide) {
+  const int seg = cut_chunks(p.T_tot, p.N, (int64_t)p.H * (p.dv / CT), longest_guess(p), 1);
+  Args A{};
+  A.N = p.N;
+  A.H = p.H;
+  A.nseg = seg ? segments(p, seg) : 1;
+  A.walk[0].s_elems = (int64_t)p.dk * p.dv;
+  return fits(walk_blocks(A, p.dk), wide ? Waves<true, true>::threads : Waves<false, true>::threads) &&
+         (A.nseg == 1 || fits(scan_blocks(A, p.dk), NTHR));
+}
+
 hipError_t launch_prefill(const Problem& p, const Operand& q, const Operand& k, const Operand& v,
                           const StatePool& st, void* o, bool o_bf16, void* ws, size_t ws_bytes,
                           hipStream_t s) {
@@ -1633,6 +1649,22 @@ size_t backward_workspace_bytes(int64_t T_tot, int N, int H, int Hk, int dk, int
   const size_t a = BackwardWs(nullptr, T_tot, N, H, Hk, dk, dv, seg, cut).bytes;
   const size_t b = BackwardWs(nullptr, T_tot, N, H, Hk, dk, dv, kBorderChunks, false).bytes;
   return a > b ? a : b;
+}
+
+bool backward_fits(const Problem& p, bool wide) {
+  bool cut;
+  const int seg = border_chunks(p.T_tot, p.N, p.H, p.dk, p.dv, longest_guess(p), &cut);
+  Args A{};
+  A.N = p.N;
+  A.H = p.H;
+  A.nseg = cut ? segments(p, seg) : 1;
+  A.walk[0].s_elems = (int64_t)p.dk * p.dv;
+  const int64_t qk = walk_blocks(A, p.dv), v = walk_blocks(A, p.dk);
+  return (wide ? fits(qk > v ? qk : v, Waves<true, true>::threads)
+               : fits(2 * qk + v, Waves<false, true>::threads)) &&
+         (A.nseg == 1 || (fits(scan_blocks(A, p.dv), NTHR) && fits(scan_blocks(A, p.dk), NTHR))) &&
+         fits(slots_of(p.T_tot, p.N, seg) * p.H, DGT) &&
+         (p.Hk == p.H || fits(group_sum_blocks(p), NTHR));
 }
 
 hipError_t launch_backward(const Problem& p, const Operand& q, const Operand& k, const Operand& v,
@@ -1717,9 +1749,7 @@ hipError_t launch_backward(const Problem& p, const Operand& q, const Operand& k,
     if (e != hipSuccess) return e;
   }
   if (group > 1 && p.T_tot > 0) {
-    const int64_t n = cdiv(p.T_tot * p.Hk * (DK / 4), NTHR);
-    if (n > 0x7fffffff) return hipErrorInvalidValue;
-    group_sum_kernel<<<dim3((unsigned)n, 2), NTHR, 0, s>>>(A, b.hq, b.hk, DK, group, dq, dk,
+    group_sum_kernel<<<dim3((unsigned)group_sum_blocks(p), 2), NTHR, 0, s>>>(A, b.hq, b.hk, DK, group, dq, dk,
                                                          grad_bf16);
     e = hipGetLastError();
   }

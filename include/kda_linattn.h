@@ -28,6 +28,11 @@
  * before it too.  A NaN in g is carried on.  (Rows of q, k, v and g that belong
  * to no sequence may hold anything.)
  *
+ * Sizes: T_tot < 2^31, H <= 16384, N*H <= 2^24; and the work items of a launch (fewer
+ * than 2^32) have to hold the call, which ends at about 3 million (sequence, head) pairs
+ * in the prefill, 1 million in its gradients (dk = dv = 128) and 8.3 million in the
+ * decode.  Calls beyond that are refused (KDA_ERR_UNSUPPORTED).
+ *
  * Strides: q, k and v give the distance between tokens (sequences, in the
  * decode) in elements: at least heads * dim, so that they may be slices of a
  * fused projection; heads and channels are dense.  Rows are 16-byte aligned.
