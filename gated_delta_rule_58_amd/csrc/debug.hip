@@ -63,14 +63,20 @@ __global__ void scan_kernel(const void* __restrict__ p, int64_t n, int rule, uin
   if (bad) atomicAdd(word, bad);
 }
 
-// Rows of `cols` values, `stride` values apart.
+// Rows of `cols` values, `stride` values apart, of those that `which` takes.
 template <bool BF16>
 __global__ void scan_rows_kernel(const void* __restrict__ p, int64_t rows, int64_t cols,
-                                 int64_t stride, int rule, uint32_t* word) {
+                                 int64_t stride, int rule, Rows which, uint32_t* word) {
   uint32_t bad = 0;
+  if (which.end) {
+    const int64_t e = *which.end;
+    rows = e < 0 ? 0 : e < rows ? e : rows;
+  }
   const int64_t step = (int64_t)gridDim.x * blockDim.x;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < rows * cols; i += step) {
-    const int64_t at = (i / cols) * stride + i % cols;
+    const int64_t row = i / cols;
+    if (which.idx && (which.idx[row] < 0 || which.idx[row] >= which.slots)) continue;
+    const int64_t at = row * stride + i % cols;
     const float x = BF16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(p)[at])
                          : static_cast<const float*>(p)[at];
     bad += value_ok(x, rule) ? 0u : 1u;
@@ -152,14 +158,16 @@ void Session::add(const char* what, const void* p, int64_t n, bool bf16, int rul
 }
 
 void Session::add_rows(const char* what, const void* p, int64_t rows, int64_t cols,
-                       int64_t stride, bool bf16, int rule) {
+                       int64_t stride, bool bf16, int rule, Rows which) {
   if (!p || rows <= 0 || cols <= 0 || count_ >= kMaxScans) return;
   const int64_t blocks64 = (rows * cols + 255) / 256;
   const unsigned blocks = (unsigned)(blocks64 < 2048 ? blocks64 : 2048);
   if (bf16)
-    scan_rows_kernel<true><<<blocks, 256, 0, stream_>>>(p, rows, cols, stride, rule, words_ + count_);
+    scan_rows_kernel<true><<<blocks, 256, 0, stream_>>>(p, rows, cols, stride, rule, which,
+                                                        words_ + count_);
   else
-    scan_rows_kernel<false><<<blocks, 256, 0, stream_>>>(p, rows, cols, stride, rule, words_ + count_);
+    scan_rows_kernel<false><<<blocks, 256, 0, stream_>>>(p, rows, cols, stride, rule, which,
+                                                         words_ + count_);
   what_[count_] = what;
   rule_[count_] = rule;
   n_[count_] = rows * cols;

@@ -17,15 +17,23 @@ namespace dbg {
 enum Rule { kFinite = 0, kNotNaN = 1, kNonPositive = 2, kUnit = 3 };
 bool enabled();          // KDA_DEBUG is "1" (read on every call)
 std::mutex& mutex();     // held for a whole debug call
+// Rows of a packed tensor that belong to a sequence (the others may hold anything):
+// those before *end (null: all), and row n only if slot idx[n] is inside [0, slots)
+// (null: every row).  Device pointers.
+struct Rows {
+  const int32_t* end = nullptr;
+  const int32_t* idx = nullptr;
+  int64_t slots = 0;
+};
 class Session {
  public:
   explicit Session(hipStream_t s);
   hipError_t begin();    // clears the counters (a kernel on the stream)
   // count the values of p[0 .. n) (fp32 or bf16) that break `rule`
   void add(const char* what, const void* p, int64_t n, bool bf16, int rule);
-  // the same over rows of `cols` values, `stride` values apart
+  // the same over rows of `cols` values, `stride` values apart: those that `which` takes
   void add_rows(const char* what, const void* p, int64_t rows, int64_t cols, int64_t stride,
-                bool bf16, int rule);
+                bool bf16, int rule, Rows which = {});
   // count non-finite values of the states (elems values each) of slot idx[n] (n when
   // idx is null) for every (sequence n < N, head), skipping slots outside [0, slots)
   void add_states(const char* what, const void* p, bool bf16, const int32_t* idx, int64_t slots,

@@ -69,14 +69,20 @@ struct Inputs {
   kda::linattn::Operand op_q() const { return {q, qs, H / Hk, dt == KDA_BF16}; }
   kda::linattn::Operand op_k() const { return {k, ks, H / Hk, dt == KDA_BF16}; }
   kda::linattn::Operand op_v() const { return {v, vs, 1, dt == KDA_BF16}; }
-  void scan(kda::dbg::Session& c) const {
+  void scan(kda::dbg::Session& c, const kda::dbg::Rows& which) const {
     const bool b = dt == KDA_BF16;
-    c.add_rows("q", q, rows, (int64_t)Hk * dk, qs, b, kFinite);
-    c.add_rows("k", k, rows, (int64_t)Hk * dk, ks, b, kFinite);
-    c.add_rows("v", v, rows, (int64_t)H * dv, vs, b, kFinite);
-    c.add("g", g, g_len, false, kNonPositive);
+    c.add_rows("q", q, rows, (int64_t)Hk * dk, qs, b, kFinite, which);
+    c.add_rows("k", k, rows, (int64_t)Hk * dk, ks, b, kFinite, which);
+    c.add_rows("v", v, rows, (int64_t)H * dv, vs, b, kFinite, which);
+    if (per_token()) c.add_rows("g", g, rows, H, H, false, kNonPositive, which);
+    else c.add("g", g, g_len, false, kNonPositive);
   }
 };
+
+// The rows of a packed batch that belong to a sequence.
+kda::dbg::Rows of_sequences(const int32_t* cu, int32_t N) {
+  return {cu ? cu + N : nullptr, nullptr, 0};
+}
 
 kda_status check_inputs(const char* fn, const Inputs& a) {
   if (a.H <= 0 || a.Hk <= 0 || a.rows < 0)
@@ -221,7 +227,7 @@ kda_status kda_linattn_chunk_prefill(const void* q, int64_t q_stride, const void
     return run_checked(
         fn, s,
         [&](kda::dbg::Session& c) {
-          in.scan(c);
+          in.scan(c, of_sequences(cu_seqlens, N));
           c.add_states("initial_state", initial_state, pool.bf16, state_indices, pool.slots, N, H,
                        dk * dv);
         },
@@ -230,9 +236,8 @@ kda_status kda_linattn_chunk_prefill(const void* q, int64_t q_stride, const void
                                               o_dt == KDA_BF16, workspace, workspace_bytes, s);
         },
         [&](kda::dbg::Session& c) {
-          // without the host copy the rows behind the last sequence are unknown
-          if (!cu_seqlens || cu_seqlens_host)
-            c.add("o", o, T_tot * H * dv, o_dt == KDA_BF16, kFinite);
+          c.add_rows("o", o, T_tot, (int64_t)H * dv, (int64_t)H * dv, o_dt == KDA_BF16, kFinite,
+                     of_sequences(cu_seqlens, N));
           c.add_states("final_state", final_state, pool.bf16, state_indices, pool.slots, N, H,
                        dk * dv);
         });
@@ -302,12 +307,13 @@ kda_status kda_linattn_chunk_prefill_backward(
     }
     const kda::linattn::Operand od{d_o, (int64_t)H * dv_dim, 1, do_dt == KDA_BF16};
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    const bool all_rows = !cu_seqlens || cu_seqlens_host;
+    const kda::dbg::Rows which = of_sequences(cu_seqlens, N);
+    const int64_t wqk = (int64_t)Hk * dk_dim, wv = (int64_t)H * dv_dim;
     return run_checked(
         fn, s,
         [&](kda::dbg::Session& c) {
-          in.scan(c);
-          c.add("d_o", d_o, T_tot * H * dv_dim, do_dt == KDA_BF16, kFinite);
+          in.scan(c, which);
+          c.add_rows("d_o", d_o, T_tot, wv, wv, do_dt == KDA_BF16, kFinite, which);
           c.add_states("initial_state", initial_state, false, nullptr, N, N, H, dk_dim * dv_dim);
           c.add_states("d_final_state", d_final_state, false, nullptr, N, N, H, dk_dim * dv_dim);
         },
@@ -317,13 +323,12 @@ kda_status kda_linattn_chunk_prefill_backward(
                                                dg, d_initial_state, workspace, s);
         },
         [&](kda::dbg::Session& c) {
-          if (all_rows) {
-            const bool b = grad_dt == KDA_BF16;
-            c.add("dq", dq, T_tot * Hk * dk_dim, b, kFinite);
-            c.add("dk", dk, T_tot * Hk * dk_dim, b, kFinite);
-            c.add("dv", dv, T_tot * H * dv_dim, b, kFinite);
-            c.add("dg", dg, g_len, false, kFinite);
-          }
+          const bool b = grad_dt == KDA_BF16;
+          c.add_rows("dq", dq, T_tot, wqk, wqk, b, kFinite, which);
+          c.add_rows("dk", dk, T_tot, wqk, wqk, b, kFinite, which);
+          c.add_rows("dv", dv, T_tot, wv, wv, b, kFinite, which);
+          if (in.per_token()) c.add_rows("dg", dg, T_tot, H, H, false, kFinite, which);
+          else c.add("dg", dg, g_len, false, kFinite);
           c.add_states("d_initial_state", d_initial_state, false, nullptr, N, N, H,
                        dk_dim * dv_dim);
         });
@@ -409,7 +414,7 @@ kda_status kda_linattn_recurrent_decode(const void* q, int64_t q_stride, const v
     return run_checked(
         fn, s,
         [&](kda::dbg::Session& c) {
-          in.scan(c);
+          in.scan(c, {nullptr, state_indices, num_slots});
           c.add_states("state", state, sb, state_indices, num_slots, N, H, dk * dv);
         },
         [&] {

@@ -25,8 +25,9 @@
  *
  * q, k, v, d_o and the states must be finite: a NaN or an infinity of one token
  * may reach every token of its chunk of 64 of that sequence and head, those
- * before it too.  A NaN in g is carried on.  (Rows of q, k, v and g that belong
- * to no sequence may hold anything.)
+ * before it too.  A NaN in g is carried on.  (Rows of q, k, v, g and d_o that belong
+ * to no sequence, and those of sequences that the decode skips, may hold anything;
+ * KDA_DEBUG does not look at them.)
  *
  * Sizes: T_tot < 2^31, H <= 16384, N*H <= 2^24; and the work items of a launch (fewer
  * than 2^32) have to hold the call, which ends at about 3 million (sequence, head) pairs
