@@ -201,11 +201,13 @@ __device__ __forceinline__ void statistics(f32x8 (&x)[M], const f32x8 (&dy)[T ? 
   }
 }
 
-// Row owner q of Q walks rows q, q + Q, ... (Q a multiple of groups).
+// Row owner q of Q walks rows q, q + Q, ... (Q a multiple of groups).  y may be x: a row
+// is read before it is written and by its owner only, so neither is __restrict__ (nor are
+// dy, x and dx below).
 template <bool XB, bool YB, int L, int M>
 __global__ void __launch_bounds__(threads<L>()) forward_kernel(
-    const void* __restrict__ x, const float* __restrict__ w, const float* __restrict__ b,
-    int64_t groups, void* __restrict__ y, int64_t rows, int d, float eps, int64_t Q) {
+    const void* x, const float* __restrict__ w, const float* __restrict__ b, int64_t groups,
+    void* y, int64_t rows, int d, float eps, int64_t Q) {
   constexpr int RPB = threads<L>() / L;
   __shared__ float s_part[L > 64 ? 2 * kSums * (L / 64) : 1];
   const int l = threadIdx.x % L;
@@ -248,9 +250,8 @@ __global__ void __launch_bounds__(threads<L>()) forward_kernel(
 
 template <bool YB, bool XB, int L, int M>
 __global__ void __launch_bounds__(threads<L>()) backward_kernel(
-    const void* __restrict__ dy, const void* __restrict__ x, const float* __restrict__ w,
-    int64_t groups, void* __restrict__ dx, float* __restrict__ part, int64_t rows, int d,
-    float eps, int64_t Q) {
+    const void* dy, const void* x, const float* __restrict__ w, int64_t groups, void* dx,
+    float* __restrict__ part, int64_t rows, int d, float eps, int64_t Q) {
   constexpr int RPB = threads<L>() / L;
   __shared__ float s_part[L > 64 ? 2 * kSums * (L / 64) : 1];
   const int l = threadIdx.x % L;

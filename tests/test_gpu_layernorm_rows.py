@@ -91,3 +91,52 @@ def test_a_spread_far_below_the_mean(d, mean):
     rnd = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
     x = (mean + rnd(6, d)).float()
     _check(x, 1 + 0.3 * rnd(d), rnd(d), rnd(6, d))
+
+
+# x's shape, weight's shape: every owner of rows has several, and some one more
+MANY = [
+    ((70001, 64), (64,)), ((140000, 64), (64,)), ((1500, 96, 128), (96, 128)), ((9001, 250), (250,)),
+    ((30011, 1000), (1000,)), ((9001, 1500), (1500,)), ((4500, 2049), (2049,)),
+    ((2250, 2, 5003), (2, 5003)), ((1100, 12288), (12288,)),
+]
+
+
+def _in_place(x, w, b, dy):
+    """The calls whose output is one of their inputs: (y over x, dx over dy, dx over x)."""
+    from gated_delta_rule_58_amd import linattn
+    rows, groups, d = linattn._norm_rows(x, w, b)
+    dt, s = linattn._dt(x), torch.cuda.current_stream().cuda_stream
+    n = kda.layernorm_backward_workspace_bytes(rows, groups, d)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    y = x.clone()
+    kda.layernorm(y, w, b, eps=EPS, out=y)
+    out = []
+    for over in (0, 1):
+        args = [dy.clone(), x.clone()]
+        dw, db = torch.empty_like(w), torch.empty_like(w)
+        assert linattn._fn("kda_layernorm_backward")(
+            args[0].data_ptr(), dt, args[1].data_ptr(), dt, w.data_ptr(), groups,
+            args[over].data_ptr(), dw.data_ptr(), db.data_ptr(), rows, d, EPS, ws.data_ptr(), n,
+            s) == 0
+        out.append((args[over], dw, db))
+    return y, out
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_in_place_over_many_rows(case, dtype):
+    """y over x, dx over dy and dx over x, with several rows an owner: the bits of the calls
+    with outputs of their own."""
+    need_gpu()
+    shape, wshape = MANY[case]
+    say("layernorm in place", shape, wshape, dtype)
+    gen = torch.Generator(device=DEV).manual_seed(case)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device=DEV)  # noqa: E731
+    x, dy, w, b = rnd(*shape).to(dtype), rnd(*shape).to(dtype), 1 + 0.3 * rnd(*wshape), rnd(*wshape)
+    y = kda.layernorm(x, w, b, eps=EPS)
+    g = kda.layernorm_backward(dy, x, w, eps=EPS)
+    y2, outs = _in_place(x, w, b, dy)
+    assert torch.equal(y, y2)
+    for out in outs:
+        for a, c in zip(g, out):
+            assert torch.equal(a, c)
