@@ -337,23 +337,26 @@ def layernorm_backward_workspace_bytes(rows: int, groups: int, d: int) -> int:
 
 def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor] = None,
                        eps: float = 1e-5, want_dbias: bool = True,
-                       workspace: Optional[torch.Tensor] = None):
+                       workspace: Optional[torch.Tensor] = None,
+                       bias: Optional[torch.Tensor] = None):
     """kda_layernorm_backward: gradients of layernorm(x, weight, bias, eps) against dy.
+    bias: its values do not matter; without a weight it says that there is one, and
+    dbias gets its shape.
 
-    Returns (dx in x's dtype, dweight, dbias), the last two float32 in weight's shape
-    (None without a weight; dbias None unless want_dbias)."""
-    rows, groups, d = _norm_rows(x, weight, None)
+    Returns (dx in x's dtype, dweight, dbias), the last two float32 in weight's (bias's)
+    shape (dweight None without a weight, dbias without either or unless want_dbias)."""
+    rows, groups, d = _norm_rows(x, weight, bias)
     dev = x.device
-    _same_device(dev, dy=dy, weight=weight, workspace=workspace)
+    _same_device(dev, dy=dy, weight=weight, bias=bias, workspace=workspace)
     _shape("dy", dy, *x.shape)
     dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dw = db = None
-    if weight is not None:
-        dw = torch.empty(weight.shape, dtype=torch.float32, device=dev)
-        db = torch.empty(weight.shape, dtype=torch.float32, device=dev) if want_dbias else None
-        if workspace is None:
-            nbytes = layernorm_backward_workspace_bytes(rows, groups, d)
-            workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+    affine = weight if weight is not None else bias
+    dw = None if weight is None else torch.empty(weight.shape, dtype=torch.float32, device=dev)
+    db = (torch.empty(affine.shape, dtype=torch.float32, device=dev)
+          if affine is not None and want_dbias else None)
+    if workspace is None and (dw is not None or db is not None):
+        nbytes = layernorm_backward_workspace_bytes(rows, groups, d)
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
     with _on(dev):
         st = _fn("kda_layernorm_backward")(
             _ptr(dy), _dt(dy), _ptr(x), _dt(x), _ptr(weight), groups, _ptr(dx), _ptr(dw),
