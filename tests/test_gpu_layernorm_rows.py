@@ -93,9 +93,11 @@ def test_a_spread_far_below_the_mean(d, mean):
     _check(x, 1 + 0.3 * rnd(d), rnd(d), rnd(6, d))
 
 
-# x's shape, weight's shape: every owner of rows has several, and some one more
+# x's shape, weight's shape: owners of rows have several and some of them one more, in
+# the backward always, in the forward where there are more rows than lanes for the card
 MANY = [
     ((70001, 64), (64,)), ((140000, 64), (64,)), ((1500, 96, 128), (96, 128)), ((9001, 250), (250,)),
+    ((40000, 250), (250,)),
     ((30011, 1000), (1000,)), ((9001, 1500), (1500,)), ((4500, 2049), (2049,)),
     ((2250, 2, 5003), (2, 5003)), ((1100, 12288), (12288,)),
 ]
@@ -140,3 +142,24 @@ def test_in_place_over_many_rows(case, dtype):
     for out in outs:
         for a, c in zip(g, out):
             assert torch.equal(a, c)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_many_rows_an_owner(case, dtype):
+    """Values where an owner walks down several rows: the next row's load, the turns of the
+    sums' LDS buffers, the running sums of dw and db.  The 64-bit formulas run on the device."""
+    need_gpu()
+    shape, wshape = MANY[case]
+    say("layernorm many rows", shape, wshape, dtype)
+    gen = torch.Generator(device=DEV).manual_seed(100 + case)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device=DEV)  # noqa: E731
+    x = (1.5 * rnd(*shape) + rnd(*shape[:-1], 1)).to(dtype)
+    dy, w, b = rnd(*shape).to(dtype), 1 + 0.3 * rnd(*wshape), rnd(*wshape)
+    y = kda.layernorm(x, w, b, eps=EPS)
+    dx, dw, db = kda.layernorm_backward(dy, x, w, eps=EPS)
+    by, bdx, bdw, bdb = _bounds(x, w, b, dy)
+    want = ref.norm_backward(dy, x, w, EPS)
+    for name, got, ref64, bound in (("y", y, ref.norm(x, w, b, EPS), by), ("dx", dx, want[0], bdx),
+                                    ("dw", dw, want[1], bdw), ("db", db, want[2], bdb)):
+        say(_within(name, got, ref64.cpu(), bound.cpu(), got.dtype))
