@@ -1453,27 +1453,33 @@ hipError_t launch_walk(const Args& A, int walks, bool wide, int kd, bool full, b
 }
 
 template <int DK, int DV>
-hipError_t launch_gradients_kd(const Args& A, bool out_bf16, hipStream_t s) {
+hipError_t launch_gradients_kd(const Args& A, bool alike, bool out_bf16, hipStream_t s) {
   const int64_t qk = walk_blocks(A, DV), v = walk_blocks(A, DK), blocks = 2 * qk + v;
   // A workgroup of dq or dk takes about half as long again as one of dv.  Where a
-  // third round of workgroups would leave more than half of the CUs idle, two
-  // thirds of dv's go before dk's: the CUs then get two of the long ones or three of
-  // the short ones each (T = 4096 x 96: 427 us, in the order dq, dk, dv 450; with
-  // more rounds, 8 sequences x 96, 3640 against 3515).
-  const bool mixed = qk == v && blocks > 2 * kCus && blocks <= 5 * kCus / 2;
+  // third round of workgroups would leave more than half of the CUs idle and the
+  // sequences are alike, two thirds of dv's go before dk's: the CUs then get two of the
+  // long ones or three of the short ones each.  us in this order / in the order dq, dk,
+  // dv, bf16, dk = dv = 128: T = 4096 x 96 heads 437 / 454, x 88 388 / 412, x 104 475 /
+  // 471; two of 2,048 x 48 193 / 206, twelve of 1,000 x 8 104 / 110; dk = dv = 64, T =
+  // 4096 x 192 325 / 345.  Sequences of different lengths start longest first, and
+  // splitting dv's short ones off delays dk's long ones: 4,000 and 96 x 48 280 / 229;
+  // 2,500, 1,200, 300 and 96 x 24 148 / 123; with more rounds, 8 sequences x 96, 3640 /
+  // 3515.
+  const bool mixed = alike && qk == v && blocks > 2 * kCus && blocks <= 5 * kCus / 2;
   const int v1 = mixed ? (int)(v / 12 * 8) : 0;
   const dim3 grid((unsigned)blocks), block(Waves<false, true>::threads);
   if (out_bf16) gradient_kernel<DK, DV, kByLength><<<grid, block, 0, s>>>(A, (int)qk, v1);
   else gradient_kernel<DK, DV, 2><<<grid, block, 0, s>>>(A, (int)qk, v1);
   return hipGetLastError();
 }
-// all walks of the backward, bf16 operands
-hipError_t launch_gradients(const Args& A, int dk, int dv, bool out_bf16, hipStream_t s) {
+// all walks of the backward, bf16 operands; alike: no sequence is much longer than another
+hipError_t launch_gradients(const Args& A, int dk, int dv, bool alike, bool out_bf16,
+                            hipStream_t s) {
   if (dk == 128)
-    return dv == 128 ? launch_gradients_kd<128, 128>(A, out_bf16, s)
-                     : launch_gradients_kd<128, 64>(A, out_bf16, s);
-  return dv == 128 ? launch_gradients_kd<64, 128>(A, out_bf16, s)
-                   : launch_gradients_kd<64, 64>(A, out_bf16, s);
+    return dv == 128 ? launch_gradients_kd<128, 128>(A, alike, out_bf16, s)
+                     : launch_gradients_kd<128, 64>(A, alike, out_bf16, s);
+  return dv == 128 ? launch_gradients_kd<64, 128>(A, alike, out_bf16, s)
+                   : launch_gradients_kd<64, 64>(A, alike, out_bf16, s);
 }
 
 hipError_t launch_scan(const Args& A, int walks, int kd, hipStream_t s) {
@@ -1724,13 +1730,16 @@ hipError_t launch_backward(const Problem& p, const Operand& q, const Operand& k,
   A.walk[2] = wv;
   Args B = A;  // dv needs no dots (and for dk != dv contracts over another width)
   B.first = 2;
+  // the longest is at most a quarter longer than the mean (the longest that it can be where
+  // the lengths are not known); segments are alike
+  const bool alike = A.nseg > 1 || 4 * longest_chunks(p) * p.N <= 5 * cdiv(p.T_tot, C);
   for (int phase = A.nseg > 1 ? 0 : 2; phase < 3; ++phase) {
     hipError_t e;
     if (phase == 1) {
       e = launch_scan(A, 2, DV, s);
       if (e == hipSuccess) e = launch_scan(B, 1, DK, s);
     } else if (phase == 2 && !wide) {
-      e = launch_gradients(A, DK, DV, grad_bf16, s);
+      e = launch_gradients(A, DK, DV, alike, grad_bf16, s);
     } else {
       const bool full = phase == 2;
       e = launch_walk<true>(A, 2, wide, DV, full, grad_bf16, s);

@@ -66,3 +66,22 @@ def test_short_sequences_of_a_large_call(lens):
     want = ref.backward(q, k, v, g, cu, do, S0, None, 0.7)[2]
     size = ref.backward(q.abs(), k.abs(), v.abs(), g, cu, do.abs(), S0.abs(), None, 0.7)[2]
     say(ref.check("dv", dv, want, size, rel, BF))
+
+
+@pytest.mark.parametrize("lens", [[96, 90, 101, 100], [300, 40, 7, 0]])
+def test_the_order_of_the_gradients_work_does_not_show(lens):
+    """Batches of 576 workgroups, of like and of different lengths: the order they start in
+    depends on the lengths where the host knows them, the gradients do not."""
+    need_gpu()
+    say("linattn order of work", lens)
+    H = 24
+    q, k, v, g, cu, S0 = _draw(lens, H, H, 128, 128, BF, "mild", 44)
+    do = torch.randn(cu[-1], H, 128, generator=torch.Generator().manual_seed(45)).to(BF)
+    dev = _gpu(q, k, v, g, do, S0)
+    got = [kda.linattn_chunk_prefill_backward(*dev[:5], **kw, initial_state=dev[5])
+           for kw in (_cu(cu), dict(cu_seqlens=_cu(cu)["cu_seqlens"]))]
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    heads = slice(0, 2)
+    part = [t[:, heads] for t in (q, k, v, g, do, S0)]
+    ref.check_backward([t[:, heads] for t in got[0]], *part[:4], cu, part[4], part[5])
