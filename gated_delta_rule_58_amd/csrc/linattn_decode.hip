@@ -131,9 +131,12 @@ hipError_t launch(const Operand& q, const Operand& k, const Operand& v, const De
                   float scale, hipStream_t s) {
   const int64_t pairs = (int64_t)N * H;
   // Few states: 32 columns a workgroup, so that more CUs take part; many: a whole
-  // state each.  us whole / tiled at 128 x 128: fp32 96 states 4.2 / 3.9, 384 8.0 /
-  // 7.8, 768 13.7 / 17.9; bf16, where 32 columns are half a cache line, 32 states
-  // 3.8 / 3.5, 96 4.0 / 4.1, 384 5.5 / 6.7.
+  // state each.  us whole / tiled, fp32 at dk x dv = 128 x 128: 96 states 4.9 / 4.5, 256
+  // 7.1 / 7.0, 512 12.4 / 13.2, 768 17.7 / 20.3; 128 x 64: 512 7.9 / 7.3, 1,024 14.0 /
+  // 12.5; 64 x 128: 512 8.0 / 7.4, 768 10.0 / 11.9; 64 x 64 within 5 % from 96 to 2,048.
+  // bf16, where 32 columns are half a cache line: 128 x 128: 64 states 4.4 / 3.9, 96 4.5 /
+  // 4.6, 384 6.5 / 8.2; 128 x 64: 96 4.0 / 3.8, 192 4.4 / 4.5, 768 7.0 / 7.9; 64 x 64: 96
+  // 3.8 / 3.5, 256 4.2 / 4.2, 768 5.9 / 6.4.
   const bool tiled = pairs < (S_BF16 ? 96 : 512);
   const int64_t blocks = pairs * (tiled ? DV / 32 : 1);
   const dim3 grid(static_cast<unsigned>((blocks + 7) / 8 * 8));

@@ -432,10 +432,11 @@ struct Place {
 // False: nothing (the grid is rounded up).  Every thread of the workgroup calls it.
 //
 // Workgroups go to the XCDs in turn; an XCD gets hb = H / 8 consecutive heads (of 8 hb in
-// the list of all segments' heads) with their tiles.  (Every eighth head instead: the
-// tokens of a head are H rows apart, so for H a multiple of 16 its rows and those of the
-// heads 16 further share one channel of the XCD's L2, and the XCD used two channels of
-// sixteen.)
+// the list of all segments' heads) with their tiles, which are neighbours in a token's row
+// and share q and k where those are shared.  It makes little difference; us like this /
+// with every eighth head on an XCD: 131,072 tokens x 16 heads (2 of q/k) 728 / 745, eight
+// sequences of 4,096 x 96 790 / 779, T = 4096 x 96 123 / 122, backward of T = 4096 x 64
+// 314 / 318.
 template <int KD>
 __device__ __forceinline__ bool locate(const Args& A, const Walk& W, int block, int* s_seq,
                                        Place& at) {
@@ -1428,10 +1429,11 @@ hipError_t launch_walk_kd(const Args& A, int walks, hipStream_t s) {
 //   three values  with dots: dg is a small difference of their sums, and for one
 //                 decay a head a sum of those; with two values it was up to 3e-5 off
 //   two           out is fp32, or bf16 and the sequence has at most one chunk of tokens
-//                 (kByLength), which costs nothing there (H = 96: T = 64 7.6 against 7.5
-//                 us; T = 256 14.3 against 13.3, T = 4096 146 against 124) and where the
-//                 few roundings do not average out.  By the sequence, not by the call: a
-//                 sequence gets the same digits whatever it is packed with
+//                 (kByLength), where the few roundings do not average out and the cost
+//                 is small (H = 96: T = 64 7.6 against 7.5 us, 512 packed sequences of 64
+//                 with states 3,010 against 2,850; T = 256 14.3 against 13.3, T = 4096
+//                 146 against 124).  By the sequence, not by the call: a sequence gets
+//                 the same digits whatever it is packed with
 //   one           out is bf16: off by 2.3e-3 of its norm where bf16's own rounding is
 //                 1.7e-3 off
 template <bool DOTS>
