@@ -192,7 +192,7 @@ __device__ __forceinline__ void statistics(f32x8 (&x)[M], const f32x8 (&dy)[T ? 
   }
   row_sum<L, 2 + T>(v, s_part, turn);
   const float off = v[1] * inv_d;  // the mean's own error
-  const float var = v[0] * inv_d - off * off;
+  const float var = fmaf(-off, off, v[0] * inv_d);  // (an overflow stays one: no inf - inf)
   rstd = 1.0f / sqrtf((var < 0.f ? 0.f : var) + eps);  // (a NaN stays one)
   shift = -off * rstd;
   if constexpr (T) {

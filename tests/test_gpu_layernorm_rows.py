@@ -163,3 +163,17 @@ def test_many_rows_an_owner(case, dtype):
     for name, got, ref64, bound in (("y", y, ref.norm(x, w, b, EPS), by), ("dx", dx, want[0], bdx),
                                     ("dw", dw, want[1], bdw), ("db", db, want[2], bdb)):
         say(_within(name, got, ref64.cpu(), bound.cpu(), got.dtype))
+
+
+@pytest.mark.parametrize("d", [777, 1000, 5120, 12288])
+def test_rows_whose_squares_overflow(d):
+    """Values whose differences' squares are beyond fp32: 1 / sqrt(inf) is 0, and the row
+    gives its bias, not NaN."""
+    need_gpu()
+    say("layernorm overflow", d)
+    x = torch.full((4, d), 1e32, device=DEV)
+    x[1] = -3.3e33
+    x[2, ::2] *= -1.0
+    x[3, 5] = 1e30
+    w, b = torch.ones(d, device=DEV) * 1.5, torch.randn(d, device=DEV)
+    assert torch.equal(kda.layernorm(x, w, b), b.expand(4, d))
