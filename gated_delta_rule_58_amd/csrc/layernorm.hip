@@ -6,15 +6,15 @@
 //
 // HBM-bound: x (and dy) are read once, y (dx) is written once, the row stays
 // in registers between.  Measured, bf16: forward of 393216 rows of 128 (96 weight
-// rows) 38 us, 5.3 TB/s; backward 62 us, 4.9 TB/s; backward of 2048 x 5003, 32 us,
+// rows) 39 us, 5.1 TB/s; backward 67 us, 4.5 TB/s; backward of 2048 x 5003 30 us,
 // where a row's chain (loads, two sums over 512 lanes) leaves the card idle.
 //
 // L lanes own a row: a part of a wave up to d = 256, a wave up to 1,024, a workgroup
 // beyond that; lane l holds the M runs of eight columns (m L + l) 8 .. + 7.  The
-// lanes of a row then walk down rows of the SAME weight row (row % groups), so that w, b and the gradients' sums stay in
-// registers: row q, q + Q, q + 2Q, ... with Q a multiple of groups.
-// Neighbouring lanes own neighbouring rows, so a wave's access is contiguous
-// whatever L is.  The next row is loaded before this one is worked on.
+// lanes of a row then walk down rows of the SAME weight row (row % groups), so that w,
+// b and the gradients' sums stay in registers: row q, q + Q, q + 2Q, ... with Q a
+// multiple of groups.  Neighbouring lanes own neighbouring rows, so a wave's access is
+// contiguous whatever L is.  The next row is loaded before this one is worked on.
 //
 // The statistics are two sums over the registers: the mean, then the differences
 // from it and their squares.  The mean of fp32 sums is a few ulps off, which beside a
@@ -272,8 +272,8 @@ __global__ void __launch_bounds__(threads<L>()) backward_kernel(
   const float inv_d = 1.0f / d;
   int turn = 0;
   // The next row on its way while this one is worked on; 1,024 lanes have 128
-  // registers each, enough for one row only (512 x 12288 bf16: with the next one,
-  // spilled, 34 us, without 27).
+  // registers each, enough for one row only (512 x 12288 fp32: with the next one,
+  // spilled, 51 us, without 28).
   constexpr bool AHEAD = L < 1024;
   Eight<XB> rx[M];
   Eight<YB> ry[M];
@@ -352,17 +352,17 @@ int64_t owners(int64_t rows, int64_t groups, int64_t most) {
   const int64_t q = most < 1 ? 1 : most > rows ? rows : most;
   return (q + groups - 1) / groups * groups;
 }
-// lanes for the card: us at 2,048 / 4,096 a CU: 393216 x 128 bf16 36 / 31, 65536 x
-// 1024 44 / 42, 16384 x 4096 44 / 42; 8192 x 5000, where a row takes a workgroup of
-// 512, 35 / 38
+// lanes for the card: us at 2,048 / 4,096 a CU, bf16: 393216 x 128 37 / 36, 65536 x 1024
+// 46 / 43, 16384 x 4096 46 / 43; of 512 lanes a row, 8192 x 5000 44 / 41, 2048 x 5003
+// 14.1 / 14.7; of 1,024, 4096 x 12288 52 / 55
 int64_t forward_owners(int64_t rows, int64_t groups, int L) {
-  return owners(rows, groups, 256 * (L <= 256 ? 4096 : 2048) / L);
+  return owners(rows, groups, 256 * (L <= 512 ? 4096 : 2048) / L);
 }
 // Every owner of the backward also writes 2 d sums, which are read again: fewer
-// lanes (1,024 a CU and run of eight columns; us with half of that / that / twice:
-// 393216 x 128 bf16 74 / 61 / 70, 65536 x 1024 91 / 91 / 113), and at least eight
-// rows each (1024 x 4096: 16, with two rows each 20) unless that leaves CUs without
-// a workgroup (512 x 12288 fp32: 128 owners 59, 256 48).
+// lanes (1,024 a CU and run of eight columns; us with half of that / that / twice, bf16:
+// 393216 x 128 74 / 65 / 72, 65536 x 1024 88 / 88 / 107, 16384 x 4096 95 / 86 / 99), and
+// at least eight rows each (1024 x 4096: 18.5, with two rows each 20.5) unless that
+// leaves CUs without a workgroup (512 x 12288: 128 owners 24.4, 256 22.7).
 int64_t backward_owners(int64_t rows, int64_t groups, int L, int M) {
   const int64_t one_each = 256 * (L < 256 ? 256 / L : 1);  // a workgroup a CU
   int64_t q = 256 * 1024 / (L * M);

@@ -52,10 +52,10 @@
 // those LDS is busy for 1,600 (16-byte reads at 256 B a cycle, transposing ones at
 // 128, stores at 80 to 128) and the matrix units of a SIMD for 1,400; the rest is
 // the chain scores -> decays -> c^T P^T of an output wave.  Measured, dk = dv = 128, bf16:
-// T = 4096 x 96 heads 117 us (1.65 us a chunk of a lone workgroup; 3.5 TB/s of what
-// has to be read and written), 8 sequences of 32,768 tokens together x 96 833 us
-// (4.0 TB/s), one of 131,072 x 16 heads, in segments, 761 us; backward of T = 4096 x
-// 96 432 us.  On the way there: scores and readout in the state's waves 302 us, waves
+// T = 4096 x 96 heads 116 us (1.65 us a chunk of a lone workgroup; 3.5 TB/s of what
+// has to be read and written), 8 sequences of 32,768 tokens together x 96 831 us
+// (4.0 TB/s), one of 131,072 x 16 heads, in segments, 751 us; backward of T = 4096 x
+// 96 427 us.  On the way there: scores and readout in the state's waves 302 us, waves
 // of two kinds 253, copies and decays in waves of their own 167, one value of S and P
 // and eight output columns a store 119.
 //
