@@ -1366,14 +1366,15 @@ __global__ void __launch_bounds__(NTHR) group_sum_kernel(Args A, const float* hq
   const int Hk = A.H / group;
   const int64_t per = (int64_t)Hk * (d / 4);
   const int64_t i = (int64_t)blockIdx.x * NTHR + threadIdx.x;
-  // rows behind the last sequence stay as they are
-  int64_t T = A.T_tot;
+  // rows of no sequence stay as they are
+  int64_t t0 = 0, t1 = A.T_tot;
   if (A.cu) {
-    const int e = A.cu[A.N];
-    T = e < 0 ? 0 : (e > A.T_tot ? A.T_tot : e);
+    const int b = A.cu[0], e = A.cu[A.N];
+    t0 = b < 0 ? 0 : b;
+    t1 = e < 0 ? 0 : (e > A.T_tot ? A.T_tot : e);
   }
-  if (i >= T * per) return;
   const int64_t t = i / per;
+  if (t < t0 || t >= t1) return;
   const int rest = static_cast<int>(i - t * per);
   const int hk_i = rest / (d / 4), c = (rest % (d / 4)) * 4;
   const float* src = blockIdx.y ? hk : hq;

@@ -55,10 +55,11 @@ extern "C" {
  *         q_stride, k_stride, v_stride (elements)
  *   g     fp32 [T_tot, H] or [H] (g_len says which)
  *   cu_seqlens [N+1] int32, device copy; sequence n owns tokens cu_seqlens[n]
- *         .. cu_seqlens[n+1]-1.  NULL: N sequences of T_tot / N tokens each
- *         (T_tot % N == 0).  cu_seqlens_host: as for kda_chunk_prefill (NULL
- *         allowed; the kernels clamp every range into [0, T_tot]).  Rows of o
- *         behind the last sequence are left as they were.
+ *         .. cu_seqlens[n+1]-1.  It must not decrease and begins at 0.  NULL: N
+ *         sequences of T_tot / N tokens each (T_tot % N == 0).  cu_seqlens_host:
+ *         as for kda_chunk_prefill (NULL allowed; the kernels clamp every range
+ *         into [0, T_tot]).  Rows of o that belong to no sequence, behind the
+ *         last one, are left as they were.
  *   initial_state, final_state: pools [num_slots, H, dk, dv] of state_dt, either
  *         NULL, possibly the same (an in-place update), addressed by
  *         state_indices or by sequence, with the rules of
@@ -172,9 +173,10 @@ kda_status kda_linattn_recurrent_decode(const void* q, int64_t q_stride, const v
  *   weight, bias  fp32 [groups, d], either NULL (1 and 0); row r uses row
  *           r % groups: groups = 1 shares one weight, groups = H over an
  *           [T, H, d] tensor (rows = T*H) gives every head its own.
- * 1 <= d <= 16384, rows % groups == 0.  Pointers need only their element's
- * alignment.  The mean and the mean square of the differences are two sums in
- * fp32 over values held in registers.
+ * 1 <= d <= 16384, rows % groups == 0, groups <= 65535.  Pointers need only their
+ * element's alignment.  The mean and the mean square of the differences are sums in
+ * fp32 over values held in registers; the mean's own rounding error comes off both, so
+ * a row whose spread is far below its mean keeps its digits.
  */
 kda_status kda_layernorm(const void* x, kda_dtype x_dt, const float* weight, const float* bias,
                          int64_t groups, void* y, kda_dtype y_dt, int64_t rows, int32_t d,

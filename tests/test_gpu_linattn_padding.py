@@ -177,3 +177,39 @@ def test_rows_behind_in_a_replayed_graph():
         torch.cuda.synchronize()
         for x, y in zip(out, want):
             assert torch.equal(x, y) and not x[end:].any()
+
+
+@pytest.mark.parametrize("cu", [[5, 30, 90], [-4, 200, 300], [60, 20, 90], [0, 140, 70], [200, 300, 500]])
+def test_lengths_out_of_order_stay_inside_the_tensors(cu):
+    """Device lengths that no host copy was checked for: ranges are clamped, rows of no
+    sequence stay as they were, and what lies before and behind the tensors too."""
+    need_gpu()
+    say("linattn bad device lengths", cu)
+    from gated_delta_rule_58_amd import linattn
+    H, Hk, T = 4, 2, 140
+    q, k, v, g, _, _ = _draw([T], H, Hk, 128, 64, BF, "mild", 37)
+    do = torch.randn(T, H, 64, generator=torch.Generator().manual_seed(38)).to(BF)
+    dev = _gpu(q, k, v, g, do)
+    dev_cu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    shapes = [((Hk, 128), BF), ((Hk, 128), BF), ((H, 64), BF), ((H,), F32), ((H, 64), BF)]
+    whole = [torch.full((T + 128,) + s, 7.0, dtype=d, device=DEV) for s, d in shapes]
+    outs = [w[64:64 + T] for w in whole]
+    n = kda.linattn_chunk_prefill_backward_workspace_bytes(T, 2, H, Hk, 128, 64)
+    ws = torch.full((n + 4096,), 255, dtype=torch.uint8, device=DEV)
+    st = linattn._fn("kda_linattn_chunk_prefill_backward")(
+        dev[0].data_ptr(), Hk * 128, dev[1].data_ptr(), Hk * 128, dev[2].data_ptr(), H * 64, 1,
+        dev[3].data_ptr(), T * H, dev_cu.data_ptr(), None, 2, None, dev[4].data_ptr(), 1, None,
+        *[t.data_ptr() for t in outs[:3]], 1, outs[3].data_ptr(), None, T, H, Hk, 128, 64, 1.0,
+        ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    kda.linattn_chunk_prefill(*dev[:4], cu_seqlens=dev_cu, out=outs[4])
+    assert torch.all(ws[n:] == 255)
+    clamp = lambda x: min(max(x, 0), T)  # noqa: E731
+    mine = torch.zeros(T, dtype=torch.bool, device=DEV)
+    for a, b in zip(cu, cu[1:]):
+        mine[clamp(a):max(clamp(b), clamp(a))] = True
+    for w, t in zip(whole, outs):
+        assert torch.all(w[:64] == 7.0) and torch.all(w[64 + T:] == 7.0)
+        if cu == sorted(cu):
+            assert torch.all(t[~mine] == 7.0)
+            assert torch.isfinite(t[mine]).all()
