@@ -1761,8 +1761,8 @@ hipError_t launch_backward(const Problem& p, const Operand& q, const Operand& k,
     if (e != hipSuccess) return e;
   }
   if (group > 1 && p.T_tot > 0) {
-    group_sum_kernel<<<dim3((unsigned)group_sum_blocks(p), 2), NTHR, 0, s>>>(A, b.hq, b.hk, DK, group, dq, dk,
-                                                         grad_bf16);
+    group_sum_kernel<<<dim3((unsigned)group_sum_blocks(p), 2), NTHR, 0, s>>>(
+        A, b.hq, b.hk, DK, group, dq, dk, grad_bf16);
     e = hipGetLastError();
   }
   return e;
