@@ -2,7 +2,7 @@
 
 Thin Python binding over the C ABI of libkda.so (include/kda.h, and
 include/kda_linattn.h for linear attention with one decay per head and layer
-norm): argument marshalling only.  Every step of the computation runs in the library's HIP
+norm, include/kda_gatedrec.h for the gated linear recurrence and RMS norm): argument marshalling only.  Every step of the computation runs in the library's HIP
 kernels; PyTorch only provides device memory and the current stream.  There
 is no fallback path: if libkda.so is missing or cannot be loaded, importing
 the binding's entry points raises.
@@ -36,4 +36,15 @@ from .linattn import (  # noqa: F401
     layernorm,
     layernorm_backward,
     layernorm_backward_workspace_bytes,
+)
+from .gatedrec import (  # noqa: F401
+    gatedrec_scan,
+    gatedrec_scan_workspace_bytes,
+    gatedrec_scan_backward,
+    gatedrec_scan_backward_workspace_bytes,
+    gatedrec_decode,
+    rmsnorm,
+    rmsnorm_e4m3,
+    rmsnorm_backward,
+    rmsnorm_backward_workspace_bytes,
 )

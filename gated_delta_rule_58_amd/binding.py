@@ -110,7 +110,11 @@ def exported_symbols():
             "kda_gate_backward_workspace_bytes", "kda_linattn_chunk_prefill",
             "kda_linattn_chunk_prefill_workspace_bytes", "kda_linattn_chunk_prefill_backward",
             "kda_linattn_chunk_prefill_backward_workspace_bytes", "kda_linattn_recurrent_decode",
-            "kda_zero_rows_behind", "kda_layernorm", "kda_layernorm_backward", "kda_layernorm_backward_workspace_bytes"]
+            "kda_zero_rows_behind", "kda_layernorm", "kda_layernorm_backward", "kda_layernorm_backward_workspace_bytes",
+            "kda_gatedrec_scan", "kda_gatedrec_scan_workspace_bytes", "kda_gatedrec_starts_bytes",
+            "kda_gatedrec_scan_backward", "kda_gatedrec_scan_backward_workspace_bytes",
+            "kda_gatedrec_decode", "kda_rmsnorm", "kda_rmsnorm_e4m3", "kda_rmsnorm_backward",
+            "kda_rmsnorm_backward_workspace_bytes"]
 
 
 def _check(status: int):

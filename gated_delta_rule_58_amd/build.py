@@ -11,7 +11,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkda.so")
 SOURCES = ["api.hip", "debug.hip", "gate.hip", "decode.hip", "decode_gated.hip", "prefill.hip", "prep.hip",
            "state.hip", "shortconv.hip", "backward.hip", "linattn_api.hip", "linattn_walk.hip",
-           "linattn_decode.hip", "layernorm.hip"]
+           "linattn_decode.hip", "layernorm.hip", "gatedrec_api.hip", "gatedrec_scan.hip",
+           "gatedrec_backward.hip", "gatedrec_decode.hip", "rmsnorm.hip"]
 ARCH = os.environ.get("KDA_OFFLOAD_ARCH", "gfx950")
 
 

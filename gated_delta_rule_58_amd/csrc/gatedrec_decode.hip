@@ -1,0 +1,101 @@
+// kda_gatedrec_decode: one token per sequence over a pool of states [slots, C].
+//
+// Per (sequence n, channel c): h = exp(g) S[slot(n), c] + m sigmoid(i) x, which is the
+// output and, rounded to the pool's type, the new state.  A value reads and writes its
+// state and reads x, r and i: HBM-bound, and by the launch where there are few.
+//
+// Beside 1 the decay is taken as 1 - d with d kept (gatedrec_device.hpp): a state that
+// decays by 1e-5 a step would otherwise drift by 6e-3 of itself from what a scan gives.
+#include "gatedrec_device.hpp"
+
+namespace kda {
+namespace gatedrec {
+namespace {
+
+template <bool BF16, bool SB, int V, bool GATE, bool GATED, bool NORM>
+__global__ void __launch_bounds__(256) decode_kernel(
+    const Inputs in, int N, int C, void* pool, int64_t num_slots,
+    const int32_t* __restrict__ slots, void* __restrict__ h, bool h_bf16) {
+  constexpr int ES = BF16 ? 2 : 4;
+  const int64_t per = (C + V - 1) / V;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= per * N) return;
+  const int64_t n = id / per;
+  const int c = (int)(id - n * per) * V;
+  const int64_t slot = slots ? (int64_t)slots[n] : n;
+  const int64_t at = n * C + c;
+  float out[V];
+  if (slot < 0 || slot >= num_slots) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) out[v] = 0.0f;
+    store_row<V>(h, at, out, h_bf16);
+    return;
+  }
+  Vals<BF16, V> rx, rr, ri;
+  Vals<SB, V> st;
+  char* ps = static_cast<char*>(pool) + (slot * C + c) * (SB ? 2 : 4);
+  st.load(ps);
+  rr.load(static_cast<const char*>(in.r.p) + (n * in.r.stride + c) * ES);
+  rx.load(static_cast<const char*>(in.x.p) + (n * in.x.stride + c) * ES);
+  if constexpr (GATED) ri.load(static_cast<const char*>(in.i.p) + (n * in.i.stride + c) * ES);
+  Params<V, GATE> par;
+  par.load(in, c);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const float g = par.log2_decay(rr.get(v), v);
+    const float a = exp2_fast(g);
+    float u = rx.get(v);
+    if constexpr (GATED) u *= sigmoid_fast(ri.get(v));
+    if constexpr (NORM) u *= __builtin_amdgcn_sqrtf(one_minus_square(g, a));
+    out[v] = decayed_onto(decay_code(g), st.get(v), u);
+  }
+  Vals<SB, V>::store(ps, out);
+  store_row<V>(h, at, out, h_bf16);
+}
+
+}  // namespace
+
+hipError_t launch_decode(const Inputs& in, int N, int C, void* pool, bool state_bf16,
+                         int64_t num_slots, const int32_t* slots, void* h, bool h_bf16,
+                         hipStream_t s) {
+  if (N == 0) return hipSuccess;
+  const Out outs[] = {{h, h_bf16}, {pool, state_bf16}};
+  const int V = width(in, C, outs, 2);
+  const int64_t grid = ((int64_t)N * ((C + V - 1) / V) + 255) / 256;
+#define KDA_GR(BF, SB, V_, G, I, N_)                                                            \
+  decode_kernel<BF, SB, V_, G, I, N_><<<(unsigned)grid, 256, 0, s>>>(in, N, C, pool, num_slots, \
+                                                                   slots, h, h_bf16)
+#define KDA_GR_N(BF, SB, V_, G, I)                    \
+  do {                                                \
+    if (in.normalize) KDA_GR(BF, SB, V_, G, I, true); \
+    else KDA_GR(BF, SB, V_, G, I, false);             \
+  } while (0)
+#define KDA_GR_I(BF, SB, V_, G)                \
+  do {                                         \
+    if (in.i.p) KDA_GR_N(BF, SB, V_, G, true); \
+    else KDA_GR_N(BF, SB, V_, G, false);       \
+  } while (0)
+#define KDA_GR_G(BF, SB, V_)                   \
+  do {                                         \
+    if (in.A_log) KDA_GR_I(BF, SB, V_, true);  \
+    else KDA_GR_I(BF, SB, V_, false);          \
+  } while (0)
+#define KDA_GR_V(BF, SB)              \
+  do {                                \
+    if (V == 2) KDA_GR_G(BF, SB, 2);  \
+    else KDA_GR_G(BF, SB, 1);         \
+  } while (0)
+  if (in.bf16 && state_bf16) KDA_GR_V(true, true);
+  else if (in.bf16) KDA_GR_V(true, false);
+  else if (state_bf16) KDA_GR_G(false, true, 1);
+  else KDA_GR_G(false, false, 1);
+#undef KDA_GR_V
+#undef KDA_GR_G
+#undef KDA_GR_I
+#undef KDA_GR_N
+#undef KDA_GR
+  return hipGetLastError();
+}
+
+}  // namespace gatedrec
+}  // namespace kda

@@ -1,0 +1,327 @@
+// kda_gatedrec_scan: the gated linear recurrence over a packed batch, per channel
+//
+//   h_t = a_t h_{t-1} + b_t,  a = exp(g),  b = m sigmoid(i) x,  m = sqrt(1 - exp(2 g))
+//
+// x, r and i are read once and h written once.  A tile is kTile tokens of 64 V channels; a
+// wave holds L of the tokens, a lane V channels, all in registers: the gate first, then the
+// wave's own decay and contribution (from h = 0), which meet in LDS; the tile's own go to
+// the tiles behind it (gatedrec_device.hpp), the state before it comes, and every wave
+// runs its tokens again from the state that it begins with.  The factor 1 - a^2 under the
+// root is formed from g, so that slow channels keep its digits.
+//
+// A sequence's border inside a wave's tokens is a bit of a mask (uniform over the wave):
+// the state restarts there from the sequence's entry state, which is part of b of that
+// token, and is cut off from everything before.
+#include "gatedrec_device.hpp"
+
+namespace kda {
+namespace gatedrec {
+namespace {
+
+constexpr int kWaves = 8;
+constexpr int kL = 16;
+constexpr int kTile = kWaves * kL;
+static_assert(kTile % kStartsTokens == 0 && kStartsTokens % kL == 0, "starts at waves' tokens");
+
+struct Args {
+  Inputs in;
+  Seqs q;
+  int C;
+  StatePool st;
+  void* h;
+  bool h_bf16;
+  float* starts;
+  Chain chain;
+  int tiles, blocks;  // tiles along the tokens, workgroups across the channels
+};
+
+__device__ __forceinline__ int64_t slot_of(const StatePool& st, int n) {
+  const int64_t s = st.idx ? (int64_t)st.idx[n] : n;
+  return s >= 0 && s < st.slots ? s : -1;
+}
+
+// The final states of sequences without tokens are their entry states.
+__device__ void copy_empty(const Args& A, int first, int step) {
+  for (int n = first; n < A.q.N; n += step) {
+    if (A.q.start(n + 1) > A.q.start(n)) continue;
+    const int64_t s = slot_of(A.st, n);
+    if (s < 0) continue;
+    for (int c = threadIdx.x; c < A.C; c += blockDim.x) {
+      const int64_t at = s * A.C + c;
+      const float x = A.st.in ? load1(A.st.in, at, A.st.bf16) : 0.0f;
+      if (A.st.bf16) static_cast<uint16_t*>(A.st.out)[at] = f32_to_bf16_bits(x);
+      else static_cast<float*>(A.st.out)[at] = x;
+    }
+  }
+}
+
+template <bool BF16, int V, bool GATE, bool GATED, bool NORM>
+__global__ void __launch_bounds__(64 * kWaves) scan_kernel(const Args A) {
+  constexpr int L = kL, W = kWaves, CB = 64 * V, ES = BF16 ? 2 : 4;
+  __shared__ float s_sum[W][CB], s_add[W][CB], s_from[W][CB];
+  __shared__ int s_cut[W];
+  __shared__ uint32_t s_ticket;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool chained = A.chain.ticket != nullptr;
+  const int work = chained ? A.tiles * A.blocks : A.blocks;
+  if ((int)blockIdx.x >= work) {
+    copy_empty(A, blockIdx.x - work, gridDim.x - work);
+    return;
+  }
+  int id = blockIdx.x;
+  if (chained) {
+    if (threadIdx.x == 0)
+      s_ticket = __hip_atomic_fetch_add(A.chain.ticket, 1u, __ATOMIC_RELAXED,
+                                        __HIP_MEMORY_SCOPE_AGENT) + 1u;  // it begins at all ones
+    __syncthreads();
+    id = __builtin_amdgcn_readfirstlane(s_ticket);
+    if ((uint32_t)id >= (uint32_t)work) return;
+  }
+  const int c = (id % A.blocks) * CB + lane * V;
+  const bool on = c < A.C;
+  const int cc = on ? c : 0;
+  const int live = A.q.live();
+  Params<V, GATE> par;
+  par.load(A.in, cc);
+
+  float carry[V];  // of wave 0: the state before the tile, where one workgroup walks them all
+  const int k_end = chained ? id / A.blocks + 1 : A.tiles;
+  for (int k = chained ? id / A.blocks : 0; k < k_end; ++k) {
+    const int tile0 = k * kTile;
+    if (tile0 >= live) return;
+    const int t0 = tile0 + wave * L;
+    const int count = live - t0 < 0 ? 0 : live - t0 < L ? live - t0 : L;
+
+    Vals<BF16, V> rx[L], rr[L], ri[GATED ? L : 1];
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      const int64_t t = t0 + j < live ? t0 + j : live - 1;
+      rr[j].load(static_cast<const char*>(A.in.r.p) + t * A.in.r.stride * ES + (int64_t)cc * ES);
+      if constexpr (GATED)
+        ri[j].load(static_cast<const char*>(A.in.i.p) + t * A.in.i.stride * ES + (int64_t)cc * ES);
+      rx[j].load(static_cast<const char*>(A.in.x.p) + t * A.in.x.stride * ES + (int64_t)cc * ES);
+    }
+    Borders bd;
+    bd.find(A.q, t0, count);
+
+    float a[L][V], b[L][V], sum[V], add[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) sum[v] = add[v] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float g = par.log2_decay(rr[j].get(v), v);
+        a[j][v] = exp2_fast(g);
+        float u = rx[j].get(v);
+        if constexpr (GATED) u *= sigmoid_fast(ri[j].get(v));
+        if constexpr (NORM)
+          u *= __builtin_amdgcn_sqrtf(one_minus_square(g, a[j][v]));
+        b[j][v] = u;
+        if (j < count) sum[v] += g;
+      }
+      if (bd.first >> j & 1u) {
+        float s0[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) s0[v] = add[v] = 0.0f;
+        if (A.st.in) {
+          const int64_t s = slot_of(A.st, A.q.find(t0 + j));
+          if (s >= 0) load_state<V>(A.st.in, s * A.C + cc, s0, A.st.bf16);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) b[j][v] = fmaf(a[j][v], s0[v], b[j][v]);
+      }
+      if (j < count)
+#pragma unroll
+        for (int v = 0; v < V; ++v) add[v] = fmaf(a[j][v], add[v], b[j][v]);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      s_sum[wave][lane * V + v] = sum[v];
+      s_add[wave][lane * V + v] = add[v];
+    }
+    if (lane == 0) s_cut[wave] = bd.first != 0;
+    __syncthreads();
+
+    if (wave == 0) {
+      // the tile's own decay and contribution; behind a border, its state
+      float own[V], code[V][W], all[V];
+      bool cut = false;
+#pragma unroll
+      for (int v = 0; v < V; ++v) own[v] = all[v] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const bool cw = s_cut[w] != 0;
+        cut |= cw;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float s = s_sum[w][lane * V + v];
+          code[v][w] = decay_code(s);
+          all[v] += s;
+          const float x = s_add[w][lane * V + v];
+          own[v] = cw ? x : decayed_onto(code[v][w], own[v], x);
+        }
+      }
+      const bool alone = k == 0 || (bd.first & 1u);  // the tile begins with a sequence
+      float from[V], ends[V], tile_code[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        tile_code[v] = decay_code(all[v]);
+        from[v] = 0.0f;
+        ends[v] = own[v];
+      }
+      if (chained) {
+        const int64_t at = (int64_t)k * A.C + cc;
+        if (on) {
+          if (cut) {
+            publish<V>(A.chain.state + at, own);
+          } else {
+            publish<V>(A.chain.code + at, tile_code);
+            publish<V>(A.chain.add + at, own);
+          }
+        }
+        if (!alone) look_back<V>(A.chain, A.C, k, cc, on, from);
+      } else if (!alone) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) from[v] = carry[v];
+      }
+      if (!cut) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) ends[v] = decayed_onto(tile_code[v], from[v], own[v]);
+        if (chained && on) publish<V>(A.chain.state + (int64_t)k * A.C + cc, ends);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) carry[v] = ends[v];
+      // what every wave begins with
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        if (A.starts && on && (w * L) % kStartsTokens == 0 && tile0 + w * L < live)
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            A.starts[(int64_t)((tile0 + w * L) / kStartsTokens) * A.C + c + v] = from[v];
+        const bool cw = s_cut[w] != 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          s_from[w][lane * V + v] = from[v];
+          const float x = s_add[w][lane * V + v];
+          from[v] = cw ? x : decayed_onto(code[v][w], from[v], x);
+        }
+      }
+    }
+    __syncthreads();
+
+    if (A.h) {
+      float h[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = s_from[wave][lane * V + v];
+#pragma unroll
+      for (int j = 0; j < L; ++j) {
+        if (j < count) {
+          if (bd.first >> j & 1u)
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = 0.0f;
+#pragma unroll
+          for (int v = 0; v < V; ++v) h[v] = fmaf(a[j][v], h[v], b[j][v]);
+          if (on) store_row<V>(A.h, (int64_t)(t0 + j) * A.C + c, h, A.h_bf16);
+          if (A.st.out && (bd.last >> j & 1u)) {
+            const int64_t s = slot_of(A.st, A.q.find(t0 + j));
+            if (s >= 0 && on) store_state<V>(A.st.out, s * A.C + c, h, A.st.bf16);
+          }
+        }
+      }
+    }
+    if (!chained) __syncthreads();  // s_sum and s_add are read before they are written again
+  }
+}
+
+__global__ void __launch_bounds__(256) fill_kernel(u32x4* p, int64_t n) {
+  const int64_t step = (int64_t)gridDim.x * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step)
+    p[i] = u32x4{kEmpty, kEmpty, kEmpty, kEmpty};
+}
+
+int64_t tiles_of(int64_t T) { return (T + kTile - 1) / kTile; }
+
+}  // namespace
+
+bool scan_fits(const Batch& b) {
+  // 512 threads a workgroup, one for a tile of 64 channels, fewer than 2^32 in a launch
+  return tiles_of(b.T) * ((b.C + 63) / 64) < ((int64_t)1 << 23) - 1024;
+}
+size_t starts_bytes(int64_t T, int64_t C) {
+  return (size_t)((T + kStartsTokens - 1) / kStartsTokens) * C * sizeof(float);
+}
+hipError_t launch_fill(void* ws, size_t bytes, hipStream_t s) {
+  const int64_t n = (int64_t)(bytes / 16);
+  const int64_t blocks = (n + 1023) / 1024;
+  fill_kernel<<<(unsigned)(blocks < 1024 ? blocks : 1024), 256, 0, s>>>(static_cast<u32x4*>(ws), n);
+  return hipGetLastError();
+}
+
+size_t scan_workspace_bytes(int64_t T, int64_t C) {
+  const int64_t tiles = tiles_of(T);
+  return tiles > 1 ? chain_bytes(tiles, C) : 0;
+}
+
+hipError_t launch_scan(const Inputs& in, const Batch& b, const StatePool& st, void* h, bool h_bf16,
+                       float* starts, void* ws, size_t ws_bytes, hipStream_t s) {
+  Args A;
+  A.in = in;
+  A.q = Seqs{b.cu, b.N, b.T, b.N > 0 ? b.T / b.N : 0};
+  A.C = b.C;
+  A.st = st;
+  A.h = h;
+  A.h_bf16 = h_bf16;
+  A.starts = starts;
+  A.tiles = (int)tiles_of(b.T);
+  A.chain = Chain{};
+  const size_t need = scan_workspace_bytes(b.T, b.C);
+  if (need > 0 && ws && ws_bytes >= need) {
+    if (const hipError_t e = launch_fill(ws, need, s)) return e;
+    A.chain = chain_at(ws, A.tiles, b.C);
+  }
+  const Out outs[] = {{h, h_bf16}};
+  const int V = width(in, b.C, outs, 1);
+  A.blocks = (b.C + 64 * V - 1) / (64 * V);
+  // Sequences without tokens: workgroups of their own behind the tiles', unless the host
+  // knows that there are none or their states stay where they are.
+  bool empties = st.out && st.out != st.in;
+  if (empties && b.cu_host) {
+    empties = false;
+    for (int n = 0; n < b.N && !empties; ++n) empties = b.cu_host[n + 1] == b.cu_host[n];
+  }
+  if (!b.cu && b.T > 0) empties = false;
+  const int64_t work = A.chain.ticket ? (int64_t)A.tiles * A.blocks : A.tiles > 0 ? A.blocks : 0;
+  if (A.tiles == 0) A.blocks = 0;
+  const int64_t grid = work + (empties ? (b.N < 256 ? b.N : 256) : 0);
+  if (grid == 0) return hipSuccess;
+#define KDA_GR(BF, V_, G, I, N_) \
+  scan_kernel<BF, V_, G, I, N_><<<(unsigned)grid, 64 * kWaves, 0, s>>>(A)
+#define KDA_GR_N(BF, V_, G, I)                 \
+  do {                                         \
+    if (in.normalize) KDA_GR(BF, V_, G, I, true); \
+    else KDA_GR(BF, V_, G, I, false);          \
+  } while (0)
+#define KDA_GR_I(BF, V_, G)                \
+  do {                                     \
+    if (in.i.p) KDA_GR_N(BF, V_, G, true); \
+    else KDA_GR_N(BF, V_, G, false);       \
+  } while (0)
+#define KDA_GR_G(BF, V_)                   \
+  do {                                     \
+    if (in.A_log) KDA_GR_I(BF, V_, true);  \
+    else KDA_GR_I(BF, V_, false);          \
+  } while (0)
+  if (!in.bf16) KDA_GR_G(false, 1);
+  else if (V == 2) KDA_GR_G(true, 2);
+  else KDA_GR_G(true, 1);
+#undef KDA_GR_G
+#undef KDA_GR_I
+#undef KDA_GR_N
+#undef KDA_GR
+  return hipGetLastError();
+}
+
+}  // namespace gatedrec
+}  // namespace kda

@@ -10,39 +10,22 @@
 namespace {
 
 using kda::api::aligned;
+using kda::api::check_apart;
 using kda::api::fail;
 using kda::api::finite_scale;
+using kda::api::guarded;
 using kda::api::known_dtype;
+using kda::api::of_sequences;
 using kda::api::ok;
+using kda::api::overlap;
 using kda::api::run_checked;
+using kda::api::size_of;
+using kda::api::Span;
 using kda::dbg::kFinite;
 using kda::dbg::kNonPositive;
 
 constexpr int64_t kMaxStride = int64_t(1) << 22;  // 64 rows of fp32 stay below 2^30 bytes
 constexpr int64_t kMaxHeads = 16384;
-
-size_t size_of(kda_dtype d) { return d == KDA_BF16 ? 2 : 4; }
-
-struct Span {
-  const void* p;
-  size_t n;
-};
-bool overlap(const Span& a, const Span& b) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return a.p && b.p && a.n && b.n && x < y + b.n && y < x + a.n;
-}
-
-// Runs a C entry's body; an exception (the debug mode's strings and lock) becomes a status.
-template <class Body>
-kda_status guarded(const char* fn, Body body) {
-  try {
-    return body();
-  } catch (const std::exception& e) {
-    return fail(KDA_ERR_LAUNCH, "%s: %s", fn, e.what());
-  } catch (...) {
-    return fail(KDA_ERR_LAUNCH, "%s: unknown exception", fn);
-  }
-}
 
 // What the three linear attention calls have in common; `rows` is the token
 // (sequence) axis of q, k and v.
@@ -78,11 +61,6 @@ struct Inputs {
     else c.add("g", g, g_len, false, kNonPositive);
   }
 };
-
-// The rows of a packed batch that belong to a sequence.
-kda::dbg::Rows of_sequences(const int32_t* cu, int32_t N) {
-  return {cu ? cu + N : nullptr, nullptr, 0};
-}
 
 kda_status check_inputs(const char* fn, const Inputs& a) {
   if (a.H <= 0 || a.Hk <= 0 || a.rows < 0)
@@ -120,39 +98,14 @@ kda_status check_inputs(const char* fn, const Inputs& a) {
 
 kda_status check_batch(const char* fn, int64_t T_tot, int32_t N, int32_t H, const int32_t* cu,
                        const int32_t* cu_host) {
-  if (N <= 0) return fail(KDA_ERR_INVALID_ARG, "%s: need N > 0 (got %d)", fn, N);
-  if ((int64_t)N * H > ((int64_t)1 << 24))
+  if (N > 0 && (int64_t)N * H > ((int64_t)1 << 24))
     return fail(KDA_ERR_UNSUPPORTED, "%s: need N*H <= 2^24", fn);
-  if (!aligned(cu, 4)) return fail(KDA_ERR_ALIGNMENT, "%s: cu_seqlens must be 4-byte aligned", fn);
-  if (!cu) {
-    if (cu_host)
-      return fail(KDA_ERR_INVALID_ARG, "%s: cu_seqlens_host without cu_seqlens", fn);
-    if (T_tot % N)
-      return fail(KDA_ERR_SHAPE, "%s: without cu_seqlens T_tot = %lld must be a multiple of N = %d",
-                  fn, (long long)T_tot, N);
-  }
-  if (cu_host) {
-    if (cu_host[0] != 0 || cu_host[N] != T_tot)
-      return fail(KDA_ERR_SHAPE, "%s: cu_seqlens must start at 0 and end at T_tot = %lld "
-                                 "(got %d .. %d)", fn, (long long)T_tot, cu_host[0], cu_host[N]);
-    for (int32_t n = 0; n < N; ++n)
-      if (cu_host[n + 1] < cu_host[n])
-        return fail(KDA_ERR_SHAPE, "%s: cu_seqlens decreases at index %d", fn, n);
-  }
-  return KDA_OK;
+  return kda::api::check_batch(fn, T_tot, N, cu, cu_host);
 }
 
 kda_status too_large(const char* fn, int32_t N, int32_t H) {
   return fail(KDA_ERR_UNSUPPORTED, "%s: N = %d sequences of H = %d heads are more than a launch "
                                    "holds", fn, N, H);
-}
-
-// `out` must not touch any of the others.
-template <int K>
-kda_status check_apart(const char* fn, const char* what, const Span& out, const Span (&others)[K]) {
-  for (const Span& s : others)
-    if (overlap(out, s)) return fail(KDA_ERR_INVALID_ARG, "%s: %s overlaps another tensor", fn, what);
-  return KDA_OK;
 }
 
 }  // namespace
