@@ -40,9 +40,9 @@ bool backward_fits(const Batch& b);
 size_t starts_bytes(int64_t T, int64_t C);
 
 size_t scan_workspace_bytes(int64_t T, int64_t C);
-// ws may be null or short: the tiles of a channel are then walked one after the other.
+// h null: only starts are written.
 hipError_t launch_scan(const Inputs& in, const Batch& b, const StatePool& st, void* h, bool h_bf16,
-                       float* starts, void* ws, size_t ws_bytes, hipStream_t s);
+                       float* starts, void* ws, hipStream_t s);
 
 struct Gradients {
   void *dx = nullptr, *dr = nullptr, *di = nullptr;
@@ -54,7 +54,8 @@ hipError_t launch_backward(const Inputs& in, const Batch& b, const float* S0, co
                            const void* dh, bool dh_bf16, const float* dS, const Gradients& out,
                            void* ws, hipStream_t s);
 
-constexpr int64_t kMaxDecodeValues = (int64_t(1) << 32) - 256;  // threads of a launch
+// workgroups of a decode: a sequence's channels, 256 threads each, fewer than 2^32 in a launch
+constexpr int64_t kMaxDecodeGroups = (int64_t(1) << 24) - 1;
 hipError_t launch_decode(const Inputs& in, int N, int C, void* pool, bool state_bf16,
                          int64_t num_slots, const int32_t* slots, void* h, bool h_bf16,
                          hipStream_t s);

@@ -160,11 +160,15 @@ kda_status kda_gatedrec_scan(const void* x, int64_t x_stride, const void* r, int
     if (!aligned(h, size_of(h_dt)) || !aligned(initial_state, ss) || !aligned(final_state, ss) ||
         !aligned(starts, 4))
       return fail(KDA_ERR_ALIGNMENT, "%s: tensors must be aligned to their element size", fn);
+    const size_t need = kda::gatedrec::scan_workspace_bytes(T_tot, C);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+      return fail(KDA_ERR_WORKSPACE, "%s: need a workspace of at least %zu bytes (got %zu at %p)",
+                  fn, need, workspace_bytes, workspace);
     if (!aligned(workspace, 16))
       return fail(KDA_ERR_ALIGNMENT, "%s: workspace must be 16-byte aligned", fn);
     const size_t st_bytes = (size_t)num_slots * C * ss;
     const Span sh{h, (size_t)T_tot * C * size_of(h_dt)}, sf{final_state, st_bytes},
-        si{initial_state, st_bytes}, sw{workspace, workspace ? workspace_bytes : 0},
+        si{initial_state, st_bytes}, sw{workspace, need},
         sx{state_indices, state_indices ? (size_t)N * 4 : 0},
         sc{cu_seqlens, cu_seqlens ? ((size_t)N + 1) * 4 : 0},
         ss_{starts, kda::gatedrec::starts_bytes(T_tot, C)};
@@ -201,7 +205,7 @@ kda_status kda_gatedrec_scan(const void* x, int64_t x_stride, const void* r, int
         },
         [&] {
           return kda::gatedrec::launch_scan(in.device(), b, pool, h, h_dt == KDA_BF16, starts,
-                                            workspace, workspace ? workspace_bytes : 0, s);
+                                            workspace, s);
         },
         [&](kda::dbg::Session& c) {
           c.add_rows("h", h, T_tot, C, C, h_dt == KDA_BF16, kFinite, of_sequences(cu_seqlens, N));
@@ -319,9 +323,9 @@ kda_status kda_gatedrec_decode(const void* x, int64_t x_stride, const void* r, i
       return fail(KDA_ERR_INVALID_ARG, "%s: state and h must be non-NULL", fn);
     if (!aligned(h, size_of(h_dt)) || !aligned(state, size_of(state_dt)))
       return fail(KDA_ERR_ALIGNMENT, "%s: tensors must be aligned to their element size", fn);
-    if ((int64_t)N * C > kda::gatedrec::kMaxDecodeValues)
-      return fail(KDA_ERR_UNSUPPORTED, "%s: need N*C <= %lld", fn,
-                  (long long)kda::gatedrec::kMaxDecodeValues);
+    if ((int64_t)N * (((int64_t)C + 255) / 256) > kda::gatedrec::kMaxDecodeGroups)
+      return fail(KDA_ERR_UNSUPPORTED, "%s: need N * ceil(C / 256) <= %lld", fn,
+                  (long long)kda::gatedrec::kMaxDecodeGroups);
     const Span sp{state, (size_t)num_slots * C * size_of(state_dt)},
         sh{h, (size_t)N * C * size_of(h_dt)},
         sx{state_indices, state_indices ? (size_t)N * 4 : 0};

@@ -49,22 +49,21 @@ __device__ void copy_empty(const Args& A, int first, int step) {
 }
 
 template <bool BF16, int V, bool GATE, bool GATED, bool NORM>
-__global__ void __launch_bounds__(64 * kWaves) backward_kernel(const Args A) {
+__global__ void __launch_bounds__(64 * kWaves, 4) backward_kernel(const Args A) {
   constexpr int L = kL, W = kWaves, CB = 64 * V, ES = BF16 ? 2 : 4;
-  __shared__ float s_sum[W][CB], s_add[W][CB], s_from[W][CB];     // forwards
-  __shared__ float s_back[W][CB], s_behind[W][CB];                // backwards
-  __shared__ int s_first[W], s_last[W];
+  __shared__ Carry<W, V> s;                // backwards: wave W - 1 comes first
+  __shared__ float s_add[W][CB];           // forwards
+  __shared__ int s_first[W];
   __shared__ uint32_t s_ticket;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const bool chained = A.chain.ticket != nullptr;
-  const int work = chained ? A.tiles * A.blocks : A.blocks;
+  const int work = A.tiles * A.blocks;
   if ((int)blockIdx.x >= work) {
     copy_empty(A, blockIdx.x - work, gridDim.x - work);
     return;
   }
   int id = blockIdx.x;
-  if (chained) {
+  if (A.tiles > 1) {
     if (threadIdx.x == 0)
       s_ticket = __hip_atomic_fetch_add(A.chain.ticket, 1u, __ATOMIC_RELAXED,
                                         __HIP_MEMORY_SCOPE_AGENT) + 1u;
@@ -72,42 +71,41 @@ __global__ void __launch_bounds__(64 * kWaves) backward_kernel(const Args A) {
     id = __builtin_amdgcn_readfirstlane(s_ticket);
     if ((uint32_t)id >= (uint32_t)work) return;
   }
-  const int c = (id % A.blocks) * CB + lane * V;
+  const int k = id / A.blocks, block = id - k * A.blocks;
+  const int tile = A.tiles - 1 - k;
+  const int tile0 = tile * kTile, live = A.q.live();
+  const int c = block * CB + lane * V;
   const bool on = c < A.C;
   const int cc = on ? c : 0;
-  const int live = A.q.live();
-  Params<V, GATE> par;
-  par.load(A.in, cc);
-
-  float carry[V];
+  if (tile0 >= live) {  // behind the last sequence: nothing is waited for from here
+    if (A.part && wave == 0 && on)
 #pragma unroll
-  for (int v = 0; v < V; ++v) carry[v] = 0.0f;
-  const int k_end = chained ? id / A.blocks + 1 : A.tiles;
-  for (int k = chained ? id / A.blocks : 0; k < k_end; ++k) {
-    const int tile = A.tiles - 1 - k;
-    const int tile0 = tile * kTile;
-    if (tile0 >= live) {  // behind the last sequence: nothing is waited for from here
-      if (A.part && wave == 0 && on)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          A.part[((int64_t)tile * 2) * A.C + c + v] = 0.0f;
-          A.part[((int64_t)tile * 2 + 1) * A.C + c + v] = 0.0f;
-        }
-      continue;
-    }
-    const int t0 = tile0 + wave * L;
-    const int count = live - t0 < 0 ? 0 : live - t0 < L ? live - t0 : L;
+      for (int v = 0; v < V; ++v) {
+        A.part[((int64_t)tile * 2) * A.C + c + v] = 0.0f;
+        A.part[((int64_t)tile * 2 + 1) * A.C + c + v] = 0.0f;
+      }
+    return;
+  }
+  const int t0 = tile0 + wave * L;
 
-    Vals<BF16, V> rx[L], rr[L], ri[GATED ? L : 1];
-    float dh[L][V];
+  Vals<BF16, V> rx[L], rr[L], ri[GATED ? L : 1];
+  float dh[L][V];
+  {
+    const int t = t0 < live ? t0 : live - 1, most = live - 1 - t;  // (the last row again)
+    const uint32_t at = cc * ES;
+    const uint32_t sx = A.in.x.stride * ES, sr = A.in.r.stride * ES, si = A.in.i.stride * ES;
+    const __amdgpu_buffer_rsrc_t px = rows_from(A.in.x.p, (int64_t)t * sx),
+                                 pr = rows_from(A.in.r.p, (int64_t)t * sr),
+                                 pi = rows_from(A.in.i.p, (int64_t)t * si);
 #pragma unroll
     for (int j = 0; j < L; ++j) {
-      const int64_t t = t0 + j < live ? t0 + j : live - 1;
-      rr[j].load(static_cast<const char*>(A.in.r.p) + t * A.in.r.stride * ES + (int64_t)cc * ES);
-      if constexpr (GATED)
-        ri[j].load(static_cast<const char*>(A.in.i.p) + t * A.in.i.stride * ES + (int64_t)cc * ES);
-      rx[j].load(static_cast<const char*>(A.in.x.p) + t * A.in.x.stride * ES + (int64_t)cc * ES);
+      const uint32_t row = j < most ? j : most;
+      rr[j].load(pr, at, row * sr);
+      if constexpr (GATED) ri[j].load(pi, at, row * si);
+      rx[j].load(px, at, row * sx);
     }
+    const uint32_t sd = A.C * (A.dh_bf16 ? 2 : 4);
+    const __amdgpu_buffer_rsrc_t pd = rows_from(A.dh, (int64_t)t * sd);
     if (!A.dh) {
 #pragma unroll
       for (int j = 0; j < L; ++j)
@@ -116,9 +114,7 @@ __global__ void __launch_bounds__(64 * kWaves) backward_kernel(const Args A) {
     } else if (A.dh_bf16) {
       Vals<true, V> d[L];
 #pragma unroll
-      for (int j = 0; j < L; ++j)
-        d[j].load(static_cast<const char*>(A.dh) +
-                  ((int64_t)(t0 + j < live ? t0 + j : live - 1) * A.C + cc) * 2);
+      for (int j = 0; j < L; ++j) d[j].load(pd, cc * 2, (j < most ? j : most) * sd);
 #pragma unroll
       for (int j = 0; j < L; ++j)
 #pragma unroll
@@ -126,175 +122,111 @@ __global__ void __launch_bounds__(64 * kWaves) backward_kernel(const Args A) {
     } else {
       Vals<false, V> d[L];
 #pragma unroll
-      for (int j = 0; j < L; ++j)
-        d[j].load(static_cast<const char*>(A.dh) +
-                  ((int64_t)(t0 + j < live ? t0 + j : live - 1) * A.C + cc) * 4);
+      for (int j = 0; j < L; ++j) d[j].load(pd, cc * 4, (j < most ? j : most) * sd);
 #pragma unroll
       for (int j = 0; j < L; ++j)
 #pragma unroll
         for (int v = 0; v < V; ++v) dh[j][v] = d[j].get(v);
     }
-    Borders bd;
-    bd.find(A.q, t0, count);
-    // the state a sequence begins with; the gradient of the one it ends with
-    auto entry = [&](int j, float (&x)[V]) {
+  }
+  float start[V];  // the state before the tile
 #pragma unroll
-      for (int v = 0; v < V; ++v) x[v] = 0.0f;
-      if (A.S0) load_state<V>(A.S0, (int64_t)A.q.find(t0 + j) * A.C + cc, x, false);
-    };
-    auto exit_grad = [&](int j, float (&x)[V]) {
+  for (int v = 0; v < V; ++v) start[v] = A.starts[(int64_t)tile * A.C + cc + v];
+  Params<V, GATE> par;
+  par.load(A.in, cc);
+  Borders bd;
+  bd.find(A.q, t0, live - t0 < L ? live - t0 : L);
+  // x of the sequence of token t0 + j, zeros without x
+  auto of_sequence = [&](const float* p, int j, float (&x)[V]) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) x[v] = 0.0f;
-      if (A.dS) load_state<V>(A.dS, (int64_t)A.q.find(t0 + j) * A.C + cc, x, false);
-    };
+    for (int v = 0; v < V; ++v) x[v] = 0.0f;
+    if (p) load_state<V>(p, (int64_t)A.q.find(t0 + j) * A.C + cc, x, false);
+  };
 
-    float g[L][V], a[L][V], b[L][V], m[NORM ? L : 1][V], si[GATED ? L : 1][V];
-    float sum[V], add[V], back[V];
+  float g[L][V], a[L][V], b[L][V], m[NORM ? L : 1][V], si[GATED ? L : 1][V];
+  float sum[V], add[V], back[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) sum[v] = add[v] = back[v] = 0.0f;
+  for (int v = 0; v < V; ++v) sum[v] = add[v] = back[v] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < L; ++j) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        g[j][v] = par.log2_decay(rr[j].get(v), v);
-        a[j][v] = exp2_fast(g[j][v]);
-        float u = rx[j].get(v);
-        if constexpr (GATED) {
-          si[j][v] = sigmoid_fast(ri[j].get(v));
-          u *= si[j][v];
-        }
-        if constexpr (NORM) {
-          m[j][v] = __builtin_amdgcn_sqrtf(one_minus_square(g[j][v], a[j][v]));
-          u *= m[j][v];
-        }
-        b[j][v] = u;
-        if (j < count) sum[v] += g[j][v];
-      }
-      if (bd.first >> j & 1u) entry(j, add);
-      if (j < count)
-#pragma unroll
-        for (int v = 0; v < V; ++v) add[v] = fmaf(a[j][v], add[v], b[j][v]);
-    }
-#pragma unroll
-    for (int j = L - 1; j >= 0; --j) {
-      if (bd.last >> j & 1u) exit_grad(j, back);
-      if (j < count)
-#pragma unroll
-        for (int v = 0; v < V; ++v) back[v] = a[j][v] * (dh[j][v] + back[v]);
-    }
+  for (int j = 0; j < L; ++j) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      s_sum[wave][lane * V + v] = sum[v];
-      s_add[wave][lane * V + v] = add[v];
-      s_back[wave][lane * V + v] = back[v];
+      g[j][v] = par.log2_decay(rr[j].get(v), v);
+      a[j][v] = exp2_fast(g[j][v]);
+      float u = rx[j].get(v);
+      if constexpr (GATED) {
+        si[j][v] = sigmoid_fast(ri[j].get(v));
+        u *= si[j][v];
+      }
+      if constexpr (NORM) {
+        m[j][v] = __builtin_amdgcn_sqrtf(one_minus_square(g[j][v], a[j][v]));
+        u *= m[j][v];
+      }
+      b[j][v] = u;
+      sum[v] += g[j][v];
     }
-    if (lane == 0) {
-      s_first[wave] = bd.first != 0;
-      s_last[wave] = bd.last != 0;
-    }
-    __syncthreads();
-
-    if (wave == 0) {
-      float code[V][W], all[V], own[V], from[V];
+    if (bd.first >> j & 1u) of_sequence(A.S0, j, add);
 #pragma unroll
-      for (int v = 0; v < V; ++v) all[v] = own[v] = 0.0f;
-      bool cut = false;
+    for (int v = 0; v < V; ++v) add[v] = fmaf(a[j][v], add[v], b[j][v]);
+  }
 #pragma unroll
-      for (int w = W - 1; w >= 0; --w) {
-        const bool cw = s_last[w] != 0;
-        cut |= cw;
+  for (int j = L - 1; j >= 0; --j) {
+    if (bd.last >> j & 1u) of_sequence(A.dS, j, back);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float s = s_sum[w][lane * V + v];
-          code[v][w] = decay_code(s);
-          all[v] += s;
-          const float x = s_back[w][lane * V + v];
-          own[v] = cw ? x : decayed_onto(code[v][w], own[v], x);
-        }
-      }
-      // the tile ends with a sequence: nothing comes from behind
-      bool alone = tile0 + kTile >= live;
-      if (!alone) {
-        Borders end;
-        end.find(A.q, tile0 + kTile - 1, 1);
-        alone = end.last != 0;
-      }
-      float tile_code[V], ends[V];
+    for (int v = 0; v < V; ++v) back[v] = a[j][v] * (dh[j][v] + back[v]);
+  }
+  const int order = W - 1 - wave;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        tile_code[v] = decay_code(all[v]);
-        from[v] = 0.0f;
-        ends[v] = own[v];
-      }
-      if (chained) {
-        const int64_t at = (int64_t)k * A.C + cc;
-        if (on) {
-          if (cut) {
-            publish<V>(A.chain.state + at, own);
-          } else {
-            publish<V>(A.chain.code + at, tile_code);
-            publish<V>(A.chain.add + at, own);
-          }
-        }
-        if (!alone) look_back<V>(A.chain, A.C, k, cc, on, from);
-      } else if (!alone) {
+  for (int v = 0; v < V; ++v) {
+    s.s_sum[order][lane * V + v] = sum[v];
+    s.s_add[order][lane * V + v] = back[v];
+    s_add[wave][lane * V + v] = add[v];
+  }
+  if (lane == 0) {
+    s.s_cut[order] = bd.last != 0;
+    s_first[wave] = bd.first != 0;
+  }
+  __syncthreads();
+  // the tile ends with a sequence: nothing comes from behind
+  const bool alone = tile0 + kTile >= live || (bd.last >> (L - 1) & 1u);  // (wave W - 1 asks)
+  float h[V], e[V], dA[V], db[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) from[v] = carry[v];
-      }
-      if (!cut) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) ends[v] = decayed_onto(tile_code[v], from[v], own[v]);
-        if (chained && on) publish<V>(A.chain.state + (int64_t)k * A.C + cc, ends);
-      }
-#pragma unroll
-      for (int v = 0; v < V; ++v) carry[v] = ends[v];
-#pragma unroll
-      for (int w = W - 1; w >= 0; --w) {
-        const bool cw = s_last[w] != 0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          s_behind[w][lane * V + v] = from[v];
-          const float x = s_back[w][lane * V + v];
-          from[v] = cw ? x : decayed_onto(code[v][w], from[v], x);
-        }
-      }
-      // forwards: the state that every wave begins with
-#pragma unroll
-      for (int v = 0; v < V; ++v) from[v] = A.starts[(int64_t)tile * A.C + cc + v];
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const bool cw = s_first[w] != 0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          s_from[w][lane * V + v] = from[v];
-          const float x = s_add[w][lane * V + v];
-          from[v] = cw ? x : decayed_onto(code[v][w], from[v], x);
-        }
-      }
-    }
-    __syncthreads();
-
-    float h[V], e[V], dA[V], db[V];
+  for (int v = 0; v < V; ++v) {
+    h[v] = start[v];
+    dA[v] = db[v] = 0.0f;
+  }
+  // forwards: the state that the wave begins with
+  for (int w = 0; w < wave; ++w) {
+    const bool cw = s_first[w] != 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      h[v] = s_from[wave][lane * V + v];
-      e[v] = s_behind[wave][lane * V + v];
-      dA[v] = db[v] = 0.0f;
+      const float code = cw ? __uint_as_float(kCut) : decay_code(s.s_sum[W - 1 - w][lane * V + v]);
+      h[v] = decayed_onto(code, h[v], s_add[w][lane * V + v]);
     }
+  }
+  __syncthreads();  // (s_sum becomes the codes)
+  s.run(A.chain, k, A.tiles, block, A.C, cc, on, alone, order);
 #pragma unroll
-    for (int j = 0; j < L; ++j) {  // b becomes the state before the token
-      if (bd.first >> j & 1u) entry(j, h);
+  for (int v = 0; v < V; ++v) e[v] = s.s_from[order][lane * V + v];
+
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float add_j = b[j][v];
-        b[j][v] = h[v];
-        h[v] = fmaf(a[j][v], h[v], add_j);
-      }
+  for (int j = 0; j < L; ++j) {  // b becomes the state before the token
+    if (bd.first >> j & 1u) of_sequence(A.S0, j, h);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float add_j = b[j][v];
+      b[j][v] = h[v];
+      h[v] = fmaf(a[j][v], h[v], add_j);
     }
+  }
+  const uint32_t row = A.C * (A.out.bf16 ? 2 : 4);
+  const __amdgpu_buffer_rsrc_t px = rows_from(A.out.dx, (int64_t)t0 * row),
+                               pr = rows_from(A.out.dr, (int64_t)t0 * row),
+                               pi = rows_from(A.out.di, (int64_t)t0 * row);
 #pragma unroll
-    for (int j = L - 1; j >= 0; --j) {
-      if (j >= count) continue;
-      if (bd.last >> j & 1u) exit_grad(j, e);
+  for (int j = L - 1; j >= 0; --j) {
+    if (t0 + j < live) {
+      if (bd.last >> j & 1u) of_sequence(A.dS, j, e);
       float ox[V], orr[V], oi[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -316,7 +248,8 @@ __global__ void __launch_bounds__(64 * kWaves) backward_kernel(const Args A) {
         }
         const float r = rr[j].get(v);
         if constexpr (GATE) {
-          const float dr = dg * par.neg_a[v] * __builtin_amdgcn_rcpf(1.0f + exp2_fast(-fmaf(r, kLog2e, par.bias2[v])));
+          const float dr = dg * par.neg_a[v] *
+                           __builtin_amdgcn_rcpf(1.0f + exp2_fast(-fmaf(r, kLog2e, par.bias2[v])));
           // (where g is -inf the decay is 0, and dg with it)
           dA[v] = fmaf(dg, fmaxf(g[j][v], -3.0e38f), dA[v]);
           db[v] += dr;
@@ -326,38 +259,42 @@ __global__ void __launch_bounds__(64 * kWaves) backward_kernel(const Args A) {
         }
       }
       if (on) {
-        const int64_t at = (int64_t)(t0 + j) * A.C + c;
-        store_row<V>(A.out.dx, at, ox, A.out.bf16);
-        store_row<V>(A.out.dr, at, orr, A.out.bf16);
-        if constexpr (GATED) store_row<V>(A.out.di, at, oi, A.out.bf16);
+        if (A.out.bf16) {
+          Vals<true, V>::store(px, c * 2, j * row, ox);
+          Vals<true, V>::store(pr, c * 2, j * row, orr);
+          if constexpr (GATED) Vals<true, V>::store(pi, c * 2, j * row, oi);
+        } else {
+          Vals<false, V>::store(px, c * 4, j * row, ox);
+          Vals<false, V>::store(pr, c * 4, j * row, orr);
+          if constexpr (GATED) Vals<false, V>::store(pi, c * 4, j * row, oi);
+        }
         if (A.out.dS0 && (bd.first >> j & 1u))
           store_state<V>(A.out.dS0, (int64_t)A.q.find(t0 + j) * A.C + c, e, false);
       }
     }
-    if constexpr (GATE) {
-      if (A.part) {
-        __syncthreads();  // s_from and s_behind have been read
+  }
+  if constexpr (GATE) {
+    if (A.part) {
+      __syncthreads();  // s_add and s_from have been read
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        s.s_add[wave][lane * V + v] = dA[v];
+        s.s_from[wave][lane * V + v] = db[v];
+      }
+      __syncthreads();
+      if (wave == 0 && on)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          s_from[wave][lane * V + v] = dA[v];
-          s_behind[wave][lane * V + v] = db[v];
-        }
-        __syncthreads();
-        if (wave == 0 && on)
+          float x = 0.0f, y = 0.0f;
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            float x = 0.0f, y = 0.0f;
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-              x += s_from[w][lane * V + v];  // (of log2-decays)
-              y += s_behind[w][lane * V + v];
-            }
-            A.part[((int64_t)tile * 2) * A.C + c + v] = x * kLn2;
-            A.part[((int64_t)tile * 2 + 1) * A.C + c + v] = y;
+          for (int w = 0; w < W; ++w) {
+            x += s.s_add[w][lane * V + v];  // (of log2-decays)
+            y += s.s_from[w][lane * V + v];
           }
-      }
+          A.part[((int64_t)tile * 2) * A.C + c + v] = x * kLn2;
+          A.part[((int64_t)tile * 2 + 1) * A.C + c + v] = y;
+        }
     }
-    if (!chained) __syncthreads();
   }
 }
 
@@ -392,6 +329,10 @@ int64_t tiles_of(int64_t T) { return (T + kTile - 1) / kTile; }
 size_t part_bytes(int64_t T, int64_t C) {
   return ((size_t)tiles_of(T) * 2 * C * sizeof(float) + 255) / 256 * 256;
 }
+size_t carries_bytes(int64_t T, int64_t C, bool has_starts) {
+  const size_t own = chain_bytes(tiles_of(T), C), scan = scan_workspace_bytes(T, C);
+  return has_starts || own > scan ? own : scan;
+}
 size_t own_starts_bytes(int64_t T, int64_t C) { return (starts_bytes(T, C) + 255) / 256 * 256; }
 
 }  // namespace
@@ -400,22 +341,19 @@ bool backward_fits(const Batch& b) {  // 512 threads a workgroup, fewer than 2^3
   return tiles_of(b.T) * ((b.C + 63) / 64) < ((int64_t)1 << 23) - 1024;
 }
 
-// The tiles' carries (the forward's, without starts, use the same place before), the
+// The tiles' carries (the forward's, without starts, have been in the same place before), the
 // parameters' sums, and the states of a call without starts.
 size_t backward_workspace_bytes(int64_t T, int64_t C, bool has_starts) {
-  size_t chain = chain_bytes(tiles_of(T), C);
-  if (!has_starts && scan_workspace_bytes(T, C) > chain) chain = scan_workspace_bytes(T, C);
-  return chain + part_bytes(T, C) + (has_starts ? 0 : own_starts_bytes(T, C));
+  return carries_bytes(T, C, has_starts) + part_bytes(T, C) +
+         (has_starts ? 0 : own_starts_bytes(T, C));
 }
 
 hipError_t launch_backward(const Inputs& in, const Batch& b, const float* S0, const float* starts,
                            const void* dh, bool dh_bf16, const float* dS, const Gradients& out,
                            void* ws, hipStream_t s) {
   char* base = static_cast<char*>(ws);
-  const size_t chain =
-      backward_workspace_bytes(b.T, b.C, true) - part_bytes(b.T, b.C);
-  size_t scan_chain = starts ? 0 : scan_workspace_bytes(b.T, b.C);
-  if (scan_chain < chain) scan_chain = chain;
+  const size_t chain = chain_bytes(tiles_of(b.T), b.C);
+  char* const part = base + carries_bytes(b.T, b.C, starts != nullptr);
   Args A;
   A.in = in;
   A.q = Seqs{b.cu, b.N, b.T, b.N > 0 ? b.T / b.N : 0};
@@ -425,16 +363,15 @@ hipError_t launch_backward(const Inputs& in, const Batch& b, const float* S0, co
   A.dh = dh;
   A.dh_bf16 = dh_bf16;
   A.out = out;
-  A.part = in.A_log && (out.dA_log || out.ddt_bias) ? reinterpret_cast<float*>(base + scan_chain)
-                                                    : nullptr;
+  A.part = in.A_log && (out.dA_log || out.ddt_bias) ? reinterpret_cast<float*>(part) : nullptr;
   A.tiles = (int)tiles_of(b.T);
   A.chain = Chain{};
   if (!starts && b.T > 0) {
-    float* own = reinterpret_cast<float*>(base + scan_chain + part_bytes(b.T, b.C));
+    float* own = reinterpret_cast<float*>(part + part_bytes(b.T, b.C));
     StatePool st;
     st.in = S0;
     st.slots = b.N;
-    if (const hipError_t e = launch_scan(in, b, st, nullptr, false, own, base, scan_chain, s)) return e;
+    if (const hipError_t e = launch_scan(in, b, st, nullptr, false, own, base, s)) return e;
     starts = own;
   }
   A.starts = starts;
@@ -451,7 +388,7 @@ hipError_t launch_backward(const Inputs& in, const Batch& b, const float* S0, co
     for (int n = 0; n < b.N && !empties; ++n) empties = b.cu_host[n + 1] == b.cu_host[n];
   }
   if (!b.cu && b.T > 0) empties = false;
-  const int64_t work = A.chain.ticket ? (int64_t)A.tiles * A.blocks : A.blocks;
+  const int64_t work = (int64_t)A.tiles * A.blocks;
   const int64_t grid = work + (empties ? (b.N < 256 ? b.N : 256) : 0);
   if (grid > 0) {
 #define KDA_GR(BF, V_, G, I, N_) \

@@ -17,40 +17,40 @@ __global__ void __launch_bounds__(256) decode_kernel(
     const Inputs in, int N, int C, void* pool, int64_t num_slots,
     const int32_t* __restrict__ slots, void* __restrict__ h, bool h_bf16) {
   constexpr int ES = BF16 ? 2 : 4;
-  const int64_t per = (C + V - 1) / V;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= per * N) return;
-  const int64_t n = id / per;
-  const int c = (int)(id - n * per) * V;
-  const int64_t slot = slots ? (int64_t)slots[n] : n;
-  const int64_t at = n * C + c;
+  // a workgroup's channels belong to one sequence, so that rows are uniform
+  const int per = (C + 256 * V - 1) / (256 * V);
+  const int n = blockIdx.x / per;
+  const int c = ((blockIdx.x - n * per) * 256 + threadIdx.x) * V;
+  if (c >= C) return;
+  const int64_t slot = slots ? (int64_t)__builtin_amdgcn_readfirstlane(slots[n]) : n;
+  const __amdgpu_buffer_rsrc_t ph = rows_from(h, (int64_t)n * C * (h_bf16 ? 2 : 4));
   float out[V];
   if (slot < 0 || slot >= num_slots) {
 #pragma unroll
     for (int v = 0; v < V; ++v) out[v] = 0.0f;
-    store_row<V>(h, at, out, h_bf16);
-    return;
-  }
-  Vals<BF16, V> rx, rr, ri;
-  Vals<SB, V> st;
-  char* ps = static_cast<char*>(pool) + (slot * C + c) * (SB ? 2 : 4);
-  st.load(ps);
-  rr.load(static_cast<const char*>(in.r.p) + (n * in.r.stride + c) * ES);
-  rx.load(static_cast<const char*>(in.x.p) + (n * in.x.stride + c) * ES);
-  if constexpr (GATED) ri.load(static_cast<const char*>(in.i.p) + (n * in.i.stride + c) * ES);
-  Params<V, GATE> par;
-  par.load(in, c);
+  } else {
+    const __amdgpu_buffer_rsrc_t ps = rows_from(pool, slot * C * (SB ? 2 : 4));
+    Vals<BF16, V> rx, rr, ri;
+    Vals<SB, V> st;
+    st.load(ps, c * (SB ? 2 : 4), 0);
+    rr.load(rows_from(in.r.p, n * in.r.stride * ES), c * ES, 0);
+    rx.load(rows_from(in.x.p, n * in.x.stride * ES), c * ES, 0);
+    if constexpr (GATED) ri.load(rows_from(in.i.p, n * in.i.stride * ES), c * ES, 0);
+    Params<V, GATE> par;
+    par.load(in, c);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const float g = par.log2_decay(rr.get(v), v);
-    const float a = exp2_fast(g);
-    float u = rx.get(v);
-    if constexpr (GATED) u *= sigmoid_fast(ri.get(v));
-    if constexpr (NORM) u *= __builtin_amdgcn_sqrtf(one_minus_square(g, a));
-    out[v] = decayed_onto(decay_code(g), st.get(v), u);
+    for (int v = 0; v < V; ++v) {
+      const float g = par.log2_decay(rr.get(v), v);
+      const float a = exp2_fast(g);
+      float u = rx.get(v);
+      if constexpr (GATED) u *= sigmoid_fast(ri.get(v));
+      if constexpr (NORM) u *= __builtin_amdgcn_sqrtf(one_minus_square(g, a));
+      out[v] = decayed_onto(decay_code(g), st.get(v), u);
+    }
+    Vals<SB, V>::store(ps, c * (SB ? 2 : 4), 0, out);
   }
-  Vals<SB, V>::store(ps, out);
-  store_row<V>(h, at, out, h_bf16);
+  if (h_bf16) Vals<true, V>::store(ph, c * 2, 0, out);
+  else Vals<false, V>::store(ph, c * 4, 0, out);
 }
 
 }  // namespace
@@ -61,7 +61,7 @@ hipError_t launch_decode(const Inputs& in, int N, int C, void* pool, bool state_
   if (N == 0) return hipSuccess;
   const Out outs[] = {{h, h_bf16}, {pool, state_bf16}};
   const int V = width(in, C, outs, 2);
-  const int64_t grid = ((int64_t)N * ((C + V - 1) / V) + 255) / 256;
+  const int64_t grid = (int64_t)N * ((C + 256 * V - 1) / (256 * V));
 #define KDA_GR(BF, SB, V_, G, I, N_)                                                            \
   decode_kernel<BF, SB, V_, G, I, N_><<<(unsigned)grid, 256, 0, s>>>(in, N, C, pool, num_slots, \
                                                                    slots, h, h_bf16)

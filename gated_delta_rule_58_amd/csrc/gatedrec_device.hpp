@@ -9,42 +9,54 @@ namespace kda {
 namespace gatedrec {
 
 // ------------------------------------------------------------------ values
-// V neighbouring channels of one token as they lie in memory.
+// V neighbouring channels of one token as they lie in memory: `rows` is a resource over a
+// tensor from some row on, `row` the bytes to the token (uniform over the wave), `at` those
+// to the lane's channels.  (A 64-bit address a lane and token takes two registers and three
+// instructions, one of them in the vector unit.)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_from(const void* p, int64_t bytes) {
+  return buffer_over(static_cast<const char*>(p) + bytes, 0xffffffffu);
+}
 template <bool BF16, int V>
 struct Vals {
-  typedef uint16_t E __attribute__((ext_vector_type(V)));
-  E r;
-  __device__ __forceinline__ void load(const char* p) { r = *reinterpret_cast<const E*>(p); }
-  __device__ __forceinline__ float get(int v) const { return bf16_bits_to_f32(r[v]); }
-  static __device__ __forceinline__ void store(char* p, const float (&x)[V]) {
-    E o;
-#pragma unroll
-    for (int v = 0; v < V; ++v) o[v] = f32_to_bf16_bits(x[v]);
-    *reinterpret_cast<E*>(p) = o;
+  static constexpr int BYTES = V * (BF16 ? 2 : 4);
+  static_assert(BYTES == 2 || BYTES == 4 || BYTES == 8, "one load");
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  uint32_t w[BYTES == 8 ? 2 : 1];
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rows, uint32_t at, uint32_t row) {
+    if constexpr (BYTES == 2) {
+      w[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rows, at, row, 0);
+    } else if constexpr (BYTES == 4) {
+      w[0] = __builtin_amdgcn_raw_buffer_load_b32(rows, at, row, 0);
+    } else {
+      const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rows, at, row, 0));
+      w[0] = x[0];
+      w[1] = x[1];
+    }
   }
-};
-template <int V>
-struct Vals<false, V> {
-  typedef float E __attribute__((ext_vector_type(V)));
-  E r;
-  __device__ __forceinline__ void load(const char* p) { r = *reinterpret_cast<const E*>(p); }
-  __device__ __forceinline__ float get(int v) const { return r[v]; }
-  static __device__ __forceinline__ void store(char* p, const float (&x)[V]) {
-    E o;
-#pragma unroll
-    for (int v = 0; v < V; ++v) o[v] = x[v];
-    *reinterpret_cast<E*>(p) = o;
+  __device__ __forceinline__ float get(int v) const {
+    if constexpr (BF16) return __uint_as_float(v ? w[0] & 0xffff0000u : w[0] << 16);
+    return __uint_as_float(w[v]);
+  }
+  static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t rows, uint32_t at,
+                                               uint32_t row, const float (&x)[V]) {
+    if constexpr (BYTES == 2) {
+      __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_bits(x[0]), rows, at, row, 0);
+    } else if constexpr (BF16) {
+      typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+      const bf16x2 y = {static_cast<__bf16>(x[0]), static_cast<__bf16>(x[V - 1])};
+      __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, y), rows, at, row, 0);
+    } else if constexpr (BYTES == 4) {
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[0]), rows, at, row, 0);
+    } else {
+      const u32x2 y = {__float_as_uint(x[0]), __float_as_uint(x[V - 1])};
+      __builtin_amdgcn_raw_buffer_store_b64(y, rows, at, row, 0);
+    }
   }
 };
 template <int V>
 __device__ __forceinline__ void load_state(const void* p, int64_t at, float (&x)[V], bool bf16) {
 #pragma unroll
   for (int v = 0; v < V; ++v) x[v] = load1(p, at + v, bf16);
-}
-template <int V>
-__device__ __forceinline__ void store_row(void* p, int64_t at, const float (&x)[V], bool bf16) {
-  if (bf16) Vals<true, V>::store(static_cast<char*>(p) + at * 2, x);
-  else Vals<false, V>::store(static_cast<char*>(p) + at * 4, x);
 }
 // states (and gradients of them) need only their element's alignment
 template <int V>
@@ -150,7 +162,9 @@ struct Params {
 // A stretch's decay 2^s, s the sum of its log2-decays, as one number `code`: beside 1 it is
 // 1 - d with d = 1 - 2^s kept (code = d, sign clear), for 2^s itself would be rounded to
 // 6e-8, which over the stretches of a slow channel adds up to 6e-8 / d of the state.
-// Further away it is 2^s (code = -2^s, sign set).
+// Further away it is 2^s (code = -2^s, sign set), and where that is 0, nothing is left of
+// what comes before, whatever it was.
+constexpr uint32_t kCut = 0x80000000u;
 __device__ __forceinline__ float decay_code(float s) {
   const float e = exp2_fast(s);
   const float d = one_minus_exp2(s, e);
@@ -158,7 +172,7 @@ __device__ __forceinline__ float decay_code(float s) {
 }
 __device__ __forceinline__ float decayed_onto(float code, float h, float add) {
   const float t = fmaf(-code, h, add);
-  return __float_as_int(code) < 0 ? t : t + h;
+  return __float_as_uint(code) == kCut ? add : __float_as_int(code) < 0 ? t : t + h;
 }
 
 // ----------------------------------------------------------- packed batch
@@ -166,15 +180,18 @@ struct Seqs {
   const int32_t* cu;
   int N, T, len;  // len: tokens of every sequence when cu is null
   __device__ __forceinline__ int clamp(int t) const { return t < 0 ? 0 : t > T ? T : t; }
-  __device__ __forceinline__ int start(int n) const { return cu ? clamp(cu[n]) : n * len; }
-  __device__ __forceinline__ int live() const { return cu ? clamp(cu[N]) : T; }
+  // (read through a vector load wherever the compiler sees a store before it: the value is
+  // the same for the whole wave, and what follows from it belongs in scalar registers)
+  __device__ __forceinline__ int at(int n) const { return __builtin_amdgcn_readfirstlane(cu[n]); }
+  __device__ __forceinline__ int start(int n) const { return cu ? clamp(at(n)) : n * len; }
+  __device__ __forceinline__ int live() const { return cu ? clamp(at(N)) : T; }
   // the last sequence that begins at or before t
   __device__ __forceinline__ int find(int t) const {
     if (!cu) return len > 0 ? t / len : 0;
     int lo = 0, hi = N - 1;
     while (lo < hi) {
       const int mid = lo + (hi - lo + 1) / 2;
-      if (cu[mid] <= t) lo = mid;
+      if (at(mid) <= t) lo = mid;
       else hi = mid - 1;
     }
     return lo;
@@ -204,28 +221,33 @@ struct Borders {
 };
 
 // ------------------------------------------------------------------ carries
-// The tiles of a channel hand their state on.  Tile k (in the order of the walk) first
-// publishes its own decay and contribution (code, add), then waits for the state of the
-// tile before it and publishes its own.  A word that is not there yet is all ones; what
-// is published never is.  Nothing else is ordered by these words, so every access is a
-// relaxed one, at agent scope because neighbouring tiles run on different XCDs.
+// The tiles of a channel hand their state on.  Tile k (in the order of the walk) publishes
+// its own decay and contribution (code, add), looks for the nearest tile before it whose
+// state is known, takes what lies between (up to kReach tiles) and publishes its own state.
+// What lies between is folded one by one, forwards: wherever it begins, the bits are the same.
 //
-// Tiles are given out by a ticket, so whoever is waited for is running or done.  A tile
-// folds what lies between it and the nearest state one by one, forwards: whichever tile
-// that is, the bits are the same.
+// Tiles are given out by a ticket, so whoever is waited for is running or done.  A word that
+// is not there yet is all ones; what is published never is, so a word is its own proof
+// of being there, and every access is a relaxed atomic one (at agent scope: neighbouring tiles
+// run on different XCDs).  `mark` only says where to look, one word a tile and block of
+// channels, so that 64 tiles are looked at in one load.
 //
 // Should the words be spoilt (the workspace used by something else meanwhile), a wait
-// gives up after kSpins and the tile goes on with NaN: every wait ends.
+// gives up after kSpins and the tile goes on with NaN: every wait ends.  (A tile that waits
+// holds its place, as does everybody before it: kSpins is about a second.)
 constexpr uint32_t kEmpty = 0xffffffffu;
 constexpr int kSpins = 1 << 20;
-constexpr int kWindow = 64;  // how far back a state is looked for
+constexpr int kReach = 64;
+constexpr int kByOne = 4;  // so many tiles between, one wave folds by itself
 
 struct Chain {
-  uint32_t* ticket;  // null: one workgroup walks all tiles of its channels
+  uint32_t* ticket;
   uint32_t *state, *code, *add;  // [tiles][C]
+  uint32_t* mark;                // [blocks][tiles]: kEmpty, 1 (code and add), 2 (state)
 };
+// (blocks: at most C / 64 rounded up)
 inline size_t chain_bytes(int64_t tiles, int64_t C) {
-  return (256 + (size_t)tiles * C * 12 + 255) / 256 * 256;
+  return (256 + (size_t)tiles * C * 12 + (size_t)tiles * ((C + 63) / 64) * 4 + 255) / 256 * 256;
 }
 // makes every word empty, the ticket too
 hipError_t launch_fill(void* ws, size_t bytes, hipStream_t s);
@@ -235,7 +257,14 @@ inline Chain chain_at(void* ws, int64_t tiles, int64_t C) {
   c.state = c.ticket + 64;
   c.code = c.state + tiles * C;
   c.add = c.code + tiles * C;
+  c.mark = c.add + tiles * C;
   return c;
+}
+__device__ __forceinline__ uint32_t peek(const uint32_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void poke(uint32_t* p, uint32_t x) {
+  __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 template <int V>
@@ -247,13 +276,10 @@ __device__ __forceinline__ void publish(uint32_t* p, const float (&x)[V]) {
     if (w[v] == kEmpty) w[v] = 0x7fc00000u;
   }
   if constexpr (V == 1) {
-    __hip_atomic_store(p, w[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    poke(p, w[0]);
   } else {
-#pragma unroll
-    for (int v = 0; v < V; v += 2)
-      __hip_atomic_store(reinterpret_cast<uint64_t*>(p + v),
-                         (uint64_t)w[v] | (uint64_t)w[v + 1] << 32, __ATOMIC_RELAXED,
-                         __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(reinterpret_cast<uint64_t*>(p), (uint64_t)w[0] | (uint64_t)w[V - 1] << 32,
+                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
 }
 template <int V>
@@ -261,92 +287,175 @@ struct Words {
   uint32_t w[V];
   __device__ __forceinline__ void load(const uint32_t* p) {
     if constexpr (V == 1) {
-      w[0] = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      w[0] = peek(p);
     } else {
-#pragma unroll
-      for (int v = 0; v < V; v += 2) {
-        const uint64_t x = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p + v),
-                                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        w[v] = (uint32_t)x;
-        w[v + 1] = (uint32_t)(x >> 32);
-      }
+      const uint64_t x = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT);
+      w[0] = (uint32_t)x;
+      w[V - 1] = (uint32_t)(x >> 32);
     }
   }
-  // whether every lane's words are there (lanes without channels: `on` false)
-  __device__ __forceinline__ bool ready(bool on) const {
-    bool r = true;
-#pragma unroll
-    for (int v = 0; v < V; ++v) r &= w[v] != kEmpty;
-    return __all(r || !on);
-  }
+  __device__ __forceinline__ bool there() const { return w[0] != kEmpty && w[V - 1] != kEmpty; }
   __device__ __forceinline__ float get(int v) const { return __uint_as_float(w[v]); }
 };
 
-// The state behind tile k - 1 (k > 0) of a wave's channels c.
-template <int V>
-__device__ __forceinline__ void look_back(const Chain& ch, int64_t C, int k, int c, bool on,
-                                          float (&h)[V]) {
-  constexpr int B = 8;
-  int spins = 0, q = -1;
-  Words<V> st;
-  while (q < 0) {  // the nearest state that is there
-    for (int b = k - 1; b >= 0 && b > k - 1 - kWindow && q < 0; b -= B) {
-      Words<V> w[B];
-#pragma unroll
-      for (int j = 0; j < B; ++j) w[j].load(ch.state + (int64_t)(b - j < 0 ? 0 : b - j) * C + c);
-#pragma unroll
-      for (int j = 0; j < B; ++j)
-        if (q < 0 && b - j >= 0 && w[j].ready(on)) {
-          q = b - j;
-          st = w[j];
-        }
+// The nearest tile before k whose state is marked, with everything between marked too: how
+// many tiles lie between it and k (-1: gave up).  One wave; 0 < k.
+__device__ __forceinline__ int nearest_state(const uint32_t* mark, int k) {
+  const int lane = threadIdx.x & 63;
+  for (int spins = 0; spins < kSpins; ++spins) {
+    const uint32_t m = k - 1 - lane >= 0 ? peek(mark + (k - 1 - lane)) : 0u;
+    const uint64_t whole = __ballot(m == 2u), part = __ballot(m == 1u);
+    if (whole) {
+      const int n = __builtin_ctzll(whole);
+      if (n == 0 || (~part & ((1ull << n) - 1)) == 0) return n;
     }
-    if (q < 0) {
-      if (++spins > kSpins) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = __builtin_nanf("");
-        return;
-      }
-      __builtin_amdgcn_s_sleep(1);
-    }
+    __builtin_amdgcn_s_sleep(1);
   }
+  return -1;
+}
+
+// N tiles' words from tile `first` on (those before `end`), all on their way at once; words
+// that are marked may still be on theirs for a moment.
+template <int N, int V>
+__device__ __forceinline__ void fetch_tiles(const Chain& ch, int64_t C, int first, int end, int c,
+                                            bool on, Words<V> (&code)[N], Words<V> (&add)[N]) {
+  for (int spins = 0; spins < kSpins; ++spins) {
+    bool there = true;
 #pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = st.get(v);
-  for (int b = q + 1; b < k; b += B) {
-    Words<V> code[B], add[B];
-#pragma unroll
-    for (int j = 0; j < B; ++j) {
-      const int64_t at = (int64_t)(b + j < k ? b + j : k - 1) * C + c;
+    for (int j = 0; j < N; ++j) {
+      const int64_t at = (int64_t)(first + j < end ? first + j : end - 1) * C + c;
       code[j].load(ch.code + at);
       add[j].load(ch.add + at);
     }
 #pragma unroll
-    for (int j = 0; j < B; ++j) {
-      if (b + j < k) {
-        const int64_t at = (int64_t)(b + j) * C + c;
-        bool whole = false;  // the tile's state came instead
-        while (!(code[j].ready(on) && add[j].ready(on))) {
-          st.load(ch.state + at);
-          if (st.ready(on)) {
-            whole = true;
-            break;
-          }
-          if (++spins > kSpins) {
+    for (int j = 0; j < N; ++j) there = there && code[j].there() && add[j].there();
+    if (__all(there || !on)) return;
+  }
 #pragma unroll
-            for (int v = 0; v < V; ++v) h[v] = __builtin_nanf("");
-            return;
-          }
-          __builtin_amdgcn_s_sleep(1);
-          code[j].load(ch.code + at);
-          add[j].load(ch.add + at);
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int v = 0; v < V; ++v) add[j].w[v] = 0x7fc00000u;
+}
+template <int V>
+__device__ __forceinline__ void fetch_state(const uint32_t* p, bool on, float (&x)[V]) {
+  Words<V> w;
+  for (int spins = 0;; ++spins) {
+    w.load(p);
+    if (__all(w.there() || !on) || spins >= kSpins) break;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) x[v] = w.get(v);  // (an empty word is a NaN)
+}
+
+// What a tile's waves do between their own tokens and those tokens' states.  Every wave has
+// its decay's sum and its contribution in s_sum and s_add, and whether a border lies in it in
+// s_cut; waves count in the order of the walk.  Afterwards s_from holds what every wave
+// begins with and s_sum the waves' decay codes.  All waves come here, `order` is their place;
+// `alone` (asked of the first one): nothing comes from before the tile.
+template <int W, int V>
+struct Carry {
+  static constexpr int CB = 64 * V;
+  float s_sum[W][CB], s_add[W][CB], s_from[W][CB];
+  // of the tiles between (at most kReach - 1; a wave brings kByOne at a time)
+  float s_code[kReach][CB], s_own[kReach][CB];
+  int s_cut[W];
+  int s_between;
+
+  __device__ __forceinline__ void run(const Chain& ch, int k, int tiles, int block, int64_t C, int c,
+                                      bool on, bool alone, int order) {
+    const int lane = threadIdx.x & 63, at = lane * V;
+    const int64_t word = (int64_t)k * C + c;
+    uint32_t* const mark = ch.mark + (int64_t)block * tiles;
+    float own[V], from[V], tile_code[V];  // of wave 0
+    bool cut = false;
+    int n = 0;
+    if (order == 0) {
+      float all[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) own[v] = all[v] = from[v] = 0.0f;
+#pragma unroll 2
+      for (int w = 0; w < W; ++w) {
+        const bool cw = s_cut[w] != 0;
+        cut |= cw;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float s = s_sum[w][at + v];
+          const float code = cw ? __uint_as_float(kCut) : decay_code(s);
+          s_sum[w][at + v] = code;
+          all[v] += s;
+          own[v] = decayed_onto(code, own[v], s_add[w][at + v]);
         }
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) tile_code[v] = cut ? __uint_as_float(kCut) : decay_code(all[v]);
+      if (tiles > 1) {
+        if (on) {
+          if (cut) publish<V>(ch.state + word, own);
+          publish<V>(ch.code + word, tile_code);
+          publish<V>(ch.add + word, own);
+        }
+        __builtin_amdgcn_s_waitcnt(0x0f70);
+        if (lane == 0) poke(mark + k, cut ? 2u : 1u);
+        if (!alone) {
+          n = nearest_state(mark, k);
+          if (n >= 0) fetch_state<V>(ch.state + word - (int64_t)(n + 1) * C, on, from);
+          else from[0] = from[V - 1] = __builtin_nanf("");
+          if (n > 0 && n <= kByOne) {
+            Words<V> code[kByOne], add[kByOne];
+            fetch_tiles<kByOne, V>(ch, C, k - n, k, c, on, code, add);
+#pragma unroll
+            for (int j = 0; j < kByOne; ++j)
+              if (j < n)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                  from[v] = decayed_onto(code[j].get(v), from[v], add[j].get(v));
+            n = 0;
+          }
+        }
+      }
+      if (lane == 0) s_between = n;
+    }
+    __syncthreads();
+    n = __builtin_amdgcn_readfirstlane(s_between);
+    if (n > 0) {  // many tiles between: every wave brings some of them to LDS
+      for (int j0 = order * kByOne; j0 < n; j0 += W * kByOne) {
+        Words<V> code[kByOne], add[kByOne];
+        fetch_tiles<kByOne, V>(ch, C, k - n + j0, k, c, on, code, add);
+#pragma unroll
+        for (int j = 0; j < kByOne; ++j)
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            s_code[j0 + j][at + v] = code[j].get(v);
+            s_own[j0 + j][at + v] = add[j].get(v);
+          }
+      }
+      __syncthreads();
+    }
+    if (order == 0) {
+#pragma unroll 4
+      for (int j = 0; j < n; ++j)
 #pragma unroll
         for (int v = 0; v < V; ++v)
-          h[v] = whole ? st.get(v) : decayed_onto(code[j].get(v), h[v], add[j].get(v));
+          from[v] = decayed_onto(s_code[j][at + v], from[v], s_own[j][at + v]);
+      if (tiles > 1 && !cut) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) own[v] = decayed_onto(tile_code[v], from[v], own[v]);
+        if (on) publish<V>(ch.state + word, own);
+        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt 0: the words are in their place
+        if (lane == 0) poke(mark + k, 2u);
       }
+#pragma unroll 2
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          s_from[w][at + v] = from[v];
+          from[v] = decayed_onto(s_sum[w][at + v], from[v], s_add[w][at + v]);
+        }
     }
+    __syncthreads();
   }
-}
+};
 
 }  // namespace gatedrec
 }  // namespace kda

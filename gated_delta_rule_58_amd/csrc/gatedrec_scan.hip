@@ -36,7 +36,7 @@ struct Args {
 };
 
 __device__ __forceinline__ int64_t slot_of(const StatePool& st, int n) {
-  const int64_t s = st.idx ? (int64_t)st.idx[n] : n;
+  const int64_t s = st.idx ? (int64_t)__builtin_amdgcn_readfirstlane(st.idx[n]) : n;
   return s >= 0 && s < st.slots ? s : -1;
 }
 
@@ -56,21 +56,19 @@ __device__ void copy_empty(const Args& A, int first, int step) {
 }
 
 template <bool BF16, int V, bool GATE, bool GATED, bool NORM>
-__global__ void __launch_bounds__(64 * kWaves) scan_kernel(const Args A) {
+__global__ void __launch_bounds__(64 * kWaves, 4) scan_kernel(const Args A) {
   constexpr int L = kL, W = kWaves, CB = 64 * V, ES = BF16 ? 2 : 4;
-  __shared__ float s_sum[W][CB], s_add[W][CB], s_from[W][CB];
-  __shared__ int s_cut[W];
+  __shared__ Carry<W, V> s;
   __shared__ uint32_t s_ticket;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const bool chained = A.chain.ticket != nullptr;
-  const int work = chained ? A.tiles * A.blocks : A.blocks;
+  const int work = A.tiles * A.blocks;
   if ((int)blockIdx.x >= work) {
     copy_empty(A, blockIdx.x - work, gridDim.x - work);
     return;
   }
   int id = blockIdx.x;
-  if (chained) {
+  if (A.tiles > 1) {
     if (threadIdx.x == 0)
       s_ticket = __hip_atomic_fetch_add(A.chain.ticket, 1u, __ATOMIC_RELAXED,
                                         __HIP_MEMORY_SCOPE_AGENT) + 1u;  // it begins at all ones
@@ -78,160 +76,133 @@ __global__ void __launch_bounds__(64 * kWaves) scan_kernel(const Args A) {
     id = __builtin_amdgcn_readfirstlane(s_ticket);
     if ((uint32_t)id >= (uint32_t)work) return;
   }
-  const int c = (id % A.blocks) * CB + lane * V;
+  const int k = id / A.blocks, block = id - k * A.blocks;
+  const int tile0 = k * kTile, live = A.q.live();
+  if (tile0 >= live) return;
+  const int t0 = tile0 + wave * L;
+  const int c = block * CB + lane * V;
   const bool on = c < A.C;
   const int cc = on ? c : 0;
-  const int live = A.q.live();
+
+  Vals<BF16, V> rx[L], rr[L], ri[GATED ? L : 1];
+  {
+    const int t = t0 < live ? t0 : live - 1, most = live - 1 - t;  // (the last row again)
+    const uint32_t at = cc * ES;
+    const uint32_t sx = A.in.x.stride * ES, sr = A.in.r.stride * ES, si = A.in.i.stride * ES;
+    const __amdgpu_buffer_rsrc_t px = rows_from(A.in.x.p, (int64_t)t * sx),
+                                 pr = rows_from(A.in.r.p, (int64_t)t * sr),
+                                 pi = rows_from(A.in.i.p, (int64_t)t * si);
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      const uint32_t row = j < most ? j : most;
+      rr[j].load(pr, at, row * sr);
+      if constexpr (GATED) ri[j].load(pi, at, row * si);
+      rx[j].load(px, at, row * sx);
+    }
+  }
   Params<V, GATE> par;
   par.load(A.in, cc);
+  Borders bd;
+  bd.find(A.q, t0, live - t0 < L ? live - t0 : L);
 
-  float carry[V];  // of wave 0: the state before the tile, where one workgroup walks them all
-  const int k_end = chained ? id / A.blocks + 1 : A.tiles;
-  for (int k = chained ? id / A.blocks : 0; k < k_end; ++k) {
-    const int tile0 = k * kTile;
-    if (tile0 >= live) return;
-    const int t0 = tile0 + wave * L;
-    const int count = live - t0 < 0 ? 0 : live - t0 < L ? live - t0 : L;
-
-    Vals<BF16, V> rx[L], rr[L], ri[GATED ? L : 1];
+  float a[L][V], b[L][V], sum[V], add[V];
 #pragma unroll
-    for (int j = 0; j < L; ++j) {
-      const int64_t t = t0 + j < live ? t0 + j : live - 1;
-      rr[j].load(static_cast<const char*>(A.in.r.p) + t * A.in.r.stride * ES + (int64_t)cc * ES);
-      if constexpr (GATED)
-        ri[j].load(static_cast<const char*>(A.in.i.p) + t * A.in.i.stride * ES + (int64_t)cc * ES);
-      rx[j].load(static_cast<const char*>(A.in.x.p) + t * A.in.x.stride * ES + (int64_t)cc * ES);
-    }
-    Borders bd;
-    bd.find(A.q, t0, count);
-
-    float a[L][V], b[L][V], sum[V], add[V];
+  for (int v = 0; v < V; ++v) sum[v] = add[v] = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) sum[v] = add[v] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float g = par.log2_decay(rr[j].get(v), v);
-        a[j][v] = exp2_fast(g);
-        float u = rx[j].get(v);
-        if constexpr (GATED) u *= sigmoid_fast(ri[j].get(v));
-        if constexpr (NORM)
-          u *= __builtin_amdgcn_sqrtf(one_minus_square(g, a[j][v]));
-        b[j][v] = u;
-        if (j < count) sum[v] += g;
-      }
-      if (bd.first >> j & 1u) {
-        float s0[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) s0[v] = add[v] = 0.0f;
-        if (A.st.in) {
-          const int64_t s = slot_of(A.st, A.q.find(t0 + j));
-          if (s >= 0) load_state<V>(A.st.in, s * A.C + cc, s0, A.st.bf16);
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) b[j][v] = fmaf(a[j][v], s0[v], b[j][v]);
-      }
-      if (j < count)
-#pragma unroll
-        for (int v = 0; v < V; ++v) add[v] = fmaf(a[j][v], add[v], b[j][v]);
-    }
+  for (int j = 0; j < L; ++j)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      s_sum[wave][lane * V + v] = sum[v];
-      s_add[wave][lane * V + v] = add[v];
+      const float g = par.log2_decay(rr[j].get(v), v);
+      a[j][v] = exp2_fast(g);
+      float u = rx[j].get(v);
+      if constexpr (GATED) u *= sigmoid_fast(ri[j].get(v));
+      if constexpr (NORM) u *= __builtin_amdgcn_sqrtf(one_minus_square(g, a[j][v]));
+      b[j][v] = u;
+      sum[v] += g;
+      add[v] = fmaf(a[j][v], add[v], u);
     }
-    if (lane == 0) s_cut[wave] = bd.first != 0;
-    __syncthreads();
+  // (tokens behind the last sequence are in sum and add too: nothing comes behind them)
+  if (bd.first) {  // entry states become part of b, and add begins there
+    if (A.st.in) {
+      for (uint32_t f = bd.first; f; f &= f - 1) {
+        const int k0 = __builtin_ctz(f);
+        const int64_t slot = slot_of(A.st, A.q.find(t0 + k0));
+        float s0[V] = {};
+        if (slot >= 0) load_state<V>(A.st.in, slot * A.C + cc, s0, A.st.bf16);
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+          if (j == k0)
+#pragma unroll
+            for (int v = 0; v < V; ++v) b[j][v] = fmaf(a[j][v], s0[v], b[j][v]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      if (bd.first >> j & 1u)
+#pragma unroll
+        for (int v = 0; v < V; ++v) add[v] = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) add[v] = fmaf(a[j][v], add[v], b[j][v]);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    s.s_sum[wave][lane * V + v] = sum[v];
+    s.s_add[wave][lane * V + v] = add[v];
+  }
+  if (lane == 0) s.s_cut[wave] = bd.first != 0;
+  __syncthreads();
+  s.run(A.chain, k, A.tiles, block, A.C, cc, on, k == 0 || (bd.first & 1u), wave);
 
-    if (wave == 0) {
-      // the tile's own decay and contribution; behind a border, its state
-      float own[V], code[V][W], all[V];
-      bool cut = false;
+  float h[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) own[v] = all[v] = 0.0f;
+  for (int v = 0; v < V; ++v) h[v] = s.s_from[wave][lane * V + v];
+  if (!on || t0 >= live) return;
+  if (A.starts && t0 % kStartsTokens == 0)
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const bool cw = s_cut[w] != 0;
-        cut |= cw;
+    for (int v = 0; v < V; ++v) A.starts[(int64_t)(t0 / kStartsTokens) * A.C + c + v] = h[v];
+  if (!A.h) return;
+  const uint32_t row = A.C * (A.h_bf16 ? 2 : 4);
+  const __amdgpu_buffer_rsrc_t ph = rows_from(A.h, (int64_t)t0 * row);
+  if (t0 + L <= live && !(bd.first | bd.last)) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float s = s_sum[w][lane * V + v];
-          code[v][w] = decay_code(s);
-          all[v] += s;
-          const float x = s_add[w][lane * V + v];
-          own[v] = cw ? x : decayed_onto(code[v][w], own[v], x);
-        }
-      }
-      const bool alone = k == 0 || (bd.first & 1u);  // the tile begins with a sequence
-      float from[V], ends[V], tile_code[V];
+    for (int j = 0; j < L; ++j)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        tile_code[v] = decay_code(all[v]);
-        from[v] = 0.0f;
-        ends[v] = own[v];
-      }
-      if (chained) {
-        const int64_t at = (int64_t)k * A.C + cc;
-        if (on) {
-          if (cut) {
-            publish<V>(A.chain.state + at, own);
-          } else {
-            publish<V>(A.chain.code + at, tile_code);
-            publish<V>(A.chain.add + at, own);
-          }
-        }
-        if (!alone) look_back<V>(A.chain, A.C, k, cc, on, from);
-      } else if (!alone) {
+      for (int v = 0; v < V; ++v) b[j][v] = h[v] = fmaf(a[j][v], h[v], b[j][v]);
+    if (A.h_bf16) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) from[v] = carry[v];
-      }
-      if (!cut) {
+      for (int j = 0; j < L; ++j) Vals<true, V>::store(ph, c * 2, j * row, b[j]);
+    } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) ends[v] = decayed_onto(tile_code[v], from[v], own[v]);
-        if (chained && on) publish<V>(A.chain.state + (int64_t)k * A.C + cc, ends);
-      }
+      for (int j = 0; j < L; ++j) Vals<false, V>::store(ph, c * 4, j * row, b[j]);
+    }
+  } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) carry[v] = ends[v];
-      // what every wave begins with
+    for (int j = 0; j < L; ++j) {
+      if (t0 + j < live) {
+        if (bd.first >> j & 1u)
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        if (A.starts && on && (w * L) % kStartsTokens == 0 && tile0 + w * L < live)
+          for (int v = 0; v < V; ++v) h[v] = 0.0f;
 #pragma unroll
-          for (int v = 0; v < V; ++v)
-            A.starts[(int64_t)((tile0 + w * L) / kStartsTokens) * A.C + c + v] = from[v];
-        const bool cw = s_cut[w] != 0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          s_from[w][lane * V + v] = from[v];
-          const float x = s_add[w][lane * V + v];
-          from[v] = cw ? x : decayed_onto(code[v][w], from[v], x);
-        }
+        for (int v = 0; v < V; ++v) b[j][v] = h[v] = fmaf(a[j][v], h[v], b[j][v]);
+        if (A.h_bf16) Vals<true, V>::store(ph, c * 2, j * row, h);
+        else Vals<false, V>::store(ph, c * 4, j * row, h);
       }
     }
-    __syncthreads();
-
-    if (A.h) {
-      float h[V];
+    if (A.st.out) {
+      for (uint32_t f = bd.last; f; f &= f - 1) {
+        const int k0 = __builtin_ctz(f);
+        const int64_t slot = slot_of(A.st, A.q.find(t0 + k0));
+        if (slot < 0) continue;
+        float x[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = s_from[wave][lane * V + v];
+        for (int j = 0; j < L; ++j)
+          if (j == k0)
 #pragma unroll
-      for (int j = 0; j < L; ++j) {
-        if (j < count) {
-          if (bd.first >> j & 1u)
-#pragma unroll
-            for (int v = 0; v < V; ++v) h[v] = 0.0f;
-#pragma unroll
-          for (int v = 0; v < V; ++v) h[v] = fmaf(a[j][v], h[v], b[j][v]);
-          if (on) store_row<V>(A.h, (int64_t)(t0 + j) * A.C + c, h, A.h_bf16);
-          if (A.st.out && (bd.last >> j & 1u)) {
-            const int64_t s = slot_of(A.st, A.q.find(t0 + j));
-            if (s >= 0 && on) store_state<V>(A.st.out, s * A.C + c, h, A.st.bf16);
-          }
-        }
+            for (int v = 0; v < V; ++v) x[v] = b[j][v];
+        store_state<V>(A.st.out, slot * A.C + c, x, A.st.bf16);
       }
     }
-    if (!chained) __syncthreads();  // s_sum and s_add are read before they are written again
   }
 }
 
@@ -265,7 +236,7 @@ size_t scan_workspace_bytes(int64_t T, int64_t C) {
 }
 
 hipError_t launch_scan(const Inputs& in, const Batch& b, const StatePool& st, void* h, bool h_bf16,
-                       float* starts, void* ws, size_t ws_bytes, hipStream_t s) {
+                       float* starts, void* ws, hipStream_t s) {
   Args A;
   A.in = in;
   A.q = Seqs{b.cu, b.N, b.T, b.N > 0 ? b.T / b.N : 0};
@@ -276,9 +247,8 @@ hipError_t launch_scan(const Inputs& in, const Batch& b, const StatePool& st, vo
   A.starts = starts;
   A.tiles = (int)tiles_of(b.T);
   A.chain = Chain{};
-  const size_t need = scan_workspace_bytes(b.T, b.C);
-  if (need > 0 && ws && ws_bytes >= need) {
-    if (const hipError_t e = launch_fill(ws, need, s)) return e;
+  if (A.tiles > 1) {
+    if (const hipError_t e = launch_fill(ws, scan_workspace_bytes(b.T, b.C), s)) return e;
     A.chain = chain_at(ws, A.tiles, b.C);
   }
   const Out outs[] = {{h, h_bf16}};
@@ -292,8 +262,7 @@ hipError_t launch_scan(const Inputs& in, const Batch& b, const StatePool& st, vo
     for (int n = 0; n < b.N && !empties; ++n) empties = b.cu_host[n + 1] == b.cu_host[n];
   }
   if (!b.cu && b.T > 0) empties = false;
-  const int64_t work = A.chain.ticket ? (int64_t)A.tiles * A.blocks : A.tiles > 0 ? A.blocks : 0;
-  if (A.tiles == 0) A.blocks = 0;
+  const int64_t work = (int64_t)A.tiles * A.blocks;
   const int64_t grid = work + (empties ? (b.N < 256 ? b.N : 256) : 0);
   if (grid == 0) return hipSuccess;
 #define KDA_GR(BF, V_, G, I, N_) \

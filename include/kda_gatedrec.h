@@ -60,10 +60,9 @@ extern "C" {
  *   starts: NULL, or fp32 [ceil(T_tot / 64), C] (kda_gatedrec_starts_bytes) that the call
  *         fills with states on its way, for kda_gatedrec_scan_backward of the same inputs.
  *         What lies behind the last sequence is left as it was.
- *   workspace: kda_gatedrec_scan_workspace_bytes, 16-byte aligned, what it holds does not
- *         matter.  It is needed to work on the tokens of a channel in many places at once; a
- *         NULL or smaller workspace is allowed (the same bits, with fewer workgroups).  It
- *         must not be used by anything else until the stream has finished this call.
+ *   workspace: kda_gatedrec_scan_workspace_bytes (0 for up to 128 tokens), 16-byte aligned,
+ *         KDA_ERR_WORKSPACE below it; what it holds does not matter.  It must not be used by
+ *         anything else until the stream has finished this call.
  * The same call gives the same bits.
  */
 kda_status kda_gatedrec_scan(const void* x, int64_t x_stride, const void* r, int64_t r_stride,
@@ -75,7 +74,7 @@ kda_status kda_gatedrec_scan(const void* x, int64_t x_stride, const void* r, int
                              int64_t T_tot, int32_t C, void* workspace, size_t workspace_bytes,
                              void* stream);
 
-/* Workspace bytes of kda_gatedrec_scan (0: none is used, or the arguments are unsupported). */
+/* Workspace bytes of kda_gatedrec_scan (0: none is needed, or the arguments are unsupported). */
 size_t kda_gatedrec_scan_workspace_bytes(int64_t T_tot, int32_t C);
 
 /* Bytes of `starts`; 0 for unsupported arguments. */

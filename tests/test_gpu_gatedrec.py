@@ -253,27 +253,28 @@ def test_gradients_against_differences():
             assert abs(got[k].view(-1)[j].item() - num) <= 2e-5 * max(1.0, abs(num)), (k, j)
 
 
-def test_long_sequence_many_tiles():
-    """More tiles than a look back reaches, slow and fast channels; and the same bits where one
-    workgroup walks them all."""
+@pytest.mark.parametrize("C", [6, 65])
+def test_long_sequence_many_tiles(C):
+    """Several times more tiles than a look back reaches, all waiting at once; the same call
+    gives the same bits."""
     need_gpu()
-    say("gatedrec long")
-    T, C = 20000, 6
+    say("gatedrec long", C)
+    T = 33000
     run_scan([T], C, BF, seed=10, slow=True, backward=True)
     x, r, i, A, B, rnd = make(T, C, BF, seed=10, slow=True)
-    X, R, I, A, B = dev(x, r, i, A, B)
-    none = torch.empty(0, dtype=torch.uint8, device=DEV)
+    X, R, I, A, B, DH = dev(x, r, i, A, B, rnd(T, C))
     a = kda.gatedrec_scan(X, R, I, A, B, True, output_starts=True)
-    b = kda.gatedrec_scan(X, R, I, A, B, True, output_starts=True, workspace=none)
-    assert all(torch.equal(p, q) for p, q in zip(a, b))
-    for _ in range(3):
+    g = kda.gatedrec_scan_backward(X, R, I, DH, A, B, True)
+    for _ in range(4):
         assert all(torch.equal(p, q) for p, q in zip(
             a, kda.gatedrec_scan(X, R, I, A, B, True, output_starts=True)))
+        assert all(torch.equal(p, q) for p, q in zip(
+            g, kda.gatedrec_scan_backward(X, R, I, DH, A, B, True)))
 
 
 def test_wide():
-    """The layer's width over many tiles and waves at once, against the walk by one workgroup
-    a channel block (which test_lengths holds to the reference)."""
+    """The layer's width over many tiles and channel blocks at once: a few channels of it alone
+    (which test_channels holds to the reference) give the same bits."""
     need_gpu()
     say("gatedrec wide")
     T, C = 3000, 12288
@@ -285,13 +286,12 @@ def test_wide():
     cu = torch.tensor([0, 1000, 1001, 3000], dtype=torch.int32)
     args = dict(normalize=True, cu_seqlens=cu.to(DEV), cu_seqlens_host=cu)
     a = kda.gatedrec_scan(X, R, I, A, B, output_starts=True, **args)
-    b = kda.gatedrec_scan(X, R, I, A, B, workspace=torch.empty(0, dtype=torch.uint8, device=DEV),
-                          **args)
-    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
-    DH = torch.randn(T, C, generator=gen, device=DEV).to(BF)
-    g = kda.gatedrec_scan_backward(X, R, I, DH, A, B, starts=a[2], **args)
     cols = [0, 63, 64, 127, 128, 5000, 12287]
     take = lambda t: t[:, cols].contiguous()  # noqa: E731
+    b = kda.gatedrec_scan(take(X), take(R), take(I), A[cols], B[cols], output_starts=True, **args)
+    assert all(torch.equal(p[:, cols], q) for p, q in zip(a, b))
+    DH = torch.randn(T, C, generator=gen, device=DEV).to(BF)
+    g = kda.gatedrec_scan_backward(X, R, I, DH, A, B, starts=a[2], **args)
     g2 = kda.gatedrec_scan_backward(take(X), take(R), take(I), take(DH), A[cols], B[cols], **args)
     for p, q in zip(g, g2):
         assert torch.equal(p[..., cols], q)
