@@ -32,7 +32,7 @@ struct Batch {
 };
 
 constexpr int kMaxC = 1 << 20;
-constexpr int kStartsTokens = 64;  // tokens between two states of `starts`
+constexpr int kStartsTokens = 32;  // tokens between two states of `starts`
 
 // Whether the launches of a call hold its work items.
 bool scan_fits(const Batch& b);

@@ -13,16 +13,27 @@
 //
 // The parameters' gradients: every tile's sum goes to memory, a second kernel adds them in
 // a fixed order.
+#include <type_traits>
+
 #include "gatedrec_device.hpp"
 
 namespace kda {
 namespace gatedrec {
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kL = 8;
-constexpr int kTile = kWaves * kL;
-static_assert(kTile == kStartsTokens, "a state for every tile");
+// L tokens a wave, W waves, waves a SIMD, the tiles that a look back reaches.
+template <int V>
+struct Shape {
+  static constexpr int L = 8, W = 8, OCC = 4, REACH = 60, TILE = L * W;
+};
+template <>
+struct Shape<2> {
+  static constexpr int L = 8, W = 4, OCC = 3, REACH = 40, TILE = L * W;
+};
+constexpr int kLeastTile = 32;
+static_assert(Shape<1>::TILE % kStartsTokens == 0 && Shape<2>::TILE % kStartsTokens == 0 &&
+                  Shape<1>::TILE >= kLeastTile && Shape<2>::TILE >= kLeastTile,
+              "a state for every tile");
 
 struct Args {
   Inputs in;
@@ -30,11 +41,11 @@ struct Args {
   int C;
   const float *S0, *starts, *dS;
   const void* dh;
-  bool dh_bf16;
   Gradients out;
   float* part;  // [tiles][2][C]
   Chain chain;
   int tiles, blocks;
+  Split by_blocks;
 };
 
 // The gradient of an entry state without tokens is that of the exit state.
@@ -48,10 +59,13 @@ __device__ void copy_empty(const Args& A, int first, int step) {
   }
 }
 
-template <bool BF16, int V, bool GATE, bool GATED, bool NORM>
-__global__ void __launch_bounds__(64 * kWaves, 4) backward_kernel(const Args A) {
-  constexpr int L = kL, W = kWaves, CB = 64 * V, ES = BF16 ? 2 : 4;
-  __shared__ Carry<W, V> s;                // backwards: wave W - 1 comes first
+template <bool BF16, bool DB, int V, bool GATE, bool GATED, bool NORM>
+__global__ void __launch_bounds__(64 * Shape<V>::W, Shape<V>::OCC)
+    backward_kernel(const Args A) {
+#pragma clang fp contract(off)  // (the same digits on every path: sums of products are spelt out)
+  constexpr int L = Shape<V>::L, W = Shape<V>::W, CB = 64 * V, ES = BF16 ? 2 : 4;
+  constexpr int kTile = Shape<V>::TILE;
+  __shared__ Carry<W, V, Shape<V>::REACH> s;          // backwards: wave W - 1 comes first
   __shared__ float s_add[W][CB];           // forwards
   __shared__ int s_first[W];
   __shared__ uint32_t s_ticket;
@@ -71,7 +85,8 @@ __global__ void __launch_bounds__(64 * kWaves, 4) backward_kernel(const Args A) 
     id = __builtin_amdgcn_readfirstlane(s_ticket);
     if ((uint32_t)id >= (uint32_t)work) return;
   }
-  const int k = id / A.blocks, block = id - k * A.blocks;
+  int block;
+  const int k = A.by_blocks(id, block);
   const int tile = A.tiles - 1 - k;
   const int tile0 = tile * kTile, live = A.q.live();
   const int c = block * CB + lane * V;
@@ -89,14 +104,18 @@ __global__ void __launch_bounds__(64 * kWaves, 4) backward_kernel(const Args A) 
   const int t0 = tile0 + wave * L;
 
   Vals<BF16, V> rx[L], rr[L], ri[GATED ? L : 1];
-  float dh[L][V];
+  Vals<DB, V> rd[L];
   {
     const int t = t0 < live ? t0 : live - 1, most = live - 1 - t;  // (the last row again)
-    const uint32_t at = cc * ES;
-    const uint32_t sx = A.in.x.stride * ES, sr = A.in.r.stride * ES, si = A.in.i.stride * ES;
+    const uint32_t at = cc * ES, DS = DB ? 2 : 4;
+    const uint32_t sx = A.in.x.stride * ES, sr = A.in.r.stride * ES, si = A.in.i.stride * ES,
+                   sd = A.C * DS;
     const __amdgpu_buffer_rsrc_t px = rows_from(A.in.x.p, (int64_t)t * sx),
                                  pr = rows_from(A.in.r.p, (int64_t)t * sr),
-                                 pi = rows_from(A.in.i.p, (int64_t)t * si);
+                                 pi = rows_from(A.in.i.p, (int64_t)t * si),
+                                 // (without dh its loads give 0)
+                                 pd = buffer_over(static_cast<const char*>(A.dh) + (int64_t)t * sd,
+                                                  A.dh ? 0xffffffffu : 0u);
 #pragma unroll
     for (int j = 0; j < L; ++j) {
       const uint32_t row = j < most ? j : most;
@@ -104,34 +123,13 @@ __global__ void __launch_bounds__(64 * kWaves, 4) backward_kernel(const Args A) 
       if constexpr (GATED) ri[j].load(pi, at, row * si);
       rx[j].load(px, at, row * sx);
     }
-    const uint32_t sd = A.C * (A.dh_bf16 ? 2 : 4);
-    const __amdgpu_buffer_rsrc_t pd = rows_from(A.dh, (int64_t)t * sd);
-    if (!A.dh) {
 #pragma unroll
-      for (int j = 0; j < L; ++j)
-#pragma unroll
-        for (int v = 0; v < V; ++v) dh[j][v] = 0.0f;
-    } else if (A.dh_bf16) {
-      Vals<true, V> d[L];
-#pragma unroll
-      for (int j = 0; j < L; ++j) d[j].load(pd, cc * 2, (j < most ? j : most) * sd);
-#pragma unroll
-      for (int j = 0; j < L; ++j)
-#pragma unroll
-        for (int v = 0; v < V; ++v) dh[j][v] = d[j].get(v);
-    } else {
-      Vals<false, V> d[L];
-#pragma unroll
-      for (int j = 0; j < L; ++j) d[j].load(pd, cc * 4, (j < most ? j : most) * sd);
-#pragma unroll
-      for (int j = 0; j < L; ++j)
-#pragma unroll
-        for (int v = 0; v < V; ++v) dh[j][v] = d[j].get(v);
-    }
+    for (int j = 0; j < L; ++j) rd[j].load(pd, cc * DS, (j < most ? j : most) * sd);
   }
+  auto dh = [&](int j, int v) { return rd[j].get(v); };
   float start[V];  // the state before the tile
 #pragma unroll
-  for (int v = 0; v < V; ++v) start[v] = A.starts[(int64_t)tile * A.C + cc + v];
+  for (int v = 0; v < V; ++v) start[v] = A.starts[(int64_t)(tile0 / kStartsTokens) * A.C + cc + v];
   Params<V, GATE> par;
   par.load(A.in, cc);
   Borders bd;
@@ -143,143 +141,201 @@ __global__ void __launch_bounds__(64 * kWaves, 4) backward_kernel(const Args A) 
     if (p) load_state<V>(p, (int64_t)A.q.find(t0 + j) * A.C + cc, x, false);
   };
 
-  float g[L][V], a[L][V], b[L][V], m[NORM ? L : 1][V], si[GATED ? L : 1][V];
-  float sum[V], add[V], back[V];
+  // First every token's g, p = m s and s, the wave's decay, what it adds to the state, and e
+  // before it from what comes in: with P_t the decay from the wave's first token to t,
+  // back = sum_t P_t dh_t.  (a is formed again below: 16 registers for two cycles a value.)
+  float g[L][V], px[L][V], pi[L][V];
+  float sum[V], add[V], back[V], P[V];
+  auto chain = [&](int j, bool first, bool last, bool in) {
+#pragma clang fp contract(off)
+    float dS[V] = {};
+    if (first) of_sequence(A.S0, j, add);
+    if (last) of_sequence(A.dS, j, dS);
 #pragma unroll
-  for (int v = 0; v < V; ++v) sum[v] = add[v] = back[v] = 0.0f;
+    for (int v = 0; v < V; ++v) {
+      const float a = exp2_fast(g[j][v]);
+      add[v] = fmaf(a, add[v], px[j][v] * rx[j].get(v));
+      P[v] *= a;
+      if (in) back[v] = fmaf(P[v], dh(j, v) + dS[v], back[v]);
+    }
+  };
+#pragma unroll
+  for (int v = 0; v < V; ++v) sum[v] = add[v] = back[v] = 0.0f, P[v] = 1.0f;
 #pragma unroll
   for (int j = 0; j < L; ++j) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       g[j][v] = par.log2_decay(rr[j].get(v), v);
-      a[j][v] = exp2_fast(g[j][v]);
-      float u = rx[j].get(v);
-      if constexpr (GATED) {
-        si[j][v] = sigmoid_fast(ri[j].get(v));
-        u *= si[j][v];
-      }
-      if constexpr (NORM) {
-        m[j][v] = __builtin_amdgcn_sqrtf(one_minus_square(g[j][v], a[j][v]));
-        u *= m[j][v];
-      }
-      b[j][v] = u;
+      px[j][v] = pi[j][v] = 1.0f;
+      if constexpr (GATED) px[j][v] = pi[j][v] = sigmoid_fast(ri[j].get(v));
+      if constexpr (NORM)
+        px[j][v] *= __builtin_amdgcn_sqrtf(one_minus_square(g[j][v], exp2_fast(g[j][v])));
       sum[v] += g[j][v];
     }
-    if (bd.first >> j & 1u) of_sequence(A.S0, j, add);
-#pragma unroll
-    for (int v = 0; v < V; ++v) add[v] = fmaf(a[j][v], add[v], b[j][v]);
+    chain(j, false, false, true);
   }
+  // What is formed again is formed again: kept from before, it would not fit the registers.
+  auto again = [&] {
 #pragma unroll
-  for (int j = L - 1; j >= 0; --j) {
-    if (bd.last >> j & 1u) of_sequence(A.dS, j, back);
+    for (int j = 0; j < L; ++j) {
+      hold(rx[j].w[0]);
+      hold(rr[j].w[0]);
+      hold(rd[j].w[0]);
 #pragma unroll
-    for (int v = 0; v < V; ++v) back[v] = a[j][v] * (dh[j][v] + back[v]);
+      for (int v = 0; v < V; ++v) hold(g[j][v]);
+    }
+  };
+  if (bd.first | bd.last) {
+    again();
+#pragma unroll
+    for (int v = 0; v < V; ++v) add[v] = back[v] = 0.0f, P[v] = 1.0f;
+#pragma unroll
+    for (int j = 0; j < L; ++j)  // (back: up to the first border)
+      chain(j, bd.first >> j & 1u, bd.last >> j & 1u, !(bd.last & ((1u << j) - 1)));
   }
   const int order = W - 1 - wave;
+  float code[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    s.s_sum[order][lane * V + v] = sum[v];
-    s.s_add[order][lane * V + v] = back[v];
+    code[v] = decay_code(sum[v]);
     s_add[wave][lane * V + v] = add[v];
   }
-  if (lane == 0) {
-    s.s_cut[order] = bd.last != 0;
-    s_first[wave] = bd.first != 0;
-  }
+  if (lane == 0) s_first[wave] = bd.first != 0;
+  s.set(order, sum, code, back, bd.last != 0);
   __syncthreads();
-  // the tile ends with a sequence: nothing comes from behind
-  const bool alone = tile0 + kTile >= live || (bd.last >> (L - 1) & 1u);  // (wave W - 1 asks)
-  float h[V], e[V], dA[V], db[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    h[v] = start[v];
-    dA[v] = db[v] = 0.0f;
-  }
+  again();
   // forwards: the state that the wave begins with
+  float h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = start[v];
   for (int w = 0; w < wave; ++w) {
     const bool cw = s_first[w] != 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float code = cw ? __uint_as_float(kCut) : decay_code(s.s_sum[W - 1 - w][lane * V + v]);
-      h[v] = decayed_onto(code, h[v], s_add[w][lane * V + v]);
+      h[v] = decayed_onto(cw ? __uint_as_float(kCut) : s.s_code[W - 1 - w][lane * V + v], h[v],
+                          s_add[w][lane * V + v]);
     }
   }
-  __syncthreads();  // (s_sum becomes the codes)
-  s.run(A.chain, k, A.tiles, block, A.C, cc, on, alone, order);
+  // Then everything that R is multiplied with, before R is known: dx = px R, di = pi R,
+  // dr = pr R, with a in the place of g.  The parameters' sums too: R_t is the sum of what comes
+  // in at s >= t (dh_s, or e behind the wave) times the decay between, so with pg = q g
+  //   sum_t R_t pg_t = sum_s dh_s Q_s + e Q_L,   Q_s = a_s Q_{s-1} + pg_s
+  // which needs no register a token and goes forwards.
+  float (&a)[L][V] = g, pr[L][V];
+  float dA[V], db[V], QA[V], Qb[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) e[v] = s.s_from[order][lane * V + v];
+  for (int v = 0; v < V; ++v) dA[v] = db[v] = QA[v] = Qb[v] = 0.0f;
+  auto products = [&](auto borders) {
+#pragma clang fp contract(off)
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      float dS[V] = {};
+      if constexpr (borders) {
+        if (bd.first >> j & 1u) {
+          of_sequence(A.S0, j, h);
+#pragma unroll
+          for (int v = 0; v < V; ++v) QA[v] = Qb[v] = 0.0f;
+        }
+        if (bd.last >> j & 1u) of_sequence(A.dS, j, dS);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float x = rx[j].get(v), r = rr[j].get(v);
+        const float gg = g[j][v], aa = exp2_fast(gg), s = pi[j][v], p = px[j][v];
+        float u = x, before = h[v];
+        if constexpr (GATED) u *= s;
+        if constexpr (NORM) {  // u / m = s u / p
+          float slope = __builtin_amdgcn_rcpf(p) * u;
+          if constexpr (GATED) slope *= s;
+          before = fmaf(-aa, p > 0.0f ? slope : 0.0f, before);
+        }
+        const float q = aa * before;
+        h[v] = fmaf(aa, h[v], p * x);
+        pi[j][v] = p * (x - u);  // of x (1 - s)
+        a[j][v] = aa;
+        if constexpr (GATE) {
+          // (where g is -inf the decay is 0, and q with it)
+          const float pg = q * fmaxf(gg, -3.0e38f);
+          pr[j][v] = q * par.neg_a[v] *
+                     __builtin_amdgcn_rcpf(1.0f + exp2_fast(-fmaf(r, kLog2e, par.bias2[v])));
+          const float in = dh(j, v) + dS[v];
+          if (!borders || t0 + j < live) {
+            QA[v] = fmaf(aa, QA[v], pg);
+            Qb[v] = fmaf(aa, Qb[v], pr[j][v]);
+            dA[v] = fmaf(in, QA[v], dA[v]);
+            db[v] = fmaf(in, Qb[v], db[v]);
+          }
+        } else {
+          pr[j][v] = r > 0.0f ? 0.0f : q;
+        }
+      }
+    }
+  };
+  const bool plain = t0 + L <= live && !(bd.first | bd.last);
+  if (plain) products(std::false_type{});
+  else products(std::true_type{});
+  // the tile ends with a sequence: nothing comes from behind (wave W - 1 asks)
+  const bool alone = tile0 + kTile >= live || (bd.last >> (L - 1) & 1u);
+  s.run(A.chain, k, A.tiles, block, A.C, cc, on, alone, order);
 
 #pragma unroll
-  for (int j = 0; j < L; ++j) {  // b becomes the state before the token
-    if (bd.first >> j & 1u) of_sequence(A.S0, j, h);
+  for (int j = 0; j < L; ++j) hold(rd[j].w[0]);
+  float e[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float add_j = b[j][v];
-      b[j][v] = h[v];
-      h[v] = fmaf(a[j][v], h[v], add_j);
+  for (int v = 0; v < V; ++v) {
+    e[v] = s.from(order, v);
+    if (t0 + L <= live && !(bd.last >> (L - 1) & 1u)) {  // (not of another sequence)
+      dA[v] = fmaf(e[v], QA[v], dA[v]);
+      db[v] = fmaf(e[v], Qb[v], db[v]);
     }
   }
   const uint32_t row = A.C * (A.out.bf16 ? 2 : 4);
-  const __amdgpu_buffer_rsrc_t px = rows_from(A.out.dx, (int64_t)t0 * row),
-                               pr = rows_from(A.out.dr, (int64_t)t0 * row),
-                               pi = rows_from(A.out.di, (int64_t)t0 * row);
+  const __amdgpu_buffer_rsrc_t ox = rows_from(A.out.dx, (int64_t)t0 * row),
+                               orr = rows_from(A.out.dr, (int64_t)t0 * row),
+                               oi = rows_from(A.out.di, (int64_t)t0 * row);
+  auto gradients = [&](auto borders, auto bf) {
+#pragma clang fp contract(off)
+    constexpr bool OB = bf;
+    constexpr int OS = OB ? 2 : 4;
 #pragma unroll
-  for (int j = L - 1; j >= 0; --j) {
-    if (t0 + j < live) {
-      if (bd.last >> j & 1u) of_sequence(A.dS, j, e);
-      float ox[V], orr[V], oi[V];
+    for (int j = L - 1; j >= 0; --j) {
+      if constexpr (borders) {
+        if (t0 + j >= live) continue;
+        if (bd.last >> j & 1u) of_sequence(A.dS, j, e);
+      }
+      float dx[V], dr[V], di[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float R = dh[j][v] + e[v];
+        const float R = dh(j, v) + e[v];
         e[v] = a[j][v] * R;
-        const float x = rx[j].get(v);
-        float u = x, du = R;
-        if constexpr (GATED) u *= si[j][v];
-        float dg = e[v] * b[j][v];
-        if constexpr (NORM) {
-          du *= m[j][v];
-          const float f = a[j][v] * a[j][v] * __builtin_amdgcn_rcpf(m[j][v]) * u * R;
-          dg -= m[j][v] > 0.0f ? f : 0.0f;
-        }
-        ox[v] = du;
-        if constexpr (GATED) {
-          ox[v] *= si[j][v];
-          oi[v] = ox[v] * x * (1.0f - si[j][v]);
-        }
-        const float r = rr[j].get(v);
-        if constexpr (GATE) {
-          const float dr = dg * par.neg_a[v] *
-                           __builtin_amdgcn_rcpf(1.0f + exp2_fast(-fmaf(r, kLog2e, par.bias2[v])));
-          // (where g is -inf the decay is 0, and dg with it)
-          dA[v] = fmaf(dg, fmaxf(g[j][v], -3.0e38f), dA[v]);
-          db[v] += dr;
-          orr[v] = dr;
-        } else {
-          orr[v] = r > 0.0f ? 0.0f : dg;
-        }
+        dx[v] = px[j][v] * R;
+        dr[v] = pr[j][v] * R;
+        if constexpr (GATED) di[v] = pi[j][v] * R;
       }
       if (on) {
-        if (A.out.bf16) {
-          Vals<true, V>::store(px, c * 2, j * row, ox);
-          Vals<true, V>::store(pr, c * 2, j * row, orr);
-          if constexpr (GATED) Vals<true, V>::store(pi, c * 2, j * row, oi);
-        } else {
-          Vals<false, V>::store(px, c * 4, j * row, ox);
-          Vals<false, V>::store(pr, c * 4, j * row, orr);
-          if constexpr (GATED) Vals<false, V>::store(pi, c * 4, j * row, oi);
-        }
-        if (A.out.dS0 && (bd.first >> j & 1u))
-          store_state<V>(A.out.dS0, (int64_t)A.q.find(t0 + j) * A.C + c, e, false);
+        Vals<OB, V>::store(ox, c * OS, j * row, dx);
+        Vals<OB, V>::store(orr, c * OS, j * row, dr);
+        if constexpr (GATED) Vals<OB, V>::store(oi, c * OS, j * row, di);
+        if constexpr (borders)
+          if (A.out.dS0 && (bd.first >> j & 1u))
+            store_state<V>(A.out.dS0, (int64_t)A.q.find(t0 + j) * A.C + c, e, false);
       }
     }
+  };
+  if (A.out.bf16) {
+    if (plain) gradients(std::false_type{}, std::true_type{});
+    else gradients(std::true_type{}, std::true_type{});
+  } else {
+    if (plain) gradients(std::false_type{}, std::false_type{});
+    else gradients(std::true_type{}, std::false_type{});
   }
   if constexpr (GATE) {
     if (A.part) {
-      __syncthreads();  // s_add and s_from have been read
+      __syncthreads();  // what is there has been read
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         s.s_add[wave][lane * V + v] = dA[v];
-        s.s_from[wave][lane * V + v] = db[v];
+        s.s_code[wave][lane * V + v] = db[v];
       }
       __syncthreads();
       if (wave == 0 && on)
@@ -289,7 +345,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) backward_kernel(const Args A) 
 #pragma unroll
           for (int w = 0; w < W; ++w) {
             x += s.s_add[w][lane * V + v];  // (of log2-decays)
-            y += s.s_from[w][lane * V + v];
+            y += s.s_code[w][lane * V + v];
           }
           A.part[((int64_t)tile * 2) * A.C + c + v] = x * kLn2;
           A.part[((int64_t)tile * 2 + 1) * A.C + c + v] = y;
@@ -325,7 +381,7 @@ __global__ void __launch_bounds__(1024) partials_kernel(const float* __restrict_
   }
 }
 
-int64_t tiles_of(int64_t T) { return (T + kTile - 1) / kTile; }
+int64_t tiles_of(int64_t T, int tile = kLeastTile) { return (T + tile - 1) / tile; }
 size_t part_bytes(int64_t T, int64_t C) {
   return ((size_t)tiles_of(T) * 2 * C * sizeof(float) + 255) / 256 * 256;
 }
@@ -352,7 +408,6 @@ hipError_t launch_backward(const Inputs& in, const Batch& b, const float* S0, co
                            const void* dh, bool dh_bf16, const float* dS, const Gradients& out,
                            void* ws, hipStream_t s) {
   char* base = static_cast<char*>(ws);
-  const size_t chain = chain_bytes(tiles_of(b.T), b.C);
   char* const part = base + carries_bytes(b.T, b.C, starts != nullptr);
   Args A;
   A.in = in;
@@ -361,10 +416,11 @@ hipError_t launch_backward(const Inputs& in, const Batch& b, const float* S0, co
   A.S0 = S0;
   A.dS = dS;
   A.dh = dh;
-  A.dh_bf16 = dh_bf16;
   A.out = out;
   A.part = in.A_log && (out.dA_log || out.ddt_bias) ? reinterpret_cast<float*>(part) : nullptr;
-  A.tiles = (int)tiles_of(b.T);
+  const Out outs[] = {{dh, dh_bf16}, {out.dx, out.bf16}, {out.dr, out.bf16}, {out.di, out.bf16}};
+  const int V = width(in, b.C, outs, 4);
+  A.tiles = (int)tiles_of(b.T, V == 2 ? Shape<2>::TILE : Shape<1>::TILE);
   A.chain = Chain{};
   if (!starts && b.T > 0) {
     float* own = reinterpret_cast<float*>(part + part_bytes(b.T, b.C));
@@ -376,12 +432,11 @@ hipError_t launch_backward(const Inputs& in, const Batch& b, const float* S0, co
   }
   A.starts = starts;
   if (A.tiles > 1) {
-    if (const hipError_t e = launch_fill(base, chain, s)) return e;
+    if (const hipError_t e = launch_fill(base, chain_bytes(A.tiles, b.C), s)) return e;
     A.chain = chain_at(base, A.tiles, b.C);
   }
-  const Out outs[] = {{dh, dh_bf16}, {out.dx, out.bf16}, {out.dr, out.bf16}, {out.di, out.bf16}};
-  const int V = width(in, b.C, outs, 4);
-  A.blocks = A.tiles > 0 ? (b.C + 64 * V - 1) / (64 * V) : 0;
+  A.blocks = (b.C + 64 * V - 1) / (64 * V);
+  A.by_blocks = Split(A.blocks);
   bool empties = out.dS0 != nullptr;
   if (empties && b.cu_host) {
     empties = false;
@@ -391,8 +446,11 @@ hipError_t launch_backward(const Inputs& in, const Batch& b, const float* S0, co
   const int64_t work = (int64_t)A.tiles * A.blocks;
   const int64_t grid = work + (empties ? (b.N < 256 ? b.N : 256) : 0);
   if (grid > 0) {
-#define KDA_GR(BF, V_, G, I, N_) \
-  backward_kernel<BF, V_, G, I, N_><<<(unsigned)grid, 64 * kWaves, 0, s>>>(A)
+#define KDA_GR(BF, V_, G, I, N_)                                                              \
+  do {                                                                                        \
+    if (dh_bf16) backward_kernel<BF, true, V_, G, I, N_><<<(unsigned)grid, 64 * Shape<V_>::W, 0, s>>>(A); \
+    else backward_kernel<BF, false, V_, G, I, N_><<<(unsigned)grid, 64 * Shape<V_>::W, 0, s>>>(A);  \
+  } while (0)
 #define KDA_GR_N(BF, V_, G, I)                 \
   do {                                         \
     if (in.normalize) KDA_GR(BF, V_, G, I, true); \

@@ -136,7 +136,7 @@ struct Params {
     if constexpr (GATE) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        neg_a[v] = -expf(in.A_log[c + v]);
+        neg_a[v] = -exp2_fast(in.A_log[c + v] * kLog2e);
         neg_a2[v] = neg_a[v] * kLog2e;
         bias2[v] = in.dt_bias ? in.dt_bias[c + v] * kLog2e : 0.0f;
       }
@@ -197,8 +197,27 @@ struct Seqs {
     return lo;
   }
 };
+// id / blocks and the rest, by a reciprocal that the host has formed: the division of two
+// numbers in scalar registers goes through the vector unit.
+struct Split {
+  uint32_t n = 1, inverse = 0;  // inverse: floor(2^32 / n), 0 for 1
+  Split() = default;
+  explicit Split(uint32_t d) : n(d), inverse(d > 1 ? (uint32_t)(((uint64_t)1 << 32) / d) : 0) {}
+  __device__ __forceinline__ int operator()(int id, int& rest) const {
+    uint32_t q = inverse ? __umulhi((uint32_t)id, inverse) : (uint32_t)id;  // 0 to 1 too small
+    uint32_t r = (uint32_t)id - q * n;
+    if (r >= n) {
+      ++q;
+      r -= n;
+    }
+    rest = (int)r;
+    return (int)q;
+  }
+};
+
 // The borders among the `count` (at most 32) tokens from t0: bit j of `first` (`last`) says
 // that token t0 + j is the first (last) of its sequence.
+// Without one (nearly always) a wave takes straight code that asks for none.
 struct Borders {
   uint32_t first = 0, last = 0;
   __device__ __forceinline__ void find(const Seqs& q, int t0, int count) {
@@ -228,8 +247,8 @@ struct Borders {
 //
 // Tiles are given out by a ticket, so whoever is waited for is running or done.  A word that
 // is not there yet is all ones; what is published never is, so a word is its own proof
-// of being there, and every access is a relaxed atomic one (at agent scope: neighbouring tiles
-// run on different XCDs).  `mark` only says where to look, one word a tile and block of
+// of being there and nothing hangs on the order of accesses; they bypass what an XCD has to
+// itself, for neighbouring tiles run on different ones.  `mark` only says where to look, one word a tile and block of
 // channels, so that 64 tiles are looked at in one load.
 //
 // Should the words be spoilt (the workspace used by something else meanwhile), a wait
@@ -237,8 +256,7 @@ struct Borders {
 // holds its place, as does everybody before it: kSpins is about a second.)
 constexpr uint32_t kEmpty = 0xffffffffu;
 constexpr int kSpins = 1 << 20;
-constexpr int kReach = 64;
-constexpr int kByOne = 4;  // so many tiles between, one wave folds by itself
+constexpr int kByOne = 4;  // so many tiles one wave looks at in one go
 
 struct Chain {
   uint32_t* ticket;
@@ -267,105 +285,163 @@ __device__ __forceinline__ void poke(uint32_t* p, uint32_t x) {
   __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// V words of a lane's channels: `rows` over some tile's row of an array on, `row` the bytes to
+// the tile's, `at` those to the channels.  Coherent like an atomic access at agent scope.
+constexpr int kAgent = 16;  // buffer access cache policy: sc1
 template <int V>
-__device__ __forceinline__ void publish(uint32_t* p, const float (&x)[V]) {
+__device__ __forceinline__ void publish(__amdgpu_buffer_rsrc_t rows, uint32_t at, const float (&x)[V]) {
   uint32_t w[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     w[v] = __float_as_uint(x[v]);
     if (w[v] == kEmpty) w[v] = 0x7fc00000u;
   }
-  if constexpr (V == 1) {
-    poke(p, w[0]);
-  } else {
-    __hip_atomic_store(reinterpret_cast<uint64_t*>(p), (uint64_t)w[0] | (uint64_t)w[V - 1] << 32,
-                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  if constexpr (V == 1)
+    __builtin_amdgcn_raw_buffer_store_b32(w[0], rows, at, 0, kAgent);
+  else
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{w[0], w[V - 1]}, rows, at, 0, kAgent);
 }
 template <int V>
 struct Words {
   uint32_t w[V];
-  __device__ __forceinline__ void load(const uint32_t* p) {
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rows, uint32_t at, uint32_t row) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
     if constexpr (V == 1) {
-      w[0] = peek(p);
+      w[0] = __builtin_amdgcn_raw_buffer_load_b32(rows, at, row, kAgent);
     } else {
-      const uint64_t x = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
-                                           __HIP_MEMORY_SCOPE_AGENT);
-      w[0] = (uint32_t)x;
-      w[V - 1] = (uint32_t)(x >> 32);
+      const u32x2 x =
+          __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rows, at, row, kAgent));
+      w[0] = x[0];
+      w[V - 1] = x[1];
     }
   }
   __device__ __forceinline__ bool there() const { return w[0] != kEmpty && w[V - 1] != kEmpty; }
   __device__ __forceinline__ float get(int v) const { return __uint_as_float(w[v]); }
 };
 
-// The nearest tile before k whose state is marked, with everything between marked too: how
-// many tiles lie between it and k (-1: gave up).  One wave; 0 < k.
-__device__ __forceinline__ int nearest_state(const uint32_t* mark, int k) {
+// The nearest of the REACH tiles before k whose state is marked, with everything between
+// marked too: how many tiles lie between it and k; -1 where there is none yet.  One wave; 0 < k.
+template <int REACH>
+__device__ __forceinline__ int marked_state(const uint32_t* mark, int k) {
+  static_assert(REACH <= 64, "a lane a tile");
   const int lane = threadIdx.x & 63;
-  for (int spins = 0; spins < kSpins; ++spins) {
-    const uint32_t m = k - 1 - lane >= 0 ? peek(mark + (k - 1 - lane)) : 0u;
-    const uint64_t whole = __ballot(m == 2u), part = __ballot(m == 1u);
-    if (whole) {
-      const int n = __builtin_ctzll(whole);
-      if (n == 0 || (~part & ((1ull << n) - 1)) == 0) return n;
-    }
-    __builtin_amdgcn_s_sleep(1);
-  }
-  return -1;
+  const uint32_t m = lane < REACH && k - 1 - lane >= 0 ? peek(mark + (k - 1 - lane)) : 0u;
+  const uint64_t whole = __ballot(m == 2u), part = __ballot(m == 1u);
+  if (!whole) return -1;
+  const int n = __builtin_ctzll(whole);
+  return n == 0 || (~part & ((1ull << n) - 1)) == 0 ? n : -1;
 }
 
-// N tiles' words from tile `first` on (those before `end`), all on their way at once; words
-// that are marked may still be on theirs for a moment.
+// The state behind tile k - 1 where one of the N tiles before k has it and those after that one
+// are there: everything is asked for at once, one way to memory and back.
 template <int N, int V>
-__device__ __forceinline__ void fetch_tiles(const Chain& ch, int64_t C, int first, int end, int c,
-                                            bool on, Words<V> (&code)[N], Words<V> (&add)[N]) {
-  for (int spins = 0; spins < kSpins; ++spins) {
-    bool there = true;
+__device__ __forceinline__ bool near_state(const Chain& ch, int64_t C, int k, uint32_t at, bool on,
+                                           float (&h)[V]) {
+  Words<V> state[N], code[N], add[N];
+  const int first = k > N ? k - N : 0;
+  const __amdgpu_buffer_rsrc_t ps = rows_from(ch.state, first * C * 4),
+                               pc = rows_from(ch.code, first * C * 4),
+                               pa = rows_from(ch.add, first * C * 4);
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int64_t at = (int64_t)(first + j < end ? first + j : end - 1) * C + c;
-      code[j].load(ch.code + at);
-      add[j].load(ch.add + at);
+  for (int j = 0; j < N; ++j) {  // tile k - 1 - j
+    const uint32_t row = (uint32_t)(k - 1 - j > first ? k - 1 - j - first : 0) * (uint32_t)C * 4u;
+    state[j].load(ps, at, row);
+    if (j + 1 < N) {
+      code[j].load(pc, at, row);
+      add[j].load(pa, at, row);
     }
-#pragma unroll
-    for (int j = 0; j < N; ++j) there = there && code[j].there() && add[j].there();
-    if (__all(there || !on)) return;
   }
+  int q = -1;
+  bool open = true;
 #pragma unroll
   for (int j = 0; j < N; ++j)
+    if (open && k - 1 - j >= 0) {
+      if (__all(state[j].there() || !on)) {
+        q = j;
+        open = false;
+      } else if (j + 1 < N) {
+        open = __all((code[j].there() && add[j].there()) || !on);
+      }
+    }
+  if (q < 0) return false;
 #pragma unroll
-    for (int v = 0; v < V; ++v) add[j].w[v] = 0x7fc00000u;
-}
-template <int V>
-__device__ __forceinline__ void fetch_state(const uint32_t* p, bool on, float (&x)[V]) {
-  Words<V> w;
-  for (int spins = 0;; ++spins) {
-    w.load(p);
-    if (__all(w.there() || !on) || spins >= kSpins) break;
+  for (int j = N - 1; j >= 0; --j) {
+    if (j == q)
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = state[j].get(v);
+    if (j + 1 < N && j < q)
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = decayed_onto(code[j].get(v), h[v], add[j].get(v));
   }
+  return true;
+}
+
+// N tiles' words from tile `first` on (those before `end`) and, if asked for, the state before
+// `first`, all on their way at once; words that are marked may still be on theirs.  (A load
+// that finds none is repeated: the fence keeps the compiler from taking it for the same one.)
+template <int N, int V>
+__device__ __forceinline__ void fetch_tiles(const Chain& ch, int64_t C, int first, int end, uint32_t at,
+                                            bool on, bool with_state, Words<V> (&code)[N],
+                                            Words<V> (&add)[N], Words<V>& state) {
+  const __amdgpu_buffer_rsrc_t pc = rows_from(ch.code, first * C * 4),
+                               pa = rows_from(ch.add, first * C * 4),
+                               ps = rows_from(ch.state, (first - 1) * C * 4);
+  const int last = end - 1 - first;  // (-1: none)
+  for (int spins = 0; spins < kSpins; ++spins) {
+    bool there = true;
+    if (with_state) {
+      state.load(ps, at, 0);
+    }
 #pragma unroll
-  for (int v = 0; v < V; ++v) x[v] = w.get(v);  // (an empty word is a NaN)
+    for (int j = 0; j < N; ++j)
+      if (j <= last) {
+        const uint32_t row = (uint32_t)j * (uint32_t)C * 4u;
+        code[j].load(pc, at, row);
+        add[j].load(pa, at, row);
+      }
+    if (with_state) there = state.there();
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j <= last) there = there && code[j].there() && add[j].there();
+    if (__all(there || !on)) return;
+    asm volatile("" ::: "memory");
+  }  // (an empty word is a NaN)
 }
 
 // What a tile's waves do between their own tokens and those tokens' states.  Every wave has
-// its decay's sum and its contribution in s_sum and s_add, and whether a border lies in it in
-// s_cut; waves count in the order of the walk.  Afterwards s_from holds what every wave
-// begins with and s_sum the waves' decay codes.  All waves come here, `order` is their place;
-// `alone` (asked of the first one): nothing comes from before the tile.
-template <int W, int V>
+// put (set) its decay's sum and its contribution here, and whether a border lies in it;
+// waves count in the order of the walk.  Afterwards (from) there is what every wave begins with.
+// All waves come to run, `order` is their place; `alone` (asked of the first one): nothing
+// comes from before the tile.
+template <int W, int V, int REACH>
 struct Carry {
   static constexpr int CB = 64 * V;
-  float s_sum[W][CB], s_add[W][CB], s_from[W][CB];
-  // of the tiles between (at most kReach - 1; a wave brings kByOne at a time)
-  float s_code[kReach][CB], s_own[kReach][CB];
+  static_assert(REACH % kByOne == 0, "whole pieces");
+  float s_sum[W][CB], s_code[W][CB], s_add[W][CB];
+  // of the tiles between (at most REACH - 1; a wave brings kByOne at a time)
+  float s_tcode[REACH][CB], s_tadd[REACH][CB];
   int s_cut[W];
   int s_between;
 
+  __device__ __forceinline__ void set(int order, const float (&sum)[V], const float (&code)[V],
+                                      const float (&add)[V], bool cut) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      s_sum[order][lane * V + v] = sum[v];
+      s_code[order][lane * V + v] = code[v];
+      s_add[order][lane * V + v] = add[v];
+    }
+    if (lane == 0) s_cut[order] = cut;
+  }
+  __device__ __forceinline__ float from(int order, int v) const {
+    return s_sum[order][(threadIdx.x & 63) * V + v];
+  }
   __device__ __forceinline__ void run(const Chain& ch, int k, int tiles, int block, int64_t C, int c,
                                       bool on, bool alone, int order) {
     const int lane = threadIdx.x & 63, at = lane * V;
-    const int64_t word = (int64_t)k * C + c;
+    const uint32_t cb = c * 4;
     uint32_t* const mark = ch.mark + (int64_t)block * tiles;
     float own[V], from[V], tile_code[V];  // of wave 0
     bool cut = false;
@@ -380,37 +456,31 @@ struct Carry {
         cut |= cw;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const float s = s_sum[w][at + v];
-          const float code = cw ? __uint_as_float(kCut) : decay_code(s);
-          s_sum[w][at + v] = code;
-          all[v] += s;
-          own[v] = decayed_onto(code, own[v], s_add[w][at + v]);
+          all[v] += s_sum[w][at + v];
+          own[v] = decayed_onto(cw ? __uint_as_float(kCut) : s_code[w][at + v], own[v],
+                                s_add[w][at + v]);
         }
       }
 #pragma unroll
       for (int v = 0; v < V; ++v) tile_code[v] = cut ? __uint_as_float(kCut) : decay_code(all[v]);
       if (tiles > 1) {
         if (on) {
-          if (cut) publish<V>(ch.state + word, own);
-          publish<V>(ch.code + word, tile_code);
-          publish<V>(ch.add + word, own);
+          if (cut) publish<V>(rows_from(ch.state, k * C * 4), cb, own);
+          publish<V>(rows_from(ch.code, k * C * 4), cb, tile_code);
+          publish<V>(rows_from(ch.add, k * C * 4), cb, own);
         }
-        __builtin_amdgcn_s_waitcnt(0x0f70);
         if (lane == 0) poke(mark + k, cut ? 2u : 1u);
         if (!alone) {
-          n = nearest_state(mark, k);
-          if (n >= 0) fetch_state<V>(ch.state + word - (int64_t)(n + 1) * C, on, from);
-          else from[0] = from[V - 1] = __builtin_nanf("");
-          if (n > 0 && n <= kByOne) {
-            Words<V> code[kByOne], add[kByOne];
-            fetch_tiles<kByOne, V>(ch, C, k - n, k, c, on, code, add);
-#pragma unroll
-            for (int j = 0; j < kByOne; ++j)
-              if (j < n)
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                  from[v] = decayed_onto(code[j].get(v), from[v], add[j].get(v));
+          for (int spins = 0;; ++spins) {
+            if (near_state<kByOne, V>(ch, C, k, cb, on, from)) break;
+            n = marked_state<REACH>(mark, k);
+            if (n > 0) break;
             n = 0;
+            if (spins > kSpins) {
+              from[0] = from[V - 1] = __builtin_nanf("");
+              break;
+            }
+            asm volatile("" ::: "memory");
           }
         }
       }
@@ -419,15 +489,19 @@ struct Carry {
     __syncthreads();
     n = __builtin_amdgcn_readfirstlane(s_between);
     if (n > 0) {  // many tiles between: every wave brings some of them to LDS
+      Words<V> state;
       for (int j0 = order * kByOne; j0 < n; j0 += W * kByOne) {
         Words<V> code[kByOne], add[kByOne];
-        fetch_tiles<kByOne, V>(ch, C, k - n + j0, k, c, on, code, add);
+        fetch_tiles<kByOne, V>(ch, C, k - n + j0, k, cb, on, order + j0 == 0, code, add, state);
+        if (order + j0 == 0)
+#pragma unroll
+          for (int v = 0; v < V; ++v) from[v] = state.get(v);
 #pragma unroll
         for (int j = 0; j < kByOne; ++j)
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            s_code[j0 + j][at + v] = code[j].get(v);
-            s_own[j0 + j][at + v] = add[j].get(v);
+          for (int v = 0; v < V; ++v) {  // (past n whatever there was)
+            s_tcode[j0 + j][at + v] = code[j].get(v);
+            s_tadd[j0 + j][at + v] = add[j].get(v);
           }
       }
       __syncthreads();
@@ -437,21 +511,23 @@ struct Carry {
       for (int j = 0; j < n; ++j)
 #pragma unroll
         for (int v = 0; v < V; ++v)
-          from[v] = decayed_onto(s_code[j][at + v], from[v], s_own[j][at + v]);
+          from[v] = decayed_onto(s_tcode[j][at + v], from[v], s_tadd[j][at + v]);
       if (tiles > 1 && !cut) {
 #pragma unroll
         for (int v = 0; v < V; ++v) own[v] = decayed_onto(tile_code[v], from[v], own[v]);
-        if (on) publish<V>(ch.state + word, own);
-        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt 0: the words are in their place
+        if (on) publish<V>(rows_from(ch.state, k * C * 4), cb, own);
         if (lane == 0) poke(mark + k, 2u);
       }
 #pragma unroll 2
-      for (int w = 0; w < W; ++w)
+      for (int w = 0; w < W; ++w) {
+        const bool cw = s_cut[w] != 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          s_from[w][at + v] = from[v];
-          from[v] = decayed_onto(s_sum[w][at + v], from[v], s_add[w][at + v]);
+          s_sum[w][at + v] = from[v];
+          from[v] = decayed_onto(cw ? __uint_as_float(kCut) : s_code[w][at + v], from[v],
+                                 s_add[w][at + v]);
         }
+      }
     }
     __syncthreads();
   }

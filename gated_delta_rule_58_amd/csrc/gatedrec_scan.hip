@@ -18,10 +18,13 @@ namespace kda {
 namespace gatedrec {
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kL = 16;
-constexpr int kTile = kWaves * kL;
-static_assert(kTile % kStartsTokens == 0 && kStartsTokens % kL == 0, "starts at waves' tokens");
+constexpr int kTile = 128;
+// L tokens a wave, W waves, the tiles that a look back reaches.
+template <int V>
+struct Shape {
+  static constexpr int L = 16, W = 8, REACH = 60, TILE = L * W;
+  static_assert(TILE == kTile && kStartsTokens % L == 0, "starts at waves' tokens");
+};
 
 struct Args {
   Inputs in;
@@ -33,6 +36,7 @@ struct Args {
   float* starts;
   Chain chain;
   int tiles, blocks;  // tiles along the tokens, workgroups across the channels
+  Split by_blocks;
 };
 
 __device__ __forceinline__ int64_t slot_of(const StatePool& st, int n) {
@@ -56,9 +60,10 @@ __device__ void copy_empty(const Args& A, int first, int step) {
 }
 
 template <bool BF16, int V, bool GATE, bool GATED, bool NORM>
-__global__ void __launch_bounds__(64 * kWaves, 4) scan_kernel(const Args A) {
-  constexpr int L = kL, W = kWaves, CB = 64 * V, ES = BF16 ? 2 : 4;
-  __shared__ Carry<W, V> s;
+__global__ void __launch_bounds__(64 * Shape<V>::W, 4) scan_kernel(const Args A) {
+#pragma clang fp contract(off)  // (the same digits on every path: sums of products are spelt out)
+  constexpr int L = Shape<V>::L, W = Shape<V>::W, CB = 64 * V, ES = BF16 ? 2 : 4;
+  __shared__ Carry<W, V, Shape<V>::REACH> s;
   __shared__ uint32_t s_ticket;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -76,7 +81,8 @@ __global__ void __launch_bounds__(64 * kWaves, 4) scan_kernel(const Args A) {
     id = __builtin_amdgcn_readfirstlane(s_ticket);
     if ((uint32_t)id >= (uint32_t)work) return;
   }
-  const int k = id / A.blocks, block = id - k * A.blocks;
+  int block;
+  const int k = A.by_blocks(id, block);
   const int tile0 = k * kTile, live = A.q.live();
   if (tile0 >= live) return;
   const int t0 = tile0 + wave * L;
@@ -145,18 +151,16 @@ __global__ void __launch_bounds__(64 * kWaves, 4) scan_kernel(const Args A) {
       for (int v = 0; v < V; ++v) add[v] = fmaf(a[j][v], add[v], b[j][v]);
     }
   }
+  float code[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    s.s_sum[wave][lane * V + v] = sum[v];
-    s.s_add[wave][lane * V + v] = add[v];
-  }
-  if (lane == 0) s.s_cut[wave] = bd.first != 0;
+  for (int v = 0; v < V; ++v) code[v] = decay_code(sum[v]);
+  s.set(wave, sum, code, add, bd.first != 0);
   __syncthreads();
   s.run(A.chain, k, A.tiles, block, A.C, cc, on, k == 0 || (bd.first & 1u), wave);
 
   float h[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = s.s_from[wave][lane * V + v];
+  for (int v = 0; v < V; ++v) h[v] = s.from(wave, v);
   if (!on || t0 >= live) return;
   if (A.starts && t0 % kStartsTokens == 0)
 #pragma unroll
@@ -254,6 +258,7 @@ hipError_t launch_scan(const Inputs& in, const Batch& b, const StatePool& st, vo
   const Out outs[] = {{h, h_bf16}};
   const int V = width(in, b.C, outs, 1);
   A.blocks = (b.C + 64 * V - 1) / (64 * V);
+  A.by_blocks = Split(A.blocks);
   // Sequences without tokens: workgroups of their own behind the tiles', unless the host
   // knows that there are none or their states stay where they are.
   bool empties = st.out && st.out != st.in;
@@ -266,7 +271,7 @@ hipError_t launch_scan(const Inputs& in, const Batch& b, const StatePool& st, vo
   const int64_t grid = work + (empties ? (b.N < 256 ? b.N : 256) : 0);
   if (grid == 0) return hipSuccess;
 #define KDA_GR(BF, V_, G, I, N_) \
-  scan_kernel<BF, V_, G, I, N_><<<(unsigned)grid, 64 * kWaves, 0, s>>>(A)
+  scan_kernel<BF, V_, G, I, N_><<<(unsigned)grid, 64 * Shape<V_>::W, 0, s>>>(A)
 #define KDA_GR_N(BF, V_, G, I)                 \
   do {                                         \
     if (in.normalize) KDA_GR(BF, V_, G, I, true); \

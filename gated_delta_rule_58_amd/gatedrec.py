@@ -33,7 +33,7 @@ _SIGNATURES = {
 }
 _FNS = {}
 _E4M3 = torch.float8_e4m3fn
-STARTS_TOKENS = 64  # tokens between two states of `starts`
+STARTS_TOKENS = 32  # tokens between two states of `starts`
 
 
 def _fn(name: str):

@@ -57,7 +57,7 @@ extern "C" {
  *         sequence (NULL; then num_slots >= N).  A slot outside the pool starts from zeros
  *         and is not written; two sequences must not share a written slot.
  *   h     [T_tot, C] dtype h_dt
- *   starts: NULL, or fp32 [ceil(T_tot / 64), C] (kda_gatedrec_starts_bytes) that the call
+ *   starts: NULL, or fp32 [ceil(T_tot / 32), C] (kda_gatedrec_starts_bytes) that the call
  *         fills with states on its way, for kda_gatedrec_scan_backward of the same inputs.
  *         What lies behind the last sequence is left as it was.
  *   workspace: kda_gatedrec_scan_workspace_bytes (0 for up to 128 tokens), 16-byte aligned,

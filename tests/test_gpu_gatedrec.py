@@ -273,8 +273,8 @@ def test_long_sequence_many_tiles(C):
 
 
 def test_wide():
-    """The layer's width over many tiles and channel blocks at once: a few channels of it alone
-    (which test_channels holds to the reference) give the same bits."""
+    """The layer's width over many tiles and channel blocks at once, against the reference on a
+    few channels; the same call gives the same bits."""
     need_gpu()
     say("gatedrec wide")
     T, C = 3000, 12288
@@ -285,16 +285,22 @@ def test_wide():
     B = torch.randn(C, generator=gen, device=DEV) - 4.0
     cu = torch.tensor([0, 1000, 1001, 3000], dtype=torch.int32)
     args = dict(normalize=True, cu_seqlens=cu.to(DEV), cu_seqlens_host=cu)
-    a = kda.gatedrec_scan(X, R, I, A, B, output_starts=True, **args)
-    cols = [0, 63, 64, 127, 128, 5000, 12287]
-    take = lambda t: t[:, cols].contiguous()  # noqa: E731
-    b = kda.gatedrec_scan(take(X), take(R), take(I), A[cols], B[cols], output_starts=True, **args)
-    assert all(torch.equal(p[:, cols], q) for p, q in zip(a, b))
     DH = torch.randn(T, C, generator=gen, device=DEV).to(BF)
+    a = kda.gatedrec_scan(X, R, I, A, B, output_starts=True, **args)
     g = kda.gatedrec_scan_backward(X, R, I, DH, A, B, starts=a[2], **args)
-    g2 = kda.gatedrec_scan_backward(take(X), take(R), take(I), take(DH), A[cols], B[cols], **args)
-    for p, q in zip(g, g2):
-        assert torch.equal(p[..., cols], q)
+    cols = [0, 1, 63, 64, 127, 128, 5000, 12287]
+    take = lambda t: t[..., cols].cpu()  # noqa: E731
+    want = ref.backward(take(X), take(R), take(I), take(A), take(B), True, cu.tolist(), None,
+                        take(DH), None)
+    ref.within("h", take(a[0]), want["h"], want["eh"], BF)
+    ref.within("S", take(a[1]), want["S"], want["eS"], F32)
+    for k, (key, t) in enumerate(zip(("dx", "dr", "di", "dA", "db", "dS0"), g)):
+        say(key, "%.2g" % ref.within(key, take(t), want[key], want["e" + key], BF if k < 3 else F32))
+    for _ in range(3):
+        assert all(torch.equal(p, q) for p, q in zip(
+            a, kda.gatedrec_scan(X, R, I, A, B, output_starts=True, **args)))
+        assert all(torch.equal(p, q) for p, q in zip(
+            g, kda.gatedrec_scan_backward(X, R, I, DH, A, B, **args)))
 
 
 # ------------------------------------------------------------------- decode
