@@ -12,16 +12,22 @@ namespace kda {
 namespace gatedrec {
 namespace {
 
+// A workgroup's channels belong to one sequence, so that rows are uniform.
 template <bool BF16, bool SB, int V, bool GATE, bool GATED, bool NORM>
 __global__ void __launch_bounds__(256) decode_kernel(
     const Inputs in, int N, int C, void* pool, int64_t num_slots,
     const int32_t* __restrict__ slots, void* __restrict__ h, bool h_bf16) {
-  constexpr int ES = BF16 ? 2 : 4;
-  // a workgroup's channels belong to one sequence, so that rows are uniform
+  constexpr int ES = BF16 ? 2 : 4, SS = SB ? 2 : 4;
   const int per = (C + 256 * V - 1) / (256 * V);
   const int n = blockIdx.x / per;
   const int c = ((blockIdx.x - n * per) * 256 + threadIdx.x) * V;
   if (c >= C) return;
+  Vals<BF16, V> rx, rr, ri;  // on their way before the slot is known
+  rr.load(rows_from(in.r.p, n * in.r.stride * ES), c * ES, 0);
+  rx.load(rows_from(in.x.p, n * in.x.stride * ES), c * ES, 0);
+  if constexpr (GATED) ri.load(rows_from(in.i.p, n * in.i.stride * ES), c * ES, 0);
+  Params<V, GATE> par;
+  par.load(in, c);
   const int64_t slot = slots ? (int64_t)__builtin_amdgcn_readfirstlane(slots[n]) : n;
   const __amdgpu_buffer_rsrc_t ph = rows_from(h, (int64_t)n * C * (h_bf16 ? 2 : 4));
   float out[V];
@@ -29,15 +35,9 @@ __global__ void __launch_bounds__(256) decode_kernel(
 #pragma unroll
     for (int v = 0; v < V; ++v) out[v] = 0.0f;
   } else {
-    const __amdgpu_buffer_rsrc_t ps = rows_from(pool, slot * C * (SB ? 2 : 4));
-    Vals<BF16, V> rx, rr, ri;
+    const __amdgpu_buffer_rsrc_t ps = rows_from(pool, slot * C * SS);
     Vals<SB, V> st;
-    st.load(ps, c * (SB ? 2 : 4), 0);
-    rr.load(rows_from(in.r.p, n * in.r.stride * ES), c * ES, 0);
-    rx.load(rows_from(in.x.p, n * in.x.stride * ES), c * ES, 0);
-    if constexpr (GATED) ri.load(rows_from(in.i.p, n * in.i.stride * ES), c * ES, 0);
-    Params<V, GATE> par;
-    par.load(in, c);
+    st.load(ps, c * SS, 0);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const float g = par.log2_decay(rr.get(v), v);
@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(256) decode_kernel(
       if constexpr (NORM) u *= __builtin_amdgcn_sqrtf(one_minus_square(g, a));
       out[v] = decayed_onto(decay_code(g), st.get(v), u);
     }
-    Vals<SB, V>::store(ps, c * (SB ? 2 : 4), 0, out);
+    Vals<SB, V>::store(ps, c * SS, 0, out);
   }
   if (h_bf16) Vals<true, V>::store(ph, c * 2, 0, out);
   else Vals<false, V>::store(ph, c * 4, 0, out);
@@ -60,11 +60,11 @@ hipError_t launch_decode(const Inputs& in, int N, int C, void* pool, bool state_
                          hipStream_t s) {
   if (N == 0) return hipSuccess;
   const Out outs[] = {{h, h_bf16}, {pool, state_bf16}};
-  const int V = width(in, C, outs, 2);
+  const int V = in_pieces_of(4, in, C, outs, 2) ? 4 : 1;
   const int64_t grid = (int64_t)N * ((C + 256 * V - 1) / (256 * V));
-#define KDA_GR(BF, SB, V_, G, I, N_)                                                            \
-  decode_kernel<BF, SB, V_, G, I, N_><<<(unsigned)grid, 256, 0, s>>>(in, N, C, pool, num_slots, \
-                                                                   slots, h, h_bf16)
+#define KDA_GR(BF, SB, V_, G, I, N_)                                                               \
+  decode_kernel<BF, SB, V_, G, I, N_><<<(unsigned)grid, 256, 0, s>>>(in, N, C, pool, num_slots, slots, \
+                                                                   h, h_bf16)
 #define KDA_GR_N(BF, SB, V_, G, I)                    \
   do {                                                \
     if (in.normalize) KDA_GR(BF, SB, V_, G, I, true); \
@@ -82,13 +82,13 @@ hipError_t launch_decode(const Inputs& in, int N, int C, void* pool, bool state_
   } while (0)
 #define KDA_GR_V(BF, SB)              \
   do {                                \
-    if (V == 2) KDA_GR_G(BF, SB, 2);  \
+    if (V == 4) KDA_GR_G(BF, SB, 4);  \
     else KDA_GR_G(BF, SB, 1);         \
   } while (0)
   if (in.bf16 && state_bf16) KDA_GR_V(true, true);
   else if (in.bf16) KDA_GR_V(true, false);
-  else if (state_bf16) KDA_GR_G(false, true, 1);
-  else KDA_GR_G(false, false, 1);
+  else if (state_bf16) KDA_GR_V(false, true);
+  else KDA_GR_V(false, false);
 #undef KDA_GR_V
 #undef KDA_GR_G
 #undef KDA_GR_I

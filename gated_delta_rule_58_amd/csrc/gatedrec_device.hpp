@@ -18,38 +18,43 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_from(const void* p, int64
 }
 template <bool BF16, int V>
 struct Vals {
-  static constexpr int BYTES = V * (BF16 ? 2 : 4);
-  static_assert(BYTES == 2 || BYTES == 4 || BYTES == 8, "one load");
-  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-  uint32_t w[BYTES == 8 ? 2 : 1];
+  static constexpr int BYTES = V * (BF16 ? 2 : 4), N = BYTES < 4 ? 1 : BYTES / 4;
+  static_assert(BYTES == 2 || BYTES == 4 || BYTES == 8 || BYTES == 16, "one load");
+  typedef uint32_t Wide __attribute__((ext_vector_type(N)));
+  uint32_t w[N];
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rows, uint32_t at, uint32_t row) {
-    if constexpr (BYTES == 2) {
-      w[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rows, at, row, 0);
-    } else if constexpr (BYTES == 4) {
-      w[0] = __builtin_amdgcn_raw_buffer_load_b32(rows, at, row, 0);
-    } else {
-      const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rows, at, row, 0));
-      w[0] = x[0];
-      w[1] = x[1];
-    }
+    Wide x;
+    if constexpr (BYTES == 2) x = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rows, at, row, 0);
+    else if constexpr (BYTES == 4) x = __builtin_amdgcn_raw_buffer_load_b32(rows, at, row, 0);
+    else if constexpr (BYTES == 8)
+      x = __builtin_bit_cast(Wide, __builtin_amdgcn_raw_buffer_load_b64(rows, at, row, 0));
+    else x = __builtin_bit_cast(Wide, __builtin_amdgcn_raw_buffer_load_b128(rows, at, row, 0));
+#pragma unroll
+    for (int n = 0; n < N; ++n) w[n] = x[n];
   }
   __device__ __forceinline__ float get(int v) const {
-    if constexpr (BF16) return __uint_as_float(v ? w[0] & 0xffff0000u : w[0] << 16);
-    return __uint_as_float(w[v]);
+    if constexpr (BF16) return __uint_as_float(v & 1 ? w[v / 2] & 0xffff0000u : w[v / 2] << 16);
+    return __uint_as_float(w[BF16 ? 0 : v]);
   }
   static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t rows, uint32_t at,
                                                uint32_t row, const float (&x)[V]) {
     if constexpr (BYTES == 2) {
       __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16_bits(x[0]), rows, at, row, 0);
-    } else if constexpr (BF16) {
-      typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-      const bf16x2 y = {static_cast<__bf16>(x[0]), static_cast<__bf16>(x[V - 1])};
-      __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, y), rows, at, row, 0);
-    } else if constexpr (BYTES == 4) {
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[0]), rows, at, row, 0);
     } else {
-      const u32x2 y = {__float_as_uint(x[0]), __float_as_uint(x[V - 1])};
-      __builtin_amdgcn_raw_buffer_store_b64(y, rows, at, row, 0);
+      Wide y;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        if constexpr (BF16) {
+          typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+          y[n] = __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(x[2 * n]),
+                                                     static_cast<__bf16>(x[2 * n + 1])});
+        } else {
+          y[n] = __float_as_uint(x[n]);
+        }
+      }
+      if constexpr (BYTES == 4) __builtin_amdgcn_raw_buffer_store_b32(y[0], rows, at, row, 0);
+      else if constexpr (BYTES == 8) __builtin_amdgcn_raw_buffer_store_b64(y, rows, at, row, 0);
+      else __builtin_amdgcn_raw_buffer_store_b128(y, rows, at, row, 0);
     }
   }
 };
@@ -68,19 +73,24 @@ __device__ __forceinline__ void store_state(void* p, int64_t at, const float (&x
   }
 }
 
-// Values a lane takes at once: two of bf16 (4 bytes a lane) where every row and output is
-// aligned to that, else one.
+// Whether every row and output may be taken V values at a time.
 struct Out {
   const void* p;
   bool bf16;
 };
-inline int width(const Inputs& in, int C, const Out* outs, int count) {
-  if (!in.bf16 || C % 2) return 1;
+inline bool in_pieces_of(int V, const Inputs& in, int C, const Out* outs, int count) {
+  const size_t es = in.bf16 ? 2 : 4;
+  if (C % V) return false;
   for (const Rows* r : {&in.x, &in.r, &in.i})
-    if (reinterpret_cast<uintptr_t>(r->p) % 4 || r->stride % 2) return 1;
+    if (reinterpret_cast<uintptr_t>(r->p) % (V * es) || r->stride % V) return false;
   for (int k = 0; k < count; ++k)
-    if (reinterpret_cast<uintptr_t>(outs[k].p) % (outs[k].bf16 ? 4 : 8)) return 1;
-  return 2;
+    if (reinterpret_cast<uintptr_t>(outs[k].p) % (V * (outs[k].bf16 ? 2 : 4))) return false;
+  return true;
+}
+// Values a lane takes at once in the scan and its gradients: two of bf16 (4 bytes a lane)
+// where that is aligned, else one.
+inline int width(const Inputs& in, int C, const Out* outs, int count) {
+  return in.bf16 && in_pieces_of(2, in, C, outs, count) ? 2 : 1;
 }
 
 // -------------------------------------------------------------------- gate

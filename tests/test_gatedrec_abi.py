@@ -1,0 +1,282 @@
+"""The entry points of kda_gatedrec.h are exported and refuse bad arguments on the host
+before any HIP call (fake device addresses, never dereferenced)."""
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+DEV = [0x10000000 * (i + 1) for i in range(20)]
+FAR = [(i + 1) << 44 for i in range(20)]
+
+
+def _fn(name):
+    import gated_delta_rule_58_amd as kda
+    if not os.path.exists(kda.lib_path()):
+        from gated_delta_rule_58_amd.build import build_library
+        build_library()
+    from gated_delta_rule_58_amd import gatedrec
+    return gatedrec._fn(name)
+
+
+def _last():
+    import gated_delta_rule_58_amd as kda
+    return kda.lib().kda_last_error().decode()
+
+
+def test_every_declared_entry_point_is_bound():
+    import gated_delta_rule_58_amd as kda
+    from gated_delta_rule_58_amd import gatedrec
+    src = open(os.path.join(ROOT, "include", "kda_gatedrec.h")).read()
+    src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
+    names = set(re.findall(r"\b(kda_[a-z0-9_]+)\s*\(", src))
+    assert names == set(gatedrec._SIGNATURES)
+    assert names <= set(kda.exported_symbols())
+    for n in names:
+        _fn(n)
+
+
+def _host(cu):
+    a = np.ascontiguousarray(np.asarray(cu, dtype=np.int32))
+    return a, a.ctypes.data
+
+
+BASE = dict(x=DEV[0], xs=96, r=DEV[1], rs=96, i=DEV[2], is_=96, dt=1, A=DEV[3], b=DEV[4], norm=1,
+            C=96)
+
+
+def _rows(a):
+    return (a["x"], a["xs"], a["r"], a["rs"], a["i"], a["is_"], a["dt"], a["A"], a["b"], a["norm"])
+
+
+def _scan(cu_host=(0, 120, 300), **kw):
+    a = dict(BASE, cu=DEV[5], N=2, S0=None, Sf=DEV[6], S_dt=0, slots=2, idx=None, h=DEV[7], h_dt=1,
+             starts=DEV[8], T=300, ws=DEV[9], ws_bytes=1 << 20)
+    a.update(kw)
+    keep, hp = _host(cu_host) if cu_host is not None else (None, None)
+    return _fn("kda_gatedrec_scan")(
+        *_rows(a), a["cu"], hp, a["N"], a["S0"], a["Sf"], a["S_dt"], a["slots"], a["idx"], a["h"],
+        a["h_dt"], a["starts"], a["T"], a["C"], a["ws"], a["ws_bytes"], None)
+
+
+SHARED = [
+    (dict(C=0), 1), (dict(C=-4), 1), (dict(C=(1 << 20) + 1), 4), (dict(dt=7), 3), (dict(norm=2), 1),
+    (dict(A=None), 1), (dict(xs=95), 2), (dict(rs=95), 2), (dict(is_=95), 2),
+    (dict(xs=(1 << 24) + 1), 4), (dict(x=DEV[0] + 1), 5), (dict(r=DEV[1] + 1), 5),
+    (dict(i=DEV[2] + 1), 5), (dict(A=DEV[3] + 2), 5), (dict(b=DEV[4] + 2), 5), (dict(x=None), 1),
+    (dict(r=None), 1),
+]
+
+
+@pytest.mark.parametrize("bad, status", SHARED + [
+    (dict(T=-1), 1), (dict(T=1 << 31), 4), (dict(N=0), 1), (dict(cu=None), 1),
+    (dict(cu=DEV[5] + 2), 5), (dict(h=None), 1), (dict(h=DEV[7] + 1), 5), (dict(h_dt=5), 3),
+    (dict(S_dt=5), 3), (dict(slots=-1), 1), (dict(slots=1), 2), (dict(slots=1 << 60), 4),
+    (dict(idx=DEV[10] + 2), 5), (dict(Sf=DEV[6] + 2), 5), (dict(S0=DEV[11] + 2), 5),
+    (dict(starts=DEV[8] + 2), 5), (dict(ws=None), 6), (dict(ws_bytes=100), 6),
+    (dict(ws=DEV[9] + 8), 5), (dict(h=DEV[0]), 1), (dict(h=DEV[2] + 96), 1), (dict(Sf=DEV[1]), 1),
+    (dict(S0=DEV[6] + 16), 1), (dict(starts=DEV[3]), 1), (dict(ws=DEV[2]), 1), (dict(ws=DEV[5]), 1),
+    (dict(Sf=DEV[7]), 1), (dict(starts=DEV[7] + 64), 1), (dict(h=DEV[3]), 1),
+])
+def test_scan_refusals(bad, status):
+    assert _scan(**bad) == status, _last()
+    assert "kda_gatedrec_scan" in _last()
+
+
+@pytest.mark.parametrize("cu", [(1, 20, 300), (0, 310, 300), (0, 20, 299), (0, -1, 300)])
+def test_scan_refuses_bad_cu_seqlens(cu):
+    assert _scan(cu_host=cu) == 2
+
+
+def test_scan_equal_lengths_need_a_multiple():
+    assert _scan(cu_host=None, cu=None, N=7, slots=7) == 2
+    assert "multiple" in _last()
+
+
+def test_dt_bias_needs_A_log():
+    assert _scan(A=None, b=DEV[4]) == 1 and "dt_bias" in _last()
+
+
+def _backward(cu_host=(0, 120, 300), has_starts=True, **kw):
+    need = _fn("kda_gatedrec_scan_backward_workspace_bytes")(300, 96, 1 if has_starts else 0)
+    a = dict(BASE, cu=DEV[5], N=2, S0=None, starts=DEV[8] if has_starts else None, dh=DEV[7],
+             dh_dt=1, dS=None, dx=DEV[10], dr=DEV[11], di=DEV[12], g_dt=1, dA=DEV[13], db=DEV[14],
+             dS0=DEV[15], T=300, ws=DEV[16], ws_bytes=need)
+    a.update(kw)
+    keep, hp = _host(cu_host) if cu_host is not None else (None, None)
+    return _fn("kda_gatedrec_scan_backward")(
+        *_rows(a), a["cu"], hp, a["N"], a["S0"], a["starts"], a["dh"], a["dh_dt"], a["dS"], a["dx"],
+        a["dr"], a["di"], a["g_dt"], a["dA"], a["db"], a["dS0"], a["T"], a["C"], a["ws"],
+        a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("bad, status", SHARED + [
+    (dict(T=-1), 1), (dict(N=0), 1), (dict(cu=None), 1), (dict(dh_dt=4), 3), (dict(g_dt=4), 3),
+    (dict(dx=None), 1), (dict(dr=None), 1), (dict(di=None), 1), (dict(i=None), 1),
+    (dict(A=None, b=None), 1), (dict(dh=DEV[7] + 1), 5), (dict(dx=DEV[10] + 1), 5),
+    (dict(dA=DEV[13] + 2), 5), (dict(dS0=DEV[15] + 2), 5), (dict(starts=DEV[8] + 1), 5),
+    (dict(ws=None), 6), (dict(ws_bytes=1024), 6), (dict(ws=DEV[16] + 8), 5), (dict(dx=DEV[0]), 1),
+    (dict(dr=DEV[10]), 1), (dict(di=DEV[7]), 1), (dict(dS0=DEV[14]), 1), (dict(ws=DEV[8]), 1),
+    (dict(dx=DEV[16]), 1), (dict(dA=DEV[8]), 1),
+])
+def test_backward_refusals(bad, status):
+    assert _backward(**bad) == status, _last()
+    assert "kda_gatedrec_scan_backward" in _last()
+
+
+def test_a_backward_without_starts_needs_more():
+    need = _fn("kda_gatedrec_scan_backward_workspace_bytes")
+    assert need(300, 96, 0) > need(300, 96, 1) > 0
+    assert _backward(has_starts=False, ws_bytes=need(300, 96, 1)) == 6
+
+
+def _decode(**kw):
+    a = dict(BASE, S=DEV[6], S_dt=0, slots=48, idx=None, h=DEV[7], h_dt=1, N=48)
+    a.update(kw)
+    return _fn("kda_gatedrec_decode")(*_rows(a), a["S"], a["S_dt"], a["slots"], a["idx"], a["h"],
+                                      a["h_dt"], a["N"], a["C"], None)
+
+
+@pytest.mark.parametrize("bad, status", SHARED + [
+    (dict(N=-1), 1), (dict(S=None), 1), (dict(S=DEV[2]), 1), (dict(S=DEV[6] + 2), 5),
+    (dict(S=DEV[7]), 1), (dict(slots=47), 2), (dict(slots=-1), 1), (dict(h=None), 1),
+    (dict(h=DEV[0]), 1), (dict(h=DEV[7] + 1), 5), (dict(h_dt=4), 3), (dict(S_dt=4), 3),
+    (dict(idx=DEV[8] + 1), 5), (dict(S=DEV[4]), 1),
+])
+def test_decode_refusals(bad, status):
+    assert _decode(**bad) == status, _last()
+    assert "kda_gatedrec_decode" in _last()
+
+
+def test_of_nothing_is_nothing():
+    assert _decode(N=0, slots=0, x=None, r=None, S=None, h=None) == 0
+
+
+def test_calls_that_no_launch_holds():
+    far = dict(x=FAR[0], r=FAR[1], i=FAR[2], A=FAR[3], b=FAR[4])
+    C, T = 1 << 20, 1 << 19
+    rows = dict(far, xs=C, rs=C, is_=C, C=C)
+    assert _scan(cu_host=None, cu=FAR[5], N=1, Sf=None, slots=1, h=FAR[6], starts=None, T=T,
+                 ws=FAR[7], ws_bytes=1 << 43, **rows) == 4
+    assert "launch" in _last()
+    assert _backward(cu_host=None, cu=FAR[5], N=1, starts=FAR[6], dh=FAR[7], dx=FAR[8], dr=FAR[9],
+                     di=FAR[10], dA=FAR[11], db=FAR[12], dS0=None, T=T, ws=FAR[13],
+                     ws_bytes=1 << 43, **rows) == 4
+    assert "launch" in _last()
+    assert _decode(N=1 << 14, slots=1 << 14, S=FAR[6], h=FAR[7], **rows) == 4
+
+
+def test_sizes():
+    ws, st = _fn("kda_gatedrec_scan_workspace_bytes"), _fn("kda_gatedrec_starts_bytes")
+    bw = _fn("kda_gatedrec_scan_backward_workspace_bytes")
+    assert ws(128, 96) == 0 and ws(129, 96) > 0 and ws(-1, 96) == 0 and ws(300, 0) == 0
+    assert ws(1 << 31, 96) == 0 and ws(300, (1 << 20) + 1) == 0
+    assert st(1, 96) == 96 * 4 and st(33, 96) == 2 * 96 * 4 and st(0, 96) == 0
+    assert bw(300, 0, 1) == 0 and bw(300, 96, 1) > 0
+
+
+# ------------------------------------------------------------------ RMS norm
+def _rms(name="kda_rmsnorm", **kw):
+    a = dict(x=DEV[0], x_dt=1, xs=4 * 128, res=DEV[1], s=DEV[2], r_dt=1, w=DEV[3], groups=4,
+             y=DEV[4], y_dt=1, scales=DEV[5], group=128, rows=40, d=128, eps=1e-5)
+    a.update(kw)
+    head = (a["x"], a["x_dt"], a["xs"], a["res"], a["s"], a["r_dt"], a["w"], a["groups"], a["y"])
+    tail = (a["rows"], a["d"], a["eps"], None)
+    if name == "kda_rmsnorm":
+        return _fn(name)(*head, a["y_dt"], *tail)
+    return _fn(name)(*head, a["scales"], a["group"], *tail)
+
+
+RMS = [
+    (dict(rows=-1), 1), (dict(groups=0), 1), (dict(d=0), 1), (dict(rows=41), 2), (dict(x_dt=3), 3),
+    (dict(r_dt=3), 3), (dict(x_dt=0, r_dt=1), 3), (dict(d=16385, xs=1 << 20), 4),
+    (dict(groups=65536, rows=65536, xs=65536 * 128), 4), (dict(eps=-1.0), 1),
+    (dict(eps=float("nan")), 1), (dict(xs=511), 2), (dict(xs=(1 << 31) + 1), 4), (dict(x=None), 1),
+    (dict(y=None), 1), (dict(res=None), 1), (dict(s=None), 1), (dict(x=DEV[0] + 1), 5),
+    (dict(res=DEV[1] + 1), 5), (dict(s=DEV[2] + 1), 5), (dict(w=DEV[3] + 2), 5),
+    (dict(y=DEV[0] + 256), 1), (dict(y=DEV[1]), 1), (dict(y=DEV[2]), 1), (dict(y=DEV[3]), 1),
+    (dict(s=DEV[1] + 256), 1), (dict(s=DEV[0], xs=600), 1), (dict(s=DEV[0], r_dt=0), 1),
+    (dict(s=DEV[3]), 1), (dict(rows=1 << 41, groups=1), 4),
+]
+
+
+@pytest.mark.parametrize("bad, status", RMS + [
+    (dict(y_dt=3), 3), (dict(y=DEV[4] + 1), 5), (dict(y=DEV[0], y_dt=0), 1),
+    (dict(y=DEV[0], xs=600), 1),
+])
+def test_rmsnorm_refusals(bad, status):
+    assert _rms(**bad) == status, _last()
+    assert "kda_rmsnorm" in _last()
+
+
+@pytest.mark.parametrize("bad, status", RMS + [
+    (dict(group=64), 4), (dict(group=-1), 4), (dict(scales=None), 1), (dict(scales=DEV[5] + 2), 5),
+    (dict(scales=DEV[4]), 1), (dict(scales=DEV[0]), 1), (dict(y=DEV[0]), 1), (dict(scales=DEV[3]), 1),
+])
+def test_rmsnorm_e4m3_refusals(bad, status):
+    assert _rms("kda_rmsnorm_e4m3", **bad) == status, _last()
+    assert "kda_rmsnorm_e4m3" in _last()
+
+
+def test_rmsnorm_of_no_rows_is_nothing():
+    assert _rms(rows=0, x=None, y=None) == 0
+    assert _rms("kda_rmsnorm_e4m3", rows=0, x=None, y=None, scales=None) == 0
+
+
+def _rmsb(**kw):
+    a = dict(dy=DEV[0], dy_dt=1, s=DEV[1], s_dt=1, ss=4 * 128, w=DEV[2], groups=4, dres=DEV[3],
+             dx=DEV[4], dw=DEV[5], rows=40, d=128, eps=1e-5, ws=DEV[6], ws_bytes=1 << 26)
+    a.update(kw)
+    return _fn("kda_rmsnorm_backward")(
+        a["dy"], a["dy_dt"], a["s"], a["s_dt"], a["ss"], a["w"], a["groups"], a["dres"], a["dx"],
+        a["dw"], a["rows"], a["d"], a["eps"], a["ws"], a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("bad, status", [
+    (dict(rows=-4), 1), (dict(rows=42), 2), (dict(d=20000, ss=1 << 20), 4), (dict(dy_dt=9), 3),
+    (dict(s_dt=9), 3), (dict(ss=500), 2), (dict(dy=None), 1), (dict(s=None), 1), (dict(dx=None), 1),
+    (dict(ws=None), 6), (dict(ws_bytes=16), 6), (dict(ws=DEV[6] + 8), 5), (dict(dw=DEV[5] + 1), 5),
+    (dict(dres=DEV[3] + 1), 5), (dict(dx=DEV[1] + 2), 1), (dict(dx=DEV[1], ss=600), 1),
+    (dict(dx=DEV[0], dy_dt=0), 1), (dict(dx=DEV[3] + 2), 1), (dict(dw=DEV[0]), 1),
+    (dict(dx=DEV[2]), 1), (dict(ws=DEV[1]), 1), (dict(dw=DEV[4]), 1),
+])
+def test_rmsnorm_backward_refusals(bad, status):
+    assert _rmsb(**bad) == status, _last()
+    assert "kda_rmsnorm_backward" in _last()
+
+
+def test_binding_refuses_what_the_library_cannot_see():
+    """Shapes, dtypes, devices and strides are checked before any pointer is taken."""
+    import gated_delta_rule_58_amd as kda
+    x, A = torch.zeros(4, 6), torch.zeros(6)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.gatedrec_scan(x, x, x, A)
+    with pytest.raises(ValueError, match="tokens, channels"):
+        kda.gatedrec_scan(x[0], x[0])
+    with pytest.raises(ValueError, match="r must be"):
+        kda.gatedrec_scan(x, x[:3])
+    with pytest.raises(TypeError, match="one dtype"):
+        kda.gatedrec_scan(x, x, x.bfloat16())
+    with pytest.raises(ValueError, match="A_log must be"):
+        kda.gatedrec_decode(x, x, x, x, torch.zeros(5))
+    with pytest.raises(TypeError, match="dt_bias must be"):
+        kda.gatedrec_scan_backward(x, x, x, None, A, A.bfloat16())
+    with pytest.raises(ValueError, match="GPU"):
+        kda.rmsnorm(x)
+    with pytest.raises(ValueError, match="residual must be"):
+        kda.rmsnorm(x, residual=x[:3])
+    with pytest.raises(TypeError, match="residual must be"):
+        kda.rmsnorm(x, residual=x.bfloat16())
+    with pytest.raises(ValueError, match="needs a residual"):
+        kda.rmsnorm(x, residual_out=x)
+    with pytest.raises(ValueError, match="last two"):
+        kda.rmsnorm(x, torch.ones(3, 6))
+    from gated_delta_rule_58_amd import gatedrec
+    with pytest.raises(ValueError, match="dense"):
+        gatedrec._rows(torch.zeros(6, 4).t(), x, None, None, None, False)
+    with pytest.raises(ValueError, match="contiguous"):
+        gatedrec._token_stride("x", torch.zeros(4, 3, 6).transpose(0, 1), 1, 6)
+    assert gatedrec._token_stride("x", torch.zeros(4, 9)[:, 2:8], 1, 6) == 9
+    assert gatedrec._token_stride("x", torch.zeros(4, 5, 6)[:, 1:3], 2, 6) == 30
