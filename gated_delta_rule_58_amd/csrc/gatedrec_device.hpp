@@ -100,19 +100,17 @@ inline int width(const Inputs& in, int C, const Out* outs, int count) {
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
 
-// log(1 + e) for 0 <= e <= 1: e times a polynomial, 3 u of itself (u = 2^-24).  A hardware
-// log with its correction for small e (gate_math.hpp) costs half as much again.
-__device__ __forceinline__ float log1p_unit(float e) {
-  float p = 0.005232629366219044f;
-  p = fmaf(p, e, -0.029504986479878426f);
-  p = fmaf(p, e, 0.07822556048631668f);
-  p = fmaf(p, e, -0.13663214445114136f);
-  p = fmaf(p, e, 0.1910599321126938f);
-  p = fmaf(p, e, -0.2484297901391983f);
-  p = fmaf(p, e, 0.3331909775733948f);
-  p = fmaf(p, e, -0.4999949336051941f);
-  p = fmaf(p, e, 0.9999999403953552f);
-  return e * p;
+// log2(1 + e) / e for 0 <= e <= 1, with the product 6 u of itself (u = 2^-24).  A hardware log
+// with its correction for small e (gate_math.hpp) costs half as much again.
+__device__ __forceinline__ float log2_1p_over(float e) {
+  float p = -0.012319324538111687f;
+  p = fmaf(p, e, 0.06360738724470139f);
+  p = fmaf(p, e, -0.1553512066602707f);
+  p = fmaf(p, e, 0.2560092806816101f);
+  p = fmaf(p, e, -0.35339468717575073f);
+  p = fmaf(p, e, 0.48006367683410645f);
+  p = fmaf(p, e, -0.7213100790977478f);
+  return fmaf(p, e, 1.4426947832107544f);
 }
 // 1 - 2^y for y <= 0, e = 2^y: the difference loses the digits of a small y, so there it is a
 // polynomial (0.3 u).
@@ -124,14 +122,14 @@ __device__ __forceinline__ float one_minus_exp2(float y, float e) {
   p = fmaf(p, y, 0.6931471824645996f);
   return y > -0.5f ? -y * p : 1.0f - e;  // NaN stays NaN
 }
-// 1 - 4^g2 for g2 <= 0, a = 2^g2: the same at y = 2 g2.
+// 1 - 4^g2 for g2 <= 0, a = 2^g2: the same, a degree less up to where a^2, two digits of
+// a off by one, leaves 21 u of the difference.
 __device__ __forceinline__ float one_minus_square(float g2, float a) {
-  float p = 0.036890022456645966f;
-  p = fmaf(p, g2, 0.15263719856739044f);
-  p = fmaf(p, g2, 0.4439200460910797f);
-  p = fmaf(p, g2, 0.9609023928642273f);
-  p = fmaf(p, g2, 1.3862943649291992f);
-  return g2 > -0.25f ? -g2 * p : fmaf(-a, a, 1.0f);
+  float p = 0.14359961450099945f;
+  p = fmaf(p, g2, 0.4432348608970642f);
+  p = fmaf(p, g2, 0.9608860015869141f);
+  p = fmaf(p, g2, 1.3862942457199097f);
+  return g2 > -0.125f ? -g2 * p : fmaf(-a, a, 1.0f);
 }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float sigmoid_fast(float x) {
@@ -141,30 +139,24 @@ __device__ __forceinline__ float sigmoid_fast(float x) {
 // The gate of a lane's channels: kda_gate's formula with its sums in log2 units.
 template <int V, bool GATE>
 struct Params {
-  float neg_a[GATE ? V : 1], neg_a2[GATE ? V : 1], bias2[GATE ? V : 1];
+  float neg_a[GATE ? V : 1], bias2[GATE ? V : 1];
   __device__ __forceinline__ void load(const Inputs& in, int c) {
     if constexpr (GATE) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         neg_a[v] = -exp2_fast(in.A_log[c + v] * kLog2e);
-        neg_a2[v] = neg_a[v] * kLog2e;
         bias2[v] = in.dt_bias ? in.dt_bias[c + v] * kLog2e : 0.0f;
       }
     }
   }
-  // g2; e: exp(-|z|), z2: z log2(e) (of the gate, for its slope)
-  __device__ __forceinline__ float log2_decay(float r, int v, float& z2, float& e) const {
-    if constexpr (GATE) {
-      z2 = fmaf(r, kLog2e, bias2[v]);
-      e = exp2_fast(-fabsf(z2));
-      return fmaf(neg_a[v], fmaxf(z2, 0.0f), neg_a2[v] * log1p_unit(e));  // (a NaN is in e)
-    }
-    z2 = e = 0.0f;
-    return r > 0.0f ? 0.0f : r * kLog2e;  // NaN stays NaN
-  }
+  // softplus in log2 units is max(z2, 0) + log2(1 + 2^-|z2|), z2 = z log2(e)
   __device__ __forceinline__ float log2_decay(float r, int v) const {
-    float z2, e;
-    return log2_decay(r, v, z2, e);
+    if constexpr (GATE) {
+      const float z2 = fmaf(r, kLog2e, bias2[v]);
+      const float e = exp2_fast(-fabsf(z2));
+      return neg_a[v] * fmaf(e, log2_1p_over(e), fmaxf(z2, 0.0f));  // (a NaN is in e)
+    }
+    return r > 0.0f ? 0.0f : r * kLog2e;  // NaN stays NaN
   }
 };
 

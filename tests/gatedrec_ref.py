@@ -2,12 +2,12 @@
 what fp32 may be off, in u = 2^-24 per rounding.
 
 Gate: z = r + dt_bias (in log2 units: its two terms and the sum are rounded, 3 u of each, at
-most |z| + 2 |dt_bias|) enters exp(-|z|), whose exp2 adds 2 u; log(1 + e) is off by 3 u, its
-products with exp(A_log) (2 u) and the sum by 5 u.  So g is off by
-eg = (12 + 2 |z| + 2 |dt_bias|) u of itself (log-decays: u).  a = exp(g): the exponent's product and the
+most |z| + 2 |dt_bias|) enters exp(-|z|), whose exp2 adds 2 u; log2(1 + e) is off by 6 u, the
+sum and the product with exp(A_log) (3 u) by 5 u.  So g is off by
+eg = (15 + 2 |z| + 2 |dt_bias|) u of itself (log-decays: u).  a = exp(g): the exponent's product and the
 hardware's exp2 make (2 + 3 |g|) u, g's error |g| eg.  m = sqrt(1 - exp(2 g)): 1 - exp(y) off
-by at most 16 u + eg of itself (1 - e beyond |y| = 0.35 magnifies e's error by 0.7/0.3), its
-root by half of that and u.  sigmoid(i): (4 + 3 |i|) u.  So b = m s x: eb = (20 + 3 |i|) u + eg.
+by at most 22 u + 2 eg of itself (beyond |y| = 0.17 it is 1 - a a, where the exp2's 2 u of a
+become 4 u 0.84 / 0.16), its root by half of that and u.  sigmoid(i): (4 + 3 |i|) u.  So b = m s x: eb = (20 + 3 |i|) u + eg (4 u for the products).
 
 h: with H_t = a H_{t-1} + |b_t| (the recurrence of absolute values, which bounds |h|):
 - a token's own b: eb;
@@ -37,7 +37,7 @@ def gate(x, r, i, A_log, dt_bias, normalize):
         f["sz"] = torch.sigmoid(z)
         f["g"] = f["k"] * torch.logaddexp(z, torch.zeros_like(z))
         bias = dt_bias.to(F64).abs() if dt_bias is not None else 0.0
-        f["eg"] = (12 + 2 * torch.nan_to_num(z).abs() + 2 * bias) * U
+        f["eg"] = (15 + 2 * torch.nan_to_num(z).abs() + 2 * bias) * U
         f["z"] = z
     else:
         f["g"] = torch.where(r > 0, torch.zeros_like(r), r)
@@ -46,7 +46,7 @@ def gate(x, r, i, A_log, dt_bias, normalize):
     f["s"] = torch.sigmoid(i.to(F64)) if i is not None else torch.ones_like(r)
     f["es"] = (4 + 3 * i.to(F64).abs().clamp(max=100)) * U if i is not None else torch.zeros_like(r)
     f["m"] = torch.sqrt(-torch.expm1(2 * f["g"])) if normalize else torch.ones_like(r)
-    f["em"] = (10 * U + f["eg"]) if normalize else torch.zeros_like(r)
+    f["em"] = (12 * U + f["eg"]) if normalize else torch.zeros_like(r)
     f["b"] = f["m"] * f["s"] * f["x"]
     f["eb"] = 4 * U + f["es"] + f["em"]
     return f
