@@ -113,9 +113,11 @@ __global__ void __launch_bounds__(64 * Shape<V>::W, Shape<V>::OCC)
     const __amdgpu_buffer_rsrc_t px = rows_from(A.in.x.p, (int64_t)t * sx),
                                  pr = rows_from(A.in.r.p, (int64_t)t * sr),
                                  pi = rows_from(A.in.i.p, (int64_t)t * si),
-                                 // (without dh its loads give 0)
-                                 pd = buffer_over(static_cast<const char*>(A.dh) + (int64_t)t * sd,
-                                                  A.dh ? 0xffffffffu : 0u);
+                                 // (without dh its loads give 0; the select is uniform, which
+                                 // the compiler has to be told or it loops over the lanes)
+                                 pd = buffer_over(
+                                     static_cast<const char*>(A.dh) + (int64_t)t * sd,
+                                     __builtin_amdgcn_readfirstlane(A.dh ? 0xffffffffu : 0u));
 #pragma unroll
     for (int j = 0; j < L; ++j) {
       const uint32_t row = j < most ? j : most;
@@ -146,17 +148,23 @@ __global__ void __launch_bounds__(64 * Shape<V>::W, Shape<V>::OCC)
   // back = sum_t P_t dh_t.  (a is formed again below: 16 registers for two cycles a value.)
   float g[L][V], px[L][V], pi[L][V];
   float sum[V], add[V], back[V], P[V];
-  auto chain = [&](int j, bool first, bool last, bool in) {
+  auto chain = [&](int j, auto borders) {
 #pragma clang fp contract(off)
     float dS[V] = {};
-    if (first) of_sequence(A.S0, j, add);
-    if (last) of_sequence(A.dS, j, dS);
+    bool in = true;
+    if constexpr (borders) {
+      if (bd.first >> j & 1u) of_sequence(A.S0, j, add);
+      if (bd.last >> j & 1u) of_sequence(A.dS, j, dS);
+      in = !(bd.last & ((1u << j) - 1));  // (back: up to the first border)
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const float a = exp2_fast(g[j][v]);
       add[v] = fmaf(a, add[v], px[j][v] * rx[j].get(v));
       P[v] *= a;
-      if (in) back[v] = fmaf(P[v], dh(j, v) + dS[v], back[v]);
+      float d = dh(j, v);
+      if constexpr (borders) d += dS[v];
+      if (in) back[v] = fmaf(P[v], d, back[v]);
     }
   };
 #pragma unroll
@@ -172,7 +180,7 @@ __global__ void __launch_bounds__(64 * Shape<V>::W, Shape<V>::OCC)
         px[j][v] *= __builtin_amdgcn_sqrtf(one_minus_square(g[j][v], exp2_fast(g[j][v])));
       sum[v] += g[j][v];
     }
-    chain(j, false, false, true);
+    chain(j, std::false_type{});
   }
   // What is formed again is formed again: kept from before, it would not fit the registers.
   auto again = [&] {
@@ -190,8 +198,7 @@ __global__ void __launch_bounds__(64 * Shape<V>::W, Shape<V>::OCC)
 #pragma unroll
     for (int v = 0; v < V; ++v) add[v] = back[v] = 0.0f, P[v] = 1.0f;
 #pragma unroll
-    for (int j = 0; j < L; ++j)  // (back: up to the first border)
-      chain(j, bd.first >> j & 1u, bd.last >> j & 1u, !(bd.last & ((1u << j) - 1)));
+    for (int j = 0; j < L; ++j) chain(j, std::true_type{});
   }
   const int order = W - 1 - wave;
   float code[V];
@@ -245,9 +252,11 @@ __global__ void __launch_bounds__(64 * Shape<V>::W, Shape<V>::OCC)
         float u = x, before = h[v];
         if constexpr (GATED) u *= s;
         if constexpr (NORM) {  // u / m = s u / p
-          float slope = __builtin_amdgcn_rcpf(p) * u;
+          // Where m is 0 this part is 0: it is left out, or, with a gate, whose own slope is 0
+          // there, it need only be finite (a g that is no 0 gives an m of 1.5e-19 or more).
+          float slope = __builtin_amdgcn_rcpf(GATE ? fmaxf(p, 1.0e-19f) : p) * u;
           if constexpr (GATED) slope *= s;
-          before = fmaf(-aa, p > 0.0f ? slope : 0.0f, before);
+          before = fmaf(-aa, GATE || p > 0.0f ? slope : 0.0f, before);
         }
         const float q = aa * before;
         h[v] = fmaf(aa, h[v], p * x);
@@ -258,7 +267,8 @@ __global__ void __launch_bounds__(64 * Shape<V>::W, Shape<V>::OCC)
           const float pg = q * fmaxf(gg, -3.0e38f);
           pr[j][v] = q * par.neg_a[v] *
                      __builtin_amdgcn_rcpf(1.0f + exp2_fast(-fmaf(r, kLog2e, par.bias2[v])));
-          const float in = dh(j, v) + dS[v];
+          float in = dh(j, v);
+          if constexpr (borders) in += dS[v];
           if (!borders || t0 + j < live) {
             QA[v] = fmaf(aa, QA[v], pg);
             Qb[v] = fmaf(aa, Qb[v], pr[j][v]);
