@@ -114,8 +114,12 @@ kda_status too_large(const char* fn, int64_t T, int32_t C) {
                                    "launch holds", fn, (long long)T, C);
 }
 
-bool plausible(int64_t T_tot, int32_t C) {
-  return T_tot >= 0 && T_tot <= kMaxRows && C > 0 && C <= kda::gatedrec::kMaxC;
+bool plausible(int64_t T_tot, int32_t C, bool (*fits)(const kda::gatedrec::Batch&)) {
+  if (T_tot < 0 || T_tot > kMaxRows || C <= 0 || C > kda::gatedrec::kMaxC) return false;
+  kda::gatedrec::Batch b;
+  b.T = (int)T_tot;
+  b.C = C;
+  return fits(b);
 }
 
 }  // namespace
@@ -123,11 +127,13 @@ bool plausible(int64_t T_tot, int32_t C) {
 extern "C" {
 
 size_t kda_gatedrec_scan_workspace_bytes(int64_t T_tot, int32_t C) {
-  return plausible(T_tot, C) ? kda::gatedrec::scan_workspace_bytes(T_tot, C) : 0;
+  return plausible(T_tot, C, kda::gatedrec::scan_fits)
+             ? kda::gatedrec::scan_workspace_bytes(T_tot, C)
+             : 0;
 }
 
 size_t kda_gatedrec_starts_bytes(int64_t T_tot, int32_t C) {
-  return plausible(T_tot, C) ? kda::gatedrec::starts_bytes(T_tot, C) : 0;
+  return plausible(T_tot, C, kda::gatedrec::scan_fits) ? kda::gatedrec::starts_bytes(T_tot, C) : 0;
 }
 
 kda_status kda_gatedrec_scan(const void* x, int64_t x_stride, const void* r, int64_t r_stride,
@@ -215,8 +221,9 @@ kda_status kda_gatedrec_scan(const void* x, int64_t x_stride, const void* r, int
 }
 
 size_t kda_gatedrec_scan_backward_workspace_bytes(int64_t T_tot, int32_t C, int32_t has_starts) {
-  return plausible(T_tot, C) ? kda::gatedrec::backward_workspace_bytes(T_tot, C, has_starts != 0)
-                             : 0;
+  return plausible(T_tot, C, kda::gatedrec::backward_fits)
+             ? kda::gatedrec::backward_workspace_bytes(T_tot, C, has_starts != 0)
+             : 0;
 }
 
 kda_status kda_gatedrec_scan_backward(

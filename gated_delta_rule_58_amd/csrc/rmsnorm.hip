@@ -9,6 +9,11 @@
 // next row on its way while this one is worked on).  The backward forms r again from s,
 // which it reads anyway.  The sums that it makes of the rows go to memory once an owner and
 // are added in a fixed order by a second kernel: the same call gives the same bits.
+//
+// bf16: 4,096 rows of 8,192 with the residual to 8 bits 47 us (5.0 TB/s), to bf16 50 us (5.4);
+// the gradients of 4,096 x 96 rows of 128, a weight a head, 65 us (4.7); of 2,048 rows of 5,003
+// (nothing wider than two bytes aligned) with the stream's gradient 30 us (2.7), 4 of them the
+// sums' kernel.
 #include "gatedrec.hpp"
 #include "norm_rows.hpp"
 
@@ -291,6 +296,9 @@ __global__ void __launch_bounds__(1024) partials_kernel(const float* __restrict_
 int64_t forward_owners(int64_t rows, int64_t groups, int L) {
   return norm::owners(rows, groups, 256 * (L <= 512 ? 4096 : 2048) / L);
 }
+// An owner has at least eight rows, for it begins with its weights and ends with its sums, and
+// there are no more than fill the card once.  Twice as many: 2,048 x 5,003 34 us beside 31, 4,096 x
+// 96 rows of 128 66 beside 64, 4,096 x 4,096 40 beside 33.
 int64_t backward_owners(int64_t rows, int64_t groups, int L, int M) {
   const int64_t one_each = 256 * (L < 256 ? 256 / L : 1);  // a workgroup a CU
   int64_t q = 256 * 1024 / (L * M);

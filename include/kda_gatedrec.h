@@ -30,9 +30,8 @@
  * its norm plus its rounding, also for channels that decay by 1e-5 a token (decays near 1
  * are carried as 1 - exp(g)).
  *
- * Sizes: T_tot < 2^31, and the work items of a launch have to hold the call: about 2^29
- * (token, 64 channels) pairs in the gradients, twice that in the scan
- * (KDA_ERR_UNSUPPORTED beyond).
+ * Sizes: T_tot < 2^31, and the work items of a launch have to hold the call: about 2^30
+ * (token, 64 channels) pairs in the scan, 2^28 in the gradients (KDA_ERR_UNSUPPORTED beyond).
  */
 #ifndef KDA_GATEDREC_H_
 #define KDA_GATEDREC_H_

@@ -175,6 +175,9 @@ def test_sizes():
     assert ws(1 << 31, 96) == 0 and ws(300, (1 << 20) + 1) == 0
     assert st(1, 96) == 96 * 4 and st(33, 96) == 2 * 96 * 4 and st(0, 96) == 0
     assert bw(300, 0, 1) == 0 and bw(300, 96, 1) > 0
+    # more than a launch holds: about 2^30 (token, 64 channels) pairs, 2^28 in the gradients
+    assert ws(1 << 20, 1 << 16) == 0 == st(1 << 20, 1 << 16) and ws(1 << 19, 1 << 16) > 0
+    assert bw(1 << 18, 1 << 16, 1) == 0 == bw(1 << 18, 1 << 16, 0) and bw(1 << 17, 1 << 16, 1) > 0
 
 
 # ------------------------------------------------------------------ RMS norm
