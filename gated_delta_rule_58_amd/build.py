@@ -4,6 +4,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -21,23 +23,33 @@ def hipcc() -> str:
     return os.path.join(rocm, "bin", "hipcc")
 
 
-def build_library(verbose: bool = False) -> str:
-    """Compile every HIP source into one shared library; returns its path."""
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [
-        hipcc(), "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-shared",
-        # packed fp32 VALU ops stay off: hipcc otherwise forms them from plain float code
-        "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-        "-munsafe-fp-atomics", "-Wno-unused-command-line-argument",
-        "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-        "-o", tmp,
-    ] + [os.path.join(CSRC, s) for s in SOURCES]
+def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("hipcc failed building libkda.so")
+
+
+def build_library(verbose: bool = False) -> str:
+    """Compile every HIP source, several at a time, into one shared library; returns its path."""
+    tmp = LIB + ".tmp%d" % os.getpid()
+    cc = [hipcc(), "--offload-arch=" + ARCH, "-fPIC"]
+    flags = [
+        "-O3", "-std=c++17",
+        # packed fp32 VALU ops stay off: hipcc otherwise forms them from plain float code
+        "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+        "-munsafe-fp-atomics", "-Wno-unused-command-line-argument",
+        "-I", os.path.join(ROOT, "include"), "-I", CSRC,
+    ]
+    jobs = int(os.environ.get("MAX_JOBS") or min(8, os.cpu_count() or 1))
+    with tempfile.TemporaryDirectory(prefix="build_", dir=HERE) as to:
+        objects = [os.path.join(to, s + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(max(1, jobs)) as pool:
+            list(pool.map(lambda so: _run(cc + flags + ["-c", os.path.join(CSRC, so[0]), "-o", so[1]],
+                                          verbose), zip(SOURCES, objects)))
+        _run(cc + ["-shared", "-o", tmp] + objects, verbose)
     os.replace(tmp, LIB)
     return LIB
 
