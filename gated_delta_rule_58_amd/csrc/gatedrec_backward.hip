@@ -15,10 +15,9 @@
 // a fixed order.
 //
 // What bounds it: the vector unit and the ways of a tile to memory and back, as in the
-// forward, with 1.7 times its traffic.  4,096 x 12,288 bf16: 216 us, 3.3 TB/s of the 704 MB it
-// has to move (135 us at a copy's rate); a SIMD issues some 30 instructions a value for the
-// gate and m, 29 for the products, 6 for the gradients, and as many a tile as 25 a value for
-// borders, sums and the carry.  What is formed twice (a, sigmoid(r)) is cheaper than the
+// forward, with 1.75 times its traffic.  4,096 x 12,288 bf16: 207 us, 3.4 TB/s of the 711 MB it
+// has to move (137 us at a copy's rate).  A value takes 86 instructions: 30 for the gate and m, 29
+// for the products, 6 for the gradients, the rest a tile's borders, sums and carry.  What is formed twice (a, sigmoid(r)) is cheaper than the
 // registers that would keep it: a wave's tokens, their gate's values and the products before
 // the carry take 164 of 168.
 #include <type_traits>

@@ -13,11 +13,12 @@
 // the state restarts there from the sequence's entry state, which is part of b of that
 // token, and is cut off from everything before.
 //
-// What bounds it: the vector unit, which a value takes for some 42 instructions (two or three
-// of them transcendental) and which is busy for 70 % of the time, and a tile's 14 us of ticket
-// (0.7), loads (2.0), gate (4.4), barrier (2.7) and carry (3.7), of which a CU overlaps two
-// tiles.  bf16: 4,096 x 12,288 107 us (3.75 TB/s of what it has to move; a copy reaches 5.2),
-// 32,768 x 4,096 in eight sequences 272 us (3.96), 131,072 x 512 without i 134 us (3.0).
+// What bounds it: the vector unit, which a value with both gates takes for 38 instructions
+// (five of them transcendental), and a tile's 14 us of ticket (0.7 to 1.4), loads (1.9), gate
+// (4.2), barrier (2.5) and carry (4.1), of which a CU overlaps two tiles.  bf16: 4,096 x 12,288
+// 107 us (3.75 TB/s of what it has to move; a copy reaches 5.2), 32,768 x 4,096 in eight
+// sequences 270 us (4.0), 131,072 x 512 without i 134 us (3.0): there 128 tiles of a channel are
+// under way at once and the carry takes 9 us of 14.6, the instructions (18 a value) little.
 #include "gatedrec_device.hpp"
 
 namespace kda {
