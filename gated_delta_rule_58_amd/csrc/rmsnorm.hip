@@ -86,13 +86,28 @@ __device__ __forceinline__ float largest(uint32_t bits) {
   const float m = __uint_as_float(bits);
   return m < kLeastMax ? kLeastMax : m;  // NaN stays NaN
 }
-// x times inv as e4m3, rounded to nearest even; |x| inv is at most 448 (1 + 2^-23).
-__device__ __forceinline__ void store_e4m3(void* p, int64_t i, int n, f32x8 x, float inv) {
+// x / scale as e4m3, rounded to nearest even; |x| / scale is at most 448 (1 + 2^-23).  The
+// quotient, not x (1 / scale), which rounds otherwise and beside the middle of two codes gives
+// another code: t = x (1 / scale) is within 1.5 of its steps of the quotient, and t + (x - t scale)
+// (1 / scale) within 2^-22 of one, rounded once.  fp32's own quotient could differ from that only
+// where it comes so near to half a step beside a middle of two codes, which takes a scale within 8
+// steps of k / 8 of a power of two; those were gone through on the CPU, and none differs.  (Where
+// the largest |y| is below 2^-85 the difference is subnormal, and t + .. within 2^-6 of a step.)
+// 4,096 x 8,192 bf16 with the residual: 42 us as with x (1 / scale), 49 with eight divisions;
+// 393,216 x 128: 32.6, 30.5, 41.8.
+__device__ __forceinline__ void store_e4m3(void* p, int64_t i, int n, f32x8 x, float scale) {
   uint8_t* d = static_cast<uint8_t*>(p) + i;
-  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * inv, x[1] * inv, 0, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2] * inv, x[3] * inv, lo, true);
-  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[4] * inv, x[5] * inv, 0, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[6] * inv, x[7] * inv, hi, true);
+  const float inv = 1.0f / scale;
+  const float s = fminf(scale, 3.4028235e38f);  // (an infinite scale leaves 0 of what is finite)
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float t = x[e] * inv;
+    x[e] = fmaf(fmaf(-t, s, x[e]), inv, t);
+  }
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[4], x[5], 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[6], x[7], hi, true);
   if (n >= 8) {
     *reinterpret_cast<u32x2_a1*>(d) = u32x2_a1{(uint32_t)lo, (uint32_t)hi};
   } else {
@@ -175,19 +190,18 @@ __global__ void __launch_bounds__(threads<L>()) forward_kernel(const Forward f, 
         const uint32_t b = max8(v[m]);
         mx = b > mx ? b : mx;
       }
-      const float top = largest(row_max<L>(mx, s_max));
-      if (l == 0) f.scales[r] = top / kE4m3Max;
-      const float inv = kE4m3Max / top;
+      const float scale = largest(row_max<L>(mx, s_max)) / kE4m3Max;
+      if (l == 0) f.scales[r] = scale;
 #pragma unroll
-      for (int m = 0; m < M; ++m) store_e4m3(f.y, r * d + (m * L + l) * 8, left[m], v[m], inv);
+      for (int m = 0; m < M; ++m) store_e4m3(f.y, r * d + (m * L + l) * 8, left[m], v[m], scale);
     } else {
       constexpr int GL = L < 16 ? L : 16;  // lanes of 128 columns
       const int64_t per_row = (d + kGroup - 1) / kGroup;
 #pragma unroll
       for (int m = 0; m < M; ++m) {
-        const float top = largest(lanes_max<GL>(max8(v[m])));
-        if (l % GL == 0 && left[m] > 0) f.scales[r * per_row + (m * L + l) / 16] = top / kE4m3Max;
-        store_e4m3(f.y, r * d + (m * L + l) * 8, left[m], v[m], kE4m3Max / top);
+        const float scale = largest(lanes_max<GL>(max8(v[m]))) / kE4m3Max;
+        if (l % GL == 0 && left[m] > 0) f.scales[r * per_row + (m * L + l) / 16] = scale;
+        store_e4m3(f.y, r * d + (m * L + l) * 8, left[m], v[m], scale);
       }
     }
   }

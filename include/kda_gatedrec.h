@@ -154,7 +154,8 @@ kda_status kda_rmsnorm(const void* x, kda_dtype x_dt, int64_t x_stride, const vo
  *
  *   scales [rows, ceil(d / 128)] fp32, one for each 128 columns (scale_group 128), or [rows, 1],
  *         one a row (scale_group 0):  scale = max(|y|) / 448 over the columns
- *   y     [rows, d]: y / scale rounded to nearest even, so that y8 * scale is about y
+ *   y     [rows, d]: the quotient y / scale in fp32, rounded to nearest even (a largest |y| below
+ *         2^-85: of that or the fp32 number beside it), so that y8 * scale is about y
  * A largest |y| below 2^-100 counts as 2^-100.  A NaN makes its scale and values NaN.
  */
 kda_status kda_rmsnorm_e4m3(const void* x, kda_dtype x_dt, int64_t x_stride, const void* residual,
