@@ -115,14 +115,15 @@ __device__ __forceinline__ float log2_1p_over(float e) {
   return fmaf(p, e, 1.4426947832107544f);
 }
 // 1 - 2^y for y <= 0, e = 2^y: the difference loses the digits of a small y, so there it is a
-// polynomial (0.3 u).
+// polynomial (0.3 u).  Its sign is clear, for zeros of either sign too (-y p of y = +0 is -0, which
+// decay_code would take for a cut): that is what the sum with +0 is for.
 __device__ __forceinline__ float one_minus_exp2(float y, float e) {
   float p = 0.0011528132017701864f;
   p = fmaf(p, y, 0.009539824910461903f);
   p = fmaf(p, y, 0.055490005761384964f);
   p = fmaf(p, y, 0.24022559821605682f);
   p = fmaf(p, y, 0.6931471824645996f);
-  return y > -0.5f ? -y * p : 1.0f - e;  // NaN stays NaN
+  return y > -0.5f ? fmaf(-y, p, 0.0f) : 1.0f - e;  // NaN stays NaN
 }
 // 1 - 4^g2 for g2 <= 0, a = 2^g2: the same, a degree less up to where a^2, two digits of
 // a off by one, leaves 21 u of the difference.
@@ -164,10 +165,10 @@ struct Params {
 
 // ------------------------------------------------------------ decay factors
 // A stretch's decay 2^s, s the sum of its log2-decays, as one number `code`: beside 1 it is
-// 1 - d with d = 1 - 2^s kept (code = d, sign clear), for 2^s itself would be rounded to
-// 6e-8, which over the stretches of a slow channel adds up to 6e-8 / d of the state.
-// Further away it is 2^s (code = -2^s, sign set), and where that is 0, nothing is left of
-// what comes before, whatever it was.
+// 1 - d with d = 1 - 2^s kept (code = d, sign clear; +0 where the stretch keeps everything), for
+// 2^s itself would be rounded to 6e-8, which over the stretches of a slow channel adds up to
+// 6e-8 / d of the state.  Further away it is 2^s (code = -2^s, sign set), and where that is 0,
+// nothing is left of what comes before, whatever it was.
 constexpr uint32_t kCut = 0x80000000u;
 __device__ __forceinline__ float decay_code(float s) {
   const float e = exp2_fast(s);
