@@ -153,9 +153,10 @@ __global__ void __launch_bounds__(64 * Shape<V>::W, Shape<V>::OCC)
     if (p) load_state<V>(p, (int64_t)A.q.find(t0 + j) * A.C + cc, x, false);
   };
 
-  // First every token's g, p = m s and s, the wave's decay, what it adds to the state, and e
+  // First every token's g, m and s, the wave's decay, what it adds to the state, and e
   // before it from what comes in: with P_t the decay from the wave's first token to t,
   // back = sum_t P_t dh_t.  (a is formed again below: 16 registers for two cycles a value.)
+  // m and s stay apart: m s may be too small for its reciprocal, where s / m is not.
   float g[L][V], px[L][V], pi[L][V];
   float sum[V], add[V], back[V], P[V];
   auto chain = [&](int j, auto borders) {
@@ -170,7 +171,10 @@ __global__ void __launch_bounds__(64 * Shape<V>::W, Shape<V>::OCC)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const float a = exp2_fast(g[j][v]);
-      add[v] = fmaf(a, add[v], px[j][v] * rx[j].get(v));
+      float b = rx[j].get(v);
+      if constexpr (GATED) b *= pi[j][v];
+      if constexpr (NORM) b *= px[j][v];
+      add[v] = fmaf(a, add[v], b);
       P[v] *= a;
       float d = dh(j, v);
       if constexpr (borders) d += dS[v];
@@ -185,9 +189,9 @@ __global__ void __launch_bounds__(64 * Shape<V>::W, Shape<V>::OCC)
     for (int v = 0; v < V; ++v) {
       g[j][v] = par.log2_decay(rr[j].get(v), v);
       px[j][v] = pi[j][v] = 1.0f;
-      if constexpr (GATED) px[j][v] = pi[j][v] = sigmoid_fast(ri[j].get(v));
+      if constexpr (GATED) pi[j][v] = sigmoid_fast(ri[j].get(v));
       if constexpr (NORM)
-        px[j][v] *= __builtin_amdgcn_sqrtf(one_minus_square(g[j][v], exp2_fast(g[j][v])));
+        px[j][v] = __builtin_amdgcn_sqrtf(one_minus_square(g[j][v], exp2_fast(g[j][v])));
       sum[v] += g[j][v];
     }
     chain(j, std::false_type{});
@@ -200,7 +204,13 @@ __global__ void __launch_bounds__(64 * Shape<V>::W, Shape<V>::OCC)
       hold(rr[j].w[0]);
       hold(rd[j].w[0]);
 #pragma unroll
-      for (int v = 0; v < V; ++v) hold(g[j][v]);
+      for (int v = 0; v < V; ++v) {
+        hold(g[j][v]);
+        if constexpr (GATED && NORM) {
+          hold(px[j][v]);
+          hold(pi[j][v]);
+        }
+      }
     }
   };
   if (bd.first | bd.last) {
@@ -234,8 +244,9 @@ __global__ void __launch_bounds__(64 * Shape<V>::W, Shape<V>::OCC)
     }
   }
   // Then everything that R is multiplied with, before R is known: dx = px R, di = pi R,
-  // dr = pr R, with a in the place of g.  The parameters' sums too: R_t is the sum of what comes
-  // in at s >= t (dh_s, or e behind the wave) times the decay between, so with pg = q g
+  // dr = pr R, with p = m s in the place of m and a in that of g.  The parameters' sums too: R_t
+  // is the sum of what comes in at s >= t (dh_s, or e behind the wave) times the decay between, so
+  // with pg = q g
   //   sum_t R_t pg_t = sum_s dh_s Q_s + e Q_L,   Q_s = a_s Q_{s-1} + pg_s
   // which needs no register a token and goes forwards.
   float (&a)[L][V] = g, pr[L][V];
@@ -258,19 +269,19 @@ __global__ void __launch_bounds__(64 * Shape<V>::W, Shape<V>::OCC)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float x = rx[j].get(v), r = rr[j].get(v);
-        const float gg = g[j][v], aa = exp2_fast(gg), s = pi[j][v], p = px[j][v];
-        float u = x, before = h[v];
-        if constexpr (GATED) u *= s;
-        if constexpr (NORM) {  // u / m = s u / p
-          // Where m is 0 this part is 0: it is left out, or, with a gate, whose own slope is 0
-          // there, it need only be finite (a g that is no 0 gives an m of 1.5e-19 or more).
-          float slope = __builtin_amdgcn_rcpf(GATE ? fmaxf(p, 1.0e-19f) : p) * u;
-          if constexpr (GATED) slope *= s;
-          before = fmaf(-aa, GATE || p > 0.0f ? slope : 0.0f, before);
+        const float gg = g[j][v], aa = exp2_fast(gg), m = px[j][v], s = pi[j][v];
+        float u = x, p = m, before = h[v];
+        if constexpr (GATED) {
+          u *= s;
+          p *= s;
         }
+        // where m is 0 this part is 0
+        if constexpr (NORM)
+          before = fmaf(-aa, m > 0.0f ? u * __builtin_amdgcn_rcpf(m) : 0.0f, before);
         const float q = aa * before;
-        h[v] = fmaf(aa, h[v], p * x);
-        pi[j][v] = p * (x - u);  // of x (1 - s)
+        h[v] = fmaf(aa, h[v], m * u);
+        px[j][v] = p;
+        if constexpr (GATED) pi[j][v] = m * u * (1.0f - s);
         a[j][v] = aa;
         if constexpr (GATE) {
           // (where g is -inf the decay is 0, and q with it)

@@ -91,7 +91,8 @@ size_t kda_gatedrec_starts_bytes(int64_t T_tot, int32_t C);
  * dh [T_tot, C] has dtype dh_dt; dh and d_final_state [N, C] fp32 may be NULL (zero).
  * starts: what the scan wrote, or NULL: the states are formed again first (a second walk).
  * The square root's slope has no bound where g is 0: its part of the gradient is taken as 0
- * where m is.  Rows behind the last sequence are left as they were.
+ * where m is, and is sigmoid(i) x / m elsewhere, which has to be within fp32's range (such an m is
+ * 1e-23 or more: for x up to 1e15 it is).  Rows behind the last sequence are left as they were.
  * The sums run in a fixed order: the same call gives the same bits.
  * workspace: kda_gatedrec_scan_backward_workspace_bytes, 16-byte aligned,
  * KDA_ERR_WORKSPACE below it.
