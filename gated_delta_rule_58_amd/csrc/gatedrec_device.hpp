@@ -102,17 +102,19 @@ inline int width(const Inputs& in, int C, const Out* outs, int count) {
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
 
-// log2(1 + e) / e for 0 <= e <= 1, with the product 6 u of itself (u = 2^-24).  A hardware log
-// with its correction for small e (gate_math.hpp) costs half as much again.
+// log2(1 + e) / e for 0 <= e <= 1, with the product 2.5 u of itself (u = 2^-24; 0.5 before its
+// roundings).  A hardware log with its correction for small e (gate_math.hpp) costs half as much
+// again.
 __device__ __forceinline__ float log2_1p_over(float e) {
-  float p = -0.012319324538111687f;
-  p = fmaf(p, e, 0.06360738724470139f);
-  p = fmaf(p, e, -0.1553512066602707f);
-  p = fmaf(p, e, 0.2560092806816101f);
-  p = fmaf(p, e, -0.35339468717575073f);
-  p = fmaf(p, e, 0.48006367683410645f);
-  p = fmaf(p, e, -0.7213100790977478f);
-  return fmaf(p, e, 1.4426947832107544f);
+  float p = 0.007651003077626228f;
+  p = fmaf(p, e, -0.04299952834844589f);
+  p = fmaf(p, e, 0.11361227184534073f);
+  p = fmaf(p, e, -0.19781996309757233f);
+  p = fmaf(p, e, 0.276011198759079f);
+  p = fmaf(p, e, -0.35851892828941345f);
+  p = fmaf(p, e, 0.48071038722991943f);
+  p = fmaf(p, e, -0.7213414311408997f);
+  return fmaf(p, e, 1.4426950216293335f);
 }
 // 1 - 2^y for y <= 0, e = 2^y: the difference loses the digits of a small y, so there it is a
 // polynomial (0.3 u).  Its sign is clear, for zeros of either sign too (-y p of y = +0 is -0, which
@@ -125,14 +127,15 @@ __device__ __forceinline__ float one_minus_exp2(float y, float e) {
   p = fmaf(p, y, 0.6931471824645996f);
   return y > -0.5f ? fmaf(-y, p, 0.0f) : 1.0f - e;  // NaN stays NaN
 }
-// 1 - 4^g2 for g2 <= 0, a = 2^g2: the same, a degree less up to where a^2, two digits of
-// a off by one, leaves 21 u of the difference.
+// 1 - 4^g2 for g2 <= 0, a = 2^g2: the same up to where a^2, two digits of a off by one, leaves
+// 4 u of the difference.
 __device__ __forceinline__ float one_minus_square(float g2, float a) {
-  float p = 0.14359961450099945f;
-  p = fmaf(p, g2, 0.4432348608970642f);
-  p = fmaf(p, g2, 0.9608860015869141f);
-  p = fmaf(p, g2, 1.3862942457199097f);
-  return g2 > -0.125f ? -g2 * p : fmaf(-a, a, 1.0f);
+  float p = 0.0371021144092083f;
+  p = fmaf(p, g2, 0.15275147557258606f);
+  p = fmaf(p, g2, 0.4439404606819153f);
+  p = fmaf(p, g2, 0.9609037637710571f);
+  p = fmaf(p, g2, 1.3862943649291992f);
+  return g2 > -0.25f ? -g2 * p : fmaf(-a, a, 1.0f);
 }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float sigmoid_fast(float x) {
