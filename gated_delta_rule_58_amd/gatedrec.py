@@ -106,8 +106,9 @@ def gatedrec_scan(x: torch.Tensor, r: torch.Tensor, i: Optional[torch.Tensor] = 
                   state_indices: Optional[torch.Tensor] = None,
                   state_dtype: Optional[torch.dtype] = None, num_seqs: int = 1):
     """kda_gatedrec_scan: h_t = exp(g_t) h_{t-1} + m_t sigmoid(i_t) x_t per channel, with
-    g = -exp(A_log) softplus(r + dt_bias) (A_log None: g = min(r, 0)) and
-    m = sqrt(1 - exp(2 g)) if normalize, else 1.
+    g = -exp(A_log) softplus(r + dt_bias) (A_log None: g = r, which must not be above 0; where it
+    is the kernels take 0, and KDA_DEBUG=1 refuses it) and m = sqrt(1 - exp(2 g)) if normalize,
+    else 1.
 
     x, r and i [T, C] (float32 or bfloat16; rows may be strided; i None: no input gate),
     A_log and dt_bias float32 [C].  cu_seqlens int32 [N+1] on the device; None: num_seqs

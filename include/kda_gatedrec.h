@@ -17,7 +17,9 @@
  * Inputs: x, r and i are [T_tot, C] of one dtype; each gives the distance between its tokens
  * in elements (at least C, at most 2^24), so that they may be columns of one fused
  * projection.  i may be NULL: no input gate (sigmoid(i) is 1).  A_log NULL: r holds the
- * log-decays themselves (g = min(r, 0); dt_bias must be NULL).  dt_bias NULL: zeros.
+ * log-decays themselves, at most 0 (dt_bias must be NULL).  The kernels take one above 0 for 0
+ * (g = min(r, 0), without a gradient); KDA_DEBUG=1 refuses it, as it does in every recurrence of
+ * the library.  dt_bias NULL: zeros.
  * Tensors need only their element's alignment; C is 1 to 2^20.  Everything but x, r and i is
  * dense.
  *
