@@ -16,10 +16,10 @@
 //
 // What bounds it: the vector unit and the ways of a tile to memory and back, as in the
 // forward, with 1.75 times its traffic.  4,096 x 12,288 bf16: 207 us, 3.4 TB/s of the 711 MB it
-// has to move (137 us at a copy's rate).  A value takes 86 instructions: 30 for the gate and m, 29
-// for the products, 6 for the gradients, the rest a tile's borders, sums and carry.  What is formed twice (a, sigmoid(r)) is cheaper than the
-// registers that would keep it: a wave's tokens, their gate's values and the products before
-// the carry take 164 of 168.
+// has to move (137 us at a copy's rate).  A value takes 88 instructions: 32 for the gate and m, 29
+// for the products, 6 for the gradients, the rest a tile's borders, sums and carry.  What is
+// formed twice (a, sigmoid(r)) is cheaper than the registers that would keep it: a wave's tokens,
+// their gate's values and the products before the carry take 164 of 168.
 #include <type_traits>
 
 #include "gatedrec_device.hpp"

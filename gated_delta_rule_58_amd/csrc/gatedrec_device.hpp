@@ -88,8 +88,8 @@ inline bool in_pieces_of(int V, const Inputs& in, int C, const Out* outs, int co
   return true;
 }
 // Values a lane takes at once in the scan and its gradients: two of bf16 (4 bytes a lane)
-// where that is aligned, else one.  4,096 x 12,288, scan and training step: 108 and 321 us,
-// one at a time 111 and 386; 8,192 x 4,096 from log-decays 59 and 71.  (fp32 has its 4 bytes
+// where that is aligned, else one.  4,096 x 12,288, scan and training step: 110 and 323 us,
+// one at a time 121 and 404; 8,192 x 4,096 from log-decays 57 and 74.  (fp32 has its 4 bytes
 // with one, and two would take the registers of two workgroups a CU.)
 inline int width(const Inputs& in, int C, const Out* outs, int count) {
   return in.bf16 && in_pieces_of(2, in, C, outs, count) ? 2 : 1;

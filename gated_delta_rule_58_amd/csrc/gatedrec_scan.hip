@@ -13,12 +13,14 @@
 // the state restarts there from the sequence's entry state, which is part of b of that
 // token, and is cut off from everything before.
 //
-// What bounds it: the vector unit, which a value with both gates takes for 38 instructions
+// What bounds it: the vector unit, which a value with both gates takes for 40 instructions
 // (five of them transcendental), and a tile's 14 us of ticket (0.7 to 1.4), loads (1.9), gate
-// (4.2), barrier (2.5) and carry (4.1), of which a CU overlaps two tiles.  bf16: 4,096 x 12,288
-// 107 us (3.75 TB/s of what it has to move; a copy reaches 5.2), 32,768 x 4,096 in eight
-// sequences 270 us (4.0), 131,072 x 512 without i 134 us (3.0): there 128 tiles of a channel are
-// under way at once and the carry takes 9 us of 14.6, the instructions (18 a value) little.
+// (4.2), barrier (2.5) and carry (4.1), of which a CU overlaps two tiles: 120 registers a lane
+// and 73.8 KB of LDS a workgroup (61 of them the look back's) hold no more.  bf16: 4,096 x 12,288
+// 109 us (3.7 TB/s of what it has to move; a copy reaches 5.2), 32,768 x 4,096 in eight
+// sequences 277 us (3.9), 131,072 x 512 without i 136 us (3.0): there 128 tiles of a channel are
+// under way at once and the carry takes 9 us of 14.6, the instructions (18 a value) little.  (Two
+// of the 40 are the gate's last digits: with a degree less in both polynomials 107, 271, 136 us.)
 #include "gatedrec_device.hpp"
 
 namespace kda {

@@ -10,10 +10,12 @@
 // which it reads anyway.  The sums that it makes of the rows go to memory once an owner and
 // are added in a fixed order by a second kernel: the same call gives the same bits.
 //
-// bf16: 4,096 rows of 8,192 with the residual to 8 bits 47 us (5.0 TB/s), to bf16 50 us (5.4);
-// the gradients of 4,096 x 96 rows of 128, a weight a head, 65 us (4.7); of 2,048 rows of 5,003
-// (nothing wider than two bytes aligned) with the stream's gradient 30 us (2.7), 4 of them the
-// sums' kernel.
+// bf16: 4,096 rows of 8,192 with the residual to 8 bits 47 us (5.0 TB/s; a scale a row the same),
+// to bf16 51 us (5.3); the gradients of 4,096 x 96 rows of 128, a weight a head, 65 us (4.6); with
+// the stream's gradient of 4,096 rows of 4,096 31 us (4.4), of 8,192 55 (4.9), of 12,288 88 (4.6);
+// of 2,048 rows of 5,003 (nothing wider than two bytes aligned) 29 us (2.8), 4 of them the sums'
+// kernel.  Above 8,192 columns the gradients' 1,024 lanes have 128 registers and spill 4 to 22 of
+// them (20 to 60 B a lane).
 #include "gatedrec.hpp"
 #include "norm_rows.hpp"
 

@@ -116,7 +116,8 @@ def gatedrec_scan(x: torch.Tensor, r: torch.Tensor, i: Optional[torch.Tensor] = 
     copied or waited for when it is missing.  States are [N, C] float32 or bfloat16, or with
     state_indices (int32 [N] on the device) pools [num_slots, C], in which final_state
     (possibly initial_state itself) is written only when passed.  output_starts: also return
-    the states that gatedrec_scan_backward wants (`starts`: a tensor for them).  workspace:
+    the states that gatedrec_scan_backward wants (`starts`: a tensor for them, float32
+    [ceil(T / 32), C]).  workspace:
     uint8; None allocates what the library asks for.  Rows behind the last sequence
     (cu_seqlens[N] < T, which needs cu_seqlens_host to be missing) stay as they were in
     `out`, and are zeros when out is None.

@@ -23,10 +23,10 @@
  * Tensors need only their element's alignment; C is 1 to 2^20.  Everything but x, r and i is
  * dense.
  *
- * Values: x and the states have to be finite, logits must not be NaN (infinite ones are the
- * gates' limits).  What is not stays in its channel of its sequence: what comes before it,
- * other channels and the sequences around it do not see it.  Rows that belong to no
- * sequence, and sequences that the step skips, may hold anything.
+ * Values: x and the states have to be finite, exp(A_log) a normal fp32 number, logits must not
+ * be NaN (infinite ones are the gates' limits).  What is not stays in its channel of its
+ * sequence: what comes before it, other channels and the sequences around it do not see it.
+ * Rows that belong to no sequence, and sequences that the step skips, may hold anything.
  *
  * Accuracy: sums and states are fp32.  h agrees with the 64-bit recurrence to about 1e-6 of
  * its norm plus its rounding, also for channels that decay by 1e-5 a token (decays near 1
